@@ -9,7 +9,8 @@ fallback.  If ``libqproj.so`` has not been built, the first call into the
 library raises ImportError (build it with ``__graft_entry__.build()`` or
 ``python -m gemv_nvfp4_int8_amd._build``).
 
-The operations and their rounding rules are documented in include/qproj.h.
+The operations and their rounding rules are documented in include/qproj.h and
+(the operators around the projections) include/qproj_layer.h.
 """
 from __future__ import annotations
 
@@ -36,6 +37,10 @@ QP_FP8_BLOCK128 = 1
 QP_FP8_SINGLE_SCALE = 2
 QP_BF16 = 3
 QP_NVFP4 = 4
+
+QP_ACT_FP8_ROW = 0
+QP_ACT_FP8_BLOCK128 = 1
+QP_ACT_INT8_BLOCK32 = 2
 
 QP_TILES_BANDED = 0
 QP_TILES_MFAST = 1
@@ -82,6 +87,8 @@ def lib() -> ctypes.CDLL:
             "fp8_gemv_rowscale": [P, P, P, P, U, U, U, P],
             "fp8_gemv_blockscale": [P, P, P, P, U, U, U, P],
             "w4a16_gemv": [P, P, P, F, P, U, U, U, P],
+            "rmsnorm_residual_quant": [P, P, P, F, I, P, P, P, U, U, P],
+            "silu_mul_quant": [P, I, P, P, U, U, P],
             "qproj_cache_create": [PP],
             "qproj_cache_destroy": [P],
             "qproj_cache_evict": [P, P],
@@ -405,6 +412,49 @@ def w4a16_gemv(x, w_packed, w_e4m3, scale2, out, stream=None):
         _stream(stream)))
 
 
+def _need_act(q, scale, fmt, rows, k):
+    """Check the output pair of an 8-bit activation format (qp_act_format)."""
+    if fmt == QP_ACT_FP8_BLOCK128:
+        _need(q, "q", U8, (rows, k))
+        _need(scale, "scale", F32, (rows, (k + 127) // 128))
+    elif fmt == QP_ACT_FP8_ROW:
+        _need(q, "q", U8, (rows, k))
+        _need(scale, "scale", F32, (rows,) if scale.dim() == 1 else (rows, 1))
+    elif fmt == QP_ACT_INT8_BLOCK32:
+        _need(q, "q", I8, (rows, k))
+        _need(scale, "scale", F32, (rows, k // 32))
+
+
+def rmsnorm_residual_quant(x, residual, weight, eps, fmt, q, scale, residual_out=None,
+                           stream=None):
+    """q, scale = the 8-bit form `fmt` (QP_ACT_*) of the RMS norm of
+    h = bf16(x + residual), which is written to residual_out (it may be
+    residual itself).  residual None: h = x, and no residual_out."""
+    rows, k = x.shape
+    _need(x, "x", BF16, (rows, k))
+    _need(weight, "weight", BF16, (k,))
+    _need_act(q, scale, fmt, rows, k)
+    if residual is not None:
+        _need(residual, "residual", BF16, (rows, k))
+    if residual_out is not None:
+        _need(residual_out, "residual_out", BF16, (rows, k))
+    _check("rmsnorm_residual_quant", lib().rmsnorm_residual_quant(
+        _ptr(x), None if residual is None else _ptr(residual), _ptr(weight), float(eps),
+        int(fmt), _ptr(q), _ptr(scale), None if residual_out is None else _ptr(residual_out),
+        rows, k, _stream(stream)))
+
+
+def silu_mul_quant(gate_up, fmt, q, scale, stream=None):
+    """q, scale = the 8-bit form `fmt` (QP_ACT_*) of silu(gate) * up, where a
+    row of gate_up holds its gate values and then its up values."""
+    rows, k2 = gate_up.shape
+    k = k2 // 2
+    _need(gate_up, "gate_up", BF16, (rows, 2 * k))
+    _need_act(q, scale, fmt, rows, k)
+    _check("silu_mul_quant", lib().silu_mul_quant(
+        _ptr(gate_up), int(fmt), _ptr(q), _ptr(scale), rows, k, _stream(stream)))
+
+
 class DerivedWeights:
     """A derived-weight cache (the library's qp_cache): weights requantised on
     first use and kept, keyed by the source weight's device address
@@ -496,6 +546,7 @@ __all__ = [
     "int8_w4a8_prefill", "int8_gemm_block_partials", "quantize_bf16_nvfp4",
     "w4a4_gemm", "requant_w_blockfp8_rowwise", "quant_rowwise_fp8",
     "fp8_gemm_rowscale", "fp8_rowwise_proj", "fp8_gemv_rowscale",
-    "fp8_gemv_blockscale", "w4a16_gemv", "DerivedWeights",
+    "fp8_gemv_blockscale", "w4a16_gemv", "rmsnorm_residual_quant",
+    "silu_mul_quant", "DerivedWeights",
     "launch_count", "status_string", "abi_version", "lib", "QProjError",
 ]

@@ -7,8 +7,7 @@
 // caller's stream and return; nothing here allocates or synchronises.
 #include <atomic>
 
-#include "qp_launch.hpp"
-#include "../../include/qproj.h"
+#include "capi_check.hpp"
 
 namespace qp {
 static std::atomic<uint64_t> g_launches{0};
@@ -33,30 +32,7 @@ uint32_t cu_count()
 }
 } // namespace qp
 
-namespace {
-
-constexpr uint64_t MAX_ELEMS = (1ull << 31) - 1;   // every tensor < 2^31 elements
-
-inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-inline int check_ptrs(std::initializer_list<const void *> ps)
-{
-    for (const void *p : ps)
-        if (!p)
-            return QP_ERR_NULL;
-    for (const void *p : ps)
-        if (!aligned16(p))
-            return QP_ERR_ALIGN;
-    return QP_OK;
-}
-
-inline bool fits(uint64_t rows, uint64_t cols) { return rows * cols <= MAX_ELEMS; }
-
-inline int done(hipError_t e) { return e == hipSuccess ? QP_OK : QP_ERR_HIP; }
-
-inline hipStream_t S(void *s) { return reinterpret_cast<hipStream_t>(s); }
-
-} // namespace
+using namespace qp::capi;
 
 extern "C" {
 
@@ -70,7 +46,7 @@ const char *qproj_status_string(int status)
     case QP_OK: return "ok";
     case QP_ERR_NULL: return "a required pointer is NULL";
     case QP_ERR_SHAPE: return "a size is zero, too large, or not a required multiple";
-    case QP_ERR_RANGE: return "GEMV row count M outside the entry point's range";
+    case QP_ERR_RANGE: return "GEMV row count M, or another value, outside the entry point's range";
     case QP_ERR_FORMAT: return "unsupported weight format tag";
     case QP_ERR_HIP: return "the HIP runtime rejected a kernel launch";
     case QP_ERR_ALIGN: return "a pointer is not 16-byte aligned";

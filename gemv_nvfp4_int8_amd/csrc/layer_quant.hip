@@ -1,0 +1,421 @@
+// layer_quant.hip -- the two operators that feed a quantized product:
+// residual addition + RMS norm, and the gated activation silu(g) * u, each
+// with an 8-bit output (E4M3 per row or per 128, int8 per 32) in the same pass.
+//
+// Both stream HBM (7 and 5 bytes per element), so every input byte is read
+// once: a row's values stay in registers between its reductions and the
+// encode.  A thread owns 16-byte chunks of 8 elements, neighbouring lanes
+// neighbouring chunks, so a 128-block is one DPP row of 16 lanes and a
+// 32-block one quad; block maxima never leave the registers.
+#include <type_traits>
+
+#include "qp_device.hpp"
+#include "qp_launch.hpp"
+
+namespace qp {
+namespace {
+
+enum { FMT_ROW = 0, FMT_BLOCK128 = 1, FMT_INT8 = 2 };
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_mov(float v)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+
+// DPP controls whose four applications, one after another, pair every lane of
+// a row of 16 with all others: swap in pairs, swap pairs in quads, mirror in
+// halves of 8, mirror in 16.
+constexpr int DPP_X1 = 0xB1, DPP_X2 = 0x4E, DPP_HALF_MIRROR = 0x141, DPP_MIRROR = 0x140;
+
+__device__ __forceinline__ float max4(float v)
+{
+    v = __builtin_fmaxf(v, dpp_mov<DPP_X1>(v));
+    return __builtin_fmaxf(v, dpp_mov<DPP_X2>(v));
+}
+__device__ __forceinline__ float max16(float v)
+{
+    v = max4(v);
+    v = __builtin_fmaxf(v, dpp_mov<DPP_HALF_MIRROR>(v));
+    return __builtin_fmaxf(v, dpp_mov<DPP_MIRROR>(v));
+}
+__device__ __forceinline__ float sum16(float v)
+{
+    v += dpp_mov<DPP_X1>(v);
+    v += dpp_mov<DPP_X2>(v);
+    v += dpp_mov<DPP_HALF_MIRROR>(v);
+    return v + dpp_mov<DPP_MIRROR>(v);
+}
+__device__ __forceinline__ float sum64(float v)
+{
+    v = sum16(v);
+    v += __shfl_xor(v, 16, WAVE);
+    return v + __shfl_xor(v, 32, WAVE);
+}
+__device__ __forceinline__ float max64(float v)
+{
+    v = max16(v);
+    v = __builtin_fmaxf(v, __shfl_xor(v, 16, WAVE));
+    return __builtin_fmaxf(v, __shfl_xor(v, 32, WAVE));
+}
+
+__device__ __forceinline__ void unpack8(u32x4 r, float *v)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(r[i]);
+        v[2 * i + 1] = bf16_hi(r[i]);
+    }
+}
+
+__device__ __forceinline__ float amax8(const float *y)
+{
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m = __builtin_fmaxf(m, __builtin_fabsf(y[i]));
+    return m;
+}
+
+// bf16(x + r), element by element.
+__device__ __forceinline__ u32x4 add_bf16(u32x4 x, u32x4 r)
+{
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        o[i] = pk_bf16(bf16_lo(x[i]) + bf16_lo(r[i]), bf16_hi(x[i]) + bf16_hi(r[i]));
+    return o;
+}
+
+// Sum of squares of a chunk, in element order.
+__device__ __forceinline__ float ssq8(u32x4 h)
+{
+    float v[8], s = 0.0f;
+    unpack8(h, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        s = __builtin_fmaf(v[i], v[i], s);
+    return s;
+}
+
+__device__ __forceinline__ void norm8(u32x4 h, u32x4 w, float rstd, float *y)
+{
+    float a[8], b[8];
+    unpack8(h, a);
+    unpack8(w, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        y[i] = a[i] * rstd * b[i];
+}
+
+// silu(g) * u with the hardware's exp2 and reciprocal (1 ulp each).  The
+// argument's rounding costs |g| * 2^-24 relative on exp(-g): at most 2e-7 of
+// y where exp(-g) <= 1 counts, and only for negative g, whose y is small,
+// more.  exp(-g) = inf gives -0, the limit.
+__device__ __forceinline__ void silu8(u32x4 g, u32x4 u, float *y)
+{
+    float a[8], b[8];
+    unpack8(g, a);
+    unpack8(u, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float e = __builtin_amdgcn_exp2f(a[i] * -0x1.715476p+0f);
+        y[i] = a[i] * __builtin_amdgcn_rcpf(1.0f + e) * b[i];
+    }
+}
+
+template <int FMT>
+__device__ __forceinline__ float scale_of(float amax)
+{
+    return div_by_const<FMT == FMT_INT8 ? 127 : 448>(amax);
+}
+
+// Eight codes of y under scale sc (0: all +0).  |y| <= amax, so a quotient
+// passes the top code by a few ulp at most, unless the scale is subnormal:
+// then it is saturated first.
+template <int FMT>
+__device__ __forceinline__ u32x2 encode8(const float *y, float sc)
+{
+    const ScaleDiv d(sc);
+    float t[8];
+    u32x2 o;
+    if (__all(d.fast || sc == 0.0f)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            t[i] = d.quick(y[i]);
+        if (FMT == FMT_INT8)
+            o = (u32x2){pack_i8x4(&t[0]), pack_i8x4(&t[4])};
+        else
+            o = (u32x2){cvt_e4m3x4_nosat(t[0], t[1], t[2], t[3]),
+                        cvt_e4m3x4_nosat(t[4], t[5], t[6], t[7])};
+    } else {
+        constexpr float TOP = FMT == FMT_INT8 ? 127.0f : 448.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            t[i] = __builtin_amdgcn_fmed3f(d(y[i]), -TOP, TOP);
+        if (FMT == FMT_INT8)
+            o = (u32x2){pack_i8x4(&t[0]), pack_i8x4(&t[4])};
+        else
+            o = (u32x2){cvt_e4m3x4(t[0], t[1], t[2], t[3]), cvt_e4m3x4(t[4], t[5], t[6], t[7])};
+    }
+    return sc == 0.0f ? (u32x2){0, 0} : o;
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t scales_per_row(uint32_t k)
+{
+    return FMT == FMT_ROW ? 1 : FMT == FMT_BLOCK128 ? (k + 127) / 128 : k / 32;
+}
+
+// Quantize and store chunk c of a row: block formats find their own scale,
+// the row format gets it.  Every lane of the wave calls this (DPP).
+template <int FMT>
+__device__ __forceinline__ void emit8(const float *y, float row_scale, uint32_t c, bool live,
+                                      uint8_t *__restrict__ qr, float *__restrict__ sr)
+{
+    float sc = row_scale;
+    if (FMT == FMT_BLOCK128)
+        sc = scale_of<FMT>(max16(amax8(y)));
+    if (FMT == FMT_INT8)
+        sc = scale_of<FMT>(max4(amax8(y)));
+    const u32x2 o = encode8<FMT>(y, sc);
+    if (live) {
+        __builtin_nontemporal_store(o, reinterpret_cast<u32x2 *>(qr + (size_t)c * 8));
+        if (FMT == FMT_BLOCK128 && (c & 15) == 0)
+            sr[c >> 4] = sc;
+        if (FMT == FMT_INT8 && (c & 3) == 0)
+            sr[c >> 2] = sc;
+    }
+}
+
+struct RowArgs {
+    const uint16_t *x;          // norm: x; activation: gate_up
+    const uint16_t *res;        // norm: residual or null
+    const uint16_t *w;          // norm: weight
+    uint16_t *res_out;
+    uint8_t *q;
+    float *s;
+    float eps;
+    uint32_t rows, k;
+};
+
+// 1 / sqrt(mean + eps) from the block sums sm[0 .. nb): lane l adds blocks l,
+// l + 64, ... and one butterfly joins the lanes.  Every kernel below forms
+// the same block sums (16 lanes of one chunk each), so a row's norm does not
+// depend on how many threads share it.
+__device__ __forceinline__ float rstd_of(const float *sm, uint32_t nb, uint32_t k, float eps)
+{
+    float v = 0.0f;
+    for (uint32_t i = threadIdx.x & 63; i < nb; i += 64)
+        v += sm[i];
+    return 1.0f / __builtin_sqrtf(sum64(v) / (float)k + eps);
+}
+
+// TPR threads per row (64: one wave, four rows per workgroup), CPL chunks per
+// thread, the row held in registers.
+template <bool NORM, int FMT, int TPR, int CPL>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_row_quant(RowArgs A)
+{
+    constexpr int RPG = TPR == 64 ? 4 : 1, NB = TPR * CPL / 16;
+    __shared__ float sums[RPG][NB];
+    __shared__ float tops[TPR / 64];
+    const int sub = RPG == 1 ? 0 : threadIdx.x >> 6;
+    const uint32_t row = blockIdx.x * RPG + sub;
+    if (RPG > 1 && row >= A.rows)
+        return;                          // the whole wave; waves share nothing
+    const uint32_t t = threadIdx.x & (TPR - 1), nch = A.k / 8;
+    const size_t at = (size_t)row * A.k;
+    float y[CPL][8];
+    if (NORM) {
+        u32x4 h[CPL], r[CPL];
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+            const uint32_t c = t + TPR * j;
+            h[j] = r[j] = (u32x4){0, 0, 0, 0};
+            if (c < nch) {
+                h[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(A.x + at + 8 * (size_t)c));
+                if (A.res)
+                    r[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(A.res + at + 8 * (size_t)c));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+            const uint32_t c = t + TPR * j;
+            if (A.res) {
+                h[j] = add_bf16(h[j], r[j]);
+                if (c < nch)
+                    *reinterpret_cast<u32x4 *>(A.res_out + at + 8 * (size_t)c) = h[j];
+            }
+            const float s = sum16(ssq8(h[j]));
+            if ((t & 15) == 0)
+                sums[sub][c >> 4] = s;   // c / 16 < NB; past the row: 0
+        }
+        if (TPR > 64)
+            __syncthreads();
+        else
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        const float rstd = rstd_of(sums[sub], NB, A.k, A.eps);
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+            const uint32_t c = t + TPR * j;
+            u32x4 w = (u32x4){0, 0, 0, 0};
+            if (c < nch)
+                w = *reinterpret_cast<const u32x4 *>(A.w + 8 * (size_t)c);
+            norm8(h[j], w, rstd, y[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+            const uint32_t c = t + TPR * j;
+            u32x4 g = (u32x4){0, 0, 0, 0}, u = g;
+            if (c < nch) {
+                g = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(A.x + 2 * at + 8 * (size_t)c));
+                u = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(A.x + 2 * at + A.k + 8 * (size_t)c));
+            }
+            silu8(g, u, y[j]);
+        }
+    }
+    float sc = 0.0f;
+    if (FMT == FMT_ROW) {
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < CPL; ++j)
+            m = __builtin_fmaxf(m, amax8(y[j]));
+        m = max64(m);
+        if (TPR > 64) {
+            if ((threadIdx.x & 63) == 0)
+                tops[threadIdx.x >> 6] = m;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < TPR / 64; ++i)
+                m = __builtin_fmaxf(m, tops[i]);
+        }
+        sc = scale_of<FMT>(m);
+        if (t == 0)
+            A.s[row] = sc;
+    }
+    float *sr = A.s + (size_t)row * scales_per_row<FMT>(A.k);
+#pragma unroll
+    for (int j = 0; j < CPL; ++j) {
+        const uint32_t c = t + TPR * j;
+        emit8<FMT>(y[j], sc, c, c < nch, A.q + at, sr);
+    }
+}
+
+// Rows longer than the registers hold: 1024 threads walk the row once per
+// step (sum, for the row format the maximum, encode) and recompute y.  With a
+// residual, h is read back from residual_out: each thread reads only what it
+// wrote itself.
+template <bool NORM, int FMT>
+__global__ __launch_bounds__(1024) void k_row_quant_long(RowArgs A)
+{
+    __shared__ float sums[(1u << 18) / 128];
+    __shared__ float tops[16];
+    const uint32_t row = blockIdx.x, t = threadIdx.x, nch = A.k / 8, nb = (nch + 15) / 16;
+    const uint32_t steps = (nch + 1023) / 1024;
+    const size_t at = (size_t)row * A.k;
+    const uint16_t *h_src = NORM && A.res ? A.res_out : A.x;
+    float rstd = 0.0f;
+    if (NORM) {
+        for (uint32_t i = 0; i < steps; ++i) {
+            const uint32_t c = t + 1024 * i;
+            u32x4 h = (u32x4){0, 0, 0, 0};
+            if (c < nch) {
+                h = *reinterpret_cast<const u32x4 *>(A.x + at + 8 * (size_t)c);
+                if (A.res) {
+                    h = add_bf16(h, *reinterpret_cast<const u32x4 *>(A.res + at + 8 * (size_t)c));
+                    *reinterpret_cast<u32x4 *>(A.res_out + at + 8 * (size_t)c) = h;
+                }
+            }
+            const float s = sum16(ssq8(h));
+            if ((t & 15) == 0 && c / 16 < nb)
+                sums[c >> 4] = s;
+        }
+        __syncthreads();
+        rstd = rstd_of(sums, nb, A.k, A.eps);
+    }
+    auto value = [&](uint32_t c, float *y) {
+        const u32x4 z = (u32x4){0, 0, 0, 0};
+        if (NORM) {
+            const u32x4 h = c < nch ? *reinterpret_cast<const u32x4 *>(h_src + at + 8 * (size_t)c) : z;
+            const u32x4 w = c < nch ? *reinterpret_cast<const u32x4 *>(A.w + 8 * (size_t)c) : z;
+            norm8(h, w, rstd, y);
+        } else {
+            const uint16_t *p = A.x + 2 * at + 8 * (size_t)c;
+            const u32x4 g = c < nch ? *reinterpret_cast<const u32x4 *>(p) : z;
+            const u32x4 u = c < nch ? *reinterpret_cast<const u32x4 *>(p + A.k) : z;
+            silu8(g, u, y);
+        }
+    };
+    float y[8], sc = 0.0f;
+    if (FMT == FMT_ROW) {
+        float m = 0.0f;
+        for (uint32_t i = 0; i < steps; ++i) {
+            value(t + 1024 * i, y);
+            m = __builtin_fmaxf(m, amax8(y));
+        }
+        m = max64(m);
+        if ((t & 63) == 0)
+            tops[t >> 6] = m;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            m = __builtin_fmaxf(m, tops[i]);
+        sc = scale_of<FMT>(m);
+        if (t == 0)
+            A.s[row] = sc;
+    }
+    float *sr = A.s + (size_t)row * scales_per_row<FMT>(A.k);
+    for (uint32_t i = 0; i < steps; ++i) {
+        const uint32_t c = t + 1024 * i;
+        value(c, y);
+        emit8<FMT>(y, sc, c, c < nch, A.q + at, sr);
+    }
+}
+
+template <bool NORM, int FMT, int TPR, int CPL>
+void launch_row(const RowArgs &A, hipStream_t st)
+{
+    constexpr int RPG = TPR == 64 ? 4 : 1;
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_row_quant<NORM, FMT, TPR, CPL>), dim3((A.rows + RPG - 1) / RPG),
+                       dim3(TPR < 256 ? 256 : TPR), 0, st, A);
+}
+
+template <bool NORM, int FMT>
+hipError_t launch_fmt(const RowArgs &A, hipStream_t st)
+{
+    const uint32_t nch = A.k / 8;
+    if (nch <= 256 * 2)
+        launch_row<NORM, FMT, 256, 2>(A, st);
+    else if (nch <= 256 * 8)
+        launch_row<NORM, FMT, 256, 8>(A, st);
+    else
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_row_quant_long<NORM, FMT>), dim3(A.rows), dim3(1024), 0, st, A);
+    count_launch();
+    return hipGetLastError();
+}
+
+template <bool NORM>
+hipError_t launch_any(const RowArgs &A, int fmt, hipStream_t st)
+{
+    return fmt == FMT_ROW        ? launch_fmt<NORM, FMT_ROW>(A, st)
+           : fmt == FMT_BLOCK128 ? launch_fmt<NORM, FMT_BLOCK128>(A, st)
+                                 : launch_fmt<NORM, FMT_INT8>(A, st);
+}
+
+} // namespace
+
+hipError_t launch_rmsnorm_residual_quant(const uint16_t *x, const uint16_t *res, const uint16_t *w,
+                                         float eps, int fmt, void *q, float *s, uint16_t *res_out,
+                                         uint32_t rows, uint32_t k, hipStream_t st)
+{
+    return launch_any<true>({x, res, w, res_out, (uint8_t *)q, s, eps, rows, k}, fmt, st);
+}
+
+hipError_t launch_silu_mul_quant(const uint16_t *gate_up, int fmt, void *q, float *s, uint32_t rows,
+                                 uint32_t k, hipStream_t st)
+{
+    return launch_any<false>({gate_up, nullptr, nullptr, nullptr, (uint8_t *)q, s, 0.0f, rows, k}, fmt, st);
+}
+
+} // namespace qp

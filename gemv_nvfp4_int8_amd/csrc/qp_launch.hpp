@@ -48,6 +48,15 @@ hipError_t launch_w4a4_gemm(const uint8_t *ap, const uint8_t *asc,
                             float sa2, float sw2, uint32_t m, uint32_t n,
                             uint32_t k, uint32_t order, hipStream_t st);
 
+// fmt: an enum qp_act_format value.  res and res_out are both null or both set
+// (and may be the same buffer).
+hipError_t launch_rmsnorm_residual_quant(const uint16_t *x, const uint16_t *res,
+                                         const uint16_t *w, float eps, int fmt, void *q,
+                                         float *s, uint16_t *res_out, uint32_t rows,
+                                         uint32_t k, hipStream_t st);
+hipError_t launch_silu_mul_quant(const uint16_t *gate_up, int fmt, void *q, float *s,
+                                 uint32_t rows, uint32_t k, hipStream_t st);
+
 // Counts kernel launches enqueued by the library (all launchers add to it).
 void count_launch(uint32_t n = 1);
 

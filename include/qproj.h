@@ -43,7 +43,7 @@ extern "C" {
 #define QP_OK 0
 #define QP_ERR_NULL (-1)   /* a required pointer is NULL                   */
 #define QP_ERR_SHAPE (-2)  /* a size is 0, too large, or breaks a multiple */
-#define QP_ERR_RANGE (-3)  /* GEMV M outside its range (1..16, or 1..8)     */
+#define QP_ERR_RANGE (-3)  /* GEMV M (1..16, or 1..8) or a value out of range */
 #define QP_ERR_FORMAT (-4) /* unsupported weight format tag                 */
 #define QP_ERR_HIP (-5)    /* the HIP runtime rejected a launch             */
 #define QP_ERR_ALIGN (-6)  /* a pointer is not 16-byte aligned              */
