@@ -89,6 +89,8 @@ def lib() -> ctypes.CDLL:
             "w4a16_gemv": [P, P, P, F, P, U, U, U, P],
             "rmsnorm_residual_quant": [P, P, P, F, I, P, P, P, U, U, P],
             "silu_mul_quant": [P, I, P, P, U, U, P],
+            "fp8_gemm_blockscale": [P, P, P, P, P, U, U, U, P],
+            "moe_fp8_blockscale": [P, P, P, P, P, P, P, ctypes.c_uint64, P, U, U, U, U, U, I, P],
             "qproj_cache_create": [PP],
             "qproj_cache_destroy": [P],
             "qproj_cache_evict": [P, P],
@@ -108,6 +110,8 @@ def lib() -> ctypes.CDLL:
         L.qproj_status_string.argtypes = [ctypes.c_int]
         L.qproj_noalloc_scratch_bytes.restype = ctypes.c_uint64
         L.qproj_noalloc_scratch_bytes.argtypes = []
+        L.moe_fp8_blockscale_workspace.restype = ctypes.c_uint64
+        L.moe_fp8_blockscale_workspace.argtypes = [U, U, U]
         L.qproj_abi_version.restype = ctypes.c_int
         L.qproj_abi_version.argtypes = []
         _lib = L
@@ -455,6 +459,49 @@ def silu_mul_quant(gate_up, fmt, q, scale, stream=None):
         _ptr(gate_up), int(fmt), _ptr(q), _ptr(scale), rows, k, _stream(stream)))
 
 
+def fp8_gemm_blockscale(a, a_scale, w, block_scale, out, stream=None):
+    """Block-scaled FP8 GEMM: a with one scale per 128 of a row
+    (QP_ACT_FP8_BLOCK128), w with one per 128 x 128 block."""
+    m, k = a.shape
+    n = w.shape[0]
+    kb = (k + 127) // 128
+    _need(a, "a", U8, (m, k))
+    _need(a_scale, "a_scale", F32, (m, kb))
+    _need(w, "w", U8, (n, k))
+    _need(block_scale, "block_scale", F32, ((n + 127) // 128, kb))
+    _need(out, "out", BF16, (m, n))
+    _check("fp8_gemm_blockscale", lib().fp8_gemm_blockscale(
+        _ptr(a), _ptr(a_scale), _ptr(w), _ptr(block_scale), _ptr(out), m, n, k,
+        _stream(stream)))
+
+
+def moe_fp8_blockscale_workspace(t, topk, i) -> int:
+    """Bytes of scratch moe_fp8_blockscale needs for t tokens, topk experts a
+    token and an intermediate size i."""
+    return int(lib().moe_fp8_blockscale_workspace(t, topk, i))
+
+
+def moe_fp8_blockscale(x, router_logits, w13, s13, w2, s2, topk, renormalize, workspace, out,
+                       stream=None):
+    """A mixture-of-experts layer for up to 16 tokens: routing, gate and up
+    products, activation, down product and the weighted sum."""
+    t, h = x.shape
+    e, i2, _ = w13.shape
+    i = i2 // 2
+    _need(x, "x", BF16, (t, h))
+    _need(router_logits, "router_logits", F32, (t, e))
+    _need(w13, "w13", U8, (e, 2 * i, h))
+    _need(s13, "s13", F32, (e, 2 * i // 128, h // 128))
+    _need(w2, "w2", U8, (e, h, i))
+    _need(s2, "s2", F32, (e, h // 128, i // 128))
+    _need(out, "out", BF16, (t, h))
+    _need(workspace, "workspace", (torch.uint8,), (workspace.numel(),))
+    _check("moe_fp8_blockscale", lib().moe_fp8_blockscale(
+        _ptr(x), _ptr(router_logits), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2),
+        _ptr(workspace), workspace.numel(), _ptr(out), t, e, int(topk), h, i, int(renormalize),
+        _stream(stream)))
+
+
 class DerivedWeights:
     """A derived-weight cache (the library's qp_cache): weights requantised on
     first use and kept, keyed by the source weight's device address
@@ -547,6 +594,7 @@ __all__ = [
     "w4a4_gemm", "requant_w_blockfp8_rowwise", "quant_rowwise_fp8",
     "fp8_gemm_rowscale", "fp8_rowwise_proj", "fp8_gemv_rowscale",
     "fp8_gemv_blockscale", "w4a16_gemv", "rmsnorm_residual_quant",
-    "silu_mul_quant", "DerivedWeights",
+    "silu_mul_quant", "fp8_gemm_blockscale", "moe_fp8_blockscale",
+    "moe_fp8_blockscale_workspace", "DerivedWeights",
     "launch_count", "status_string", "abi_version", "lib", "QProjError",
 ]

@@ -54,4 +54,38 @@ int silu_mul_quant(const uint16_t *gate_up, int fmt, void *q, float *scale, uint
     return done(qp::launch_silu_mul_quant(gate_up, fmt, q, scale, rows, k, S(stream)));
 }
 
+int fp8_gemm_blockscale(const uint8_t *a, const float *a_scale, const uint8_t *w,
+                        const float *block_scale, uint16_t *out, uint32_t m, uint32_t n,
+                        uint32_t k, void *stream)
+{
+    if (int e = check_ptrs({a, a_scale, w, block_scale, out}))
+        return e;
+    if (m == 0 || n == 0 || k == 0 || k % 16 != 0 || !fits(m, k) || !fits(n, k) || !fits(m, n))
+        return QP_ERR_SHAPE;
+    return done(qp::launch_fp8_gemm_blockscale(a, a_scale, w, block_scale, out, m, n, k, S(stream)));
+}
+
+uint64_t moe_fp8_blockscale_workspace(uint32_t t, uint32_t topk, uint32_t i)
+{
+    return qp::moe_fp8_workspace(t, topk, i);
+}
+
+int moe_fp8_blockscale(const uint16_t *x, const float *router_logits, const uint8_t *w13,
+                       const float *s13, const uint8_t *w2, const float *s2, void *workspace,
+                       uint64_t workspace_bytes, uint16_t *out, uint32_t t, uint32_t e,
+                       uint32_t topk, uint32_t h, uint32_t i, int renormalize, void *stream)
+{
+    if (int err = check_ptrs({x, router_logits, w13, s13, w2, s2, workspace, out}))
+        return err;
+    if (t < 1 || t > QP_MOE_MAX_T || topk < 1 || topk > QP_MOE_MAX_TOPK || topk > e)
+        return QP_ERR_RANGE;
+    if (e > QP_MOE_MAX_E || h == 0 || i == 0 || h % 128 != 0 || i % 128 != 0 ||
+        !fits(2 * (uint64_t)i, h) || !fits(2 * (uint64_t)t, h) || !fits(2 * (uint64_t)t * topk, i))
+        return QP_ERR_SHAPE;
+    if (workspace_bytes < qp::moe_fp8_workspace(t, topk, i))
+        return QP_ERR_SCRATCH;
+    return done(qp::launch_moe_fp8(x, router_logits, w13, s13, w2, s2, workspace, out, t, e, topk, h,
+                                   i, renormalize != 0, S(stream)));
+}
+
 } // extern "C"

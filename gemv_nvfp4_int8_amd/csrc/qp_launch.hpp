@@ -57,6 +57,16 @@ hipError_t launch_rmsnorm_residual_quant(const uint16_t *x, const uint16_t *res,
 hipError_t launch_silu_mul_quant(const uint16_t *gate_up, int fmt, void *q, float *s,
                                  uint32_t rows, uint32_t k, hipStream_t st);
 
+hipError_t launch_fp8_gemm_blockscale(const uint8_t *a, const float *as, const uint8_t *w,
+                                      const float *ws, uint16_t *out, uint32_t m, uint32_t n,
+                                      uint32_t k, hipStream_t st);
+// work: moe_fp8_workspace() bytes, 16-byte aligned.
+uint64_t moe_fp8_workspace(uint32_t T, uint32_t topk, uint32_t I);
+hipError_t launch_moe_fp8(const uint16_t *x, const float *logits, const uint8_t *w13,
+                          const float *s13, const uint8_t *w2, const float *s2, void *work,
+                          uint16_t *out, uint32_t T, uint32_t E, uint32_t topk, uint32_t H,
+                          uint32_t I, bool renorm, hipStream_t st);
+
 // Counts kernel launches enqueued by the library (all launchers add to it).
 void count_launch(uint32_t n = 1);
 

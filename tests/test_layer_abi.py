@@ -25,6 +25,11 @@ CALLS = {
     "rmsnorm_residual_quant": (lambda p, n: L.rmsnorm_residual_quant(
         p[0], p[1], p[2], 1e-6, BLOCK, p[3], p[4], p[5], n[0], n[1], None), 6, (4, 256)),
     "silu_mul_quant": (lambda p, n: L.silu_mul_quant(p[0], BLOCK, p[1], p[2], n[0], n[1], None), 3, (4, 256)),
+    "fp8_gemm_blockscale": (lambda p, n: L.fp8_gemm_blockscale(
+        p[0], p[1], p[2], p[3], p[4], n[0], n[1], n[2], None), 5, (4, 256, 256)),
+    "moe_fp8_blockscale": (lambda p, n: L.moe_fp8_blockscale(
+        p[0], p[1], p[2], p[3], p[4], p[5], p[6], 1 << 20, p[7], n[0], n[1], n[2], n[3], n[4], 1, None),
+        8, (4, 16, 2, 256, 256)),
 }
 
 
@@ -88,6 +93,30 @@ def test_silu_refusals():
     for fmt, k in ((BLOCK, 24), (ROW, 8), (INT8, 48), (ROW, (1 << 18) + 16)):
         assert call(fmt, 4, k) == qp.QP_ERR_SHAPE
     assert call(BLOCK, 1 << 20, 1 << 10) == qp.QP_ERR_SHAPE        # gate_up holds 2^31 elements
+
+
+def test_gemm_refusals():
+    call = lambda m, n, k: L.fp8_gemm_blockscale(A, B, A, B, A, m, n, k, None)  # noqa: E731
+    for k in (8, 24, 100):
+        assert call(4, 256, k) == qp.QP_ERR_SHAPE
+    assert call(1 << 16, 128, 1 << 15) == qp.QP_ERR_SHAPE          # a holds 2^31 elements
+    assert call(128, 1 << 16, 1 << 15) == qp.QP_ERR_SHAPE
+    assert call(1 << 16, 1 << 15, 128) == qp.QP_ERR_SHAPE
+
+
+def _moe(t=4, e=16, topk=2, h=256, i=256, work=1 << 20):
+    return L.moe_fp8_blockscale(A, B, A, B, A, B, A, work, B, t, e, topk, h, i, 1, None)
+
+
+def test_moe_refusals():
+    for bad in (dict(t=17), dict(topk=17), dict(e=4, topk=5), dict(t=1 << 20)):
+        assert _moe(**bad) == qp.QP_ERR_RANGE, bad
+    for bad in (dict(e=513), dict(h=192), dict(i=64), dict(h=1 << 16, i=1 << 14)):
+        assert _moe(**bad) == qp.QP_ERR_SHAPE, bad
+    need = qp.moe_fp8_blockscale_workspace(4, 2, 256)
+    assert 4 * 4 * 2 * 256 < need <= 4 * 4 * 2 * 256 + 65536
+    assert _moe(work=need - 1) == qp.QP_ERR_SCRATCH
+    assert _moe(work=0) == qp.QP_ERR_SCRATCH
 
 
 def test_binding_refuses_what_the_kernels_would_overrun():
