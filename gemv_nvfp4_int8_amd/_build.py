@@ -10,7 +10,8 @@ the source tree.  Flags:
                                          code rounding relies on
   -target-feature -packed-fp32-ops       no packed-FP32 VALU instructions
 Per file (FILE_FLAGS):
-  gemv_w4a16.hip, gemm_int8.hip: -mllvm -amdgpu-mfma-vgpr-form
+  gemv_w4a16.hip, gemm_int8.hip, gemm_fp8_block.hip, moe_fp8.hip:
+                                 -mllvm -amdgpu-mfma-vgpr-form
                                          MFMA results in ordinary VGPRs:
                                          these kernels fold every MFMA result
                                          with VALU FMAs, and the
@@ -44,6 +45,8 @@ DEVICE_FLAGS = [
 FILE_FLAGS = {
     "gemv_w4a16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "gemm_int8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "gemm_fp8_block.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "moe_fp8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

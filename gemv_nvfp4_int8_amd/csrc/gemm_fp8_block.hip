@@ -12,104 +12,572 @@
 // no broadcast.
 #include "gemm_common.hpp"
 #include "qp_launch.hpp"
+#include <type_traits>
 
 namespace qp {
 namespace {
 
-constexpr int FB_T = 128, FB_BK = 128, FB_PITCH = FB_BK + 16;
+// ---------------------------------------------------------------------------
+// Large tiles: MW x NW waves, each 64 rows of A by 16*TJ rows of W, as 4 x TJ
+// MFMAs v_mfma_f32_16x16x128 per K block: one instruction is one whole P_b of
+// a 16 x 16 tile, so P_b costs four registers for a moment and its fold, four
+// FMAs, runs under the next tiles' MFMAs.  The running sums stay in ordinary
+// registers (the vector ALU cannot reach accumulator registers), which caps a
+// wave at 64 x 128; two waves share a SIMD so that one's folds, LDS reads and
+// waits run under the other's MFMAs.
+//
+// Operand panels of one K block (128 bytes per row of A or of W) arrive by
+// 16-byte buffer loads to LDS, swizzled as in gemm_common.hpp, into a ring of
+// five slots: panel i of A0, W0, A1, W1, ... in slot i % 5.  A block's A
+// fragments are all in registers soon after it starts, its W fragments at
+// three quarters of it; each time a barrier says so and the slot is refilled
+// at once, W two blocks ahead and A three, so that a panel has 1.65 to 2
+// blocks' time to come (with one block's time, 475 against 371 us without any
+// loads; 8192 x 12288 x 5120).
+// Rows past M or N lie past the buffer and read as zeros, so tiles at the
+// edges need no clamping; where 128 does not divide K, A's chunks past K are
+// given an offset past the buffer (zero products, whatever W's row goes on
+// with).
+//
+// The scales of five K blocks are loaded at once: lane l holds as * ws of its
+// wave's row l for each; a block's four values per lane (its rows 16t + l%16)
+// come from three lane swaps.
+// ---------------------------------------------------------------------------
+constexpr uint32_t FB_OOB = 0x80000000u;
 
-__device__ __forceinline__ i32x8 frag32(const uint8_t *p)
+// s_waitcnt immediates: vmcnt <= n alone, lgkmcnt == 0 alone
+constexpr int waitcnt_vm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
+constexpr int WAIT_LGKM0 = 15 | (7 << 4) | (3 << 14);
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t fb_rsrc(const void *p, uint32_t bytes)
 {
-    const i32x4 a = *reinterpret_cast<const i32x4 *>(p);
-    const i32x4 b = *reinterpret_cast<const i32x4 *>(p + 16);
-    return (i32x8){a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, 0x00020000);
 }
 
-// 128 x 128 tiles, any shape: operand stages of one K block go through
-// registers (zeros past the edges) into two LDS buffers.
-__global__ __launch_bounds__(256) void k_fp8_gemm_block(
+// v's four rows of 16 lanes, each spread over all four.
+__device__ __forceinline__ void spread_rows(float v, float *s)
+{
+    const uint32_t u = __float_as_uint(v);
+    const auto h = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const auto a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+    s[0] = __uint_as_float(a[0]);
+    s[1] = __uint_as_float(a[1]);
+    s[2] = __uint_as_float(b[0]);
+    s[3] = __uint_as_float(b[1]);
+}
+
+template <int MW, int NW, int TJ>
+__global__ __launch_bounds__(64 * MW * NW) void k_fp8_gemm_block_tiles(
     const uint8_t *__restrict__ A, const float *__restrict__ as,
     const uint8_t *__restrict__ W, const float *__restrict__ ws,
     uint16_t *__restrict__ out, uint32_t M, uint32_t N, uint32_t K,
-    uint32_t mtiles, uint32_t ntiles)
+    uint32_t mtiles, uint32_t ntiles, uint32_t first, uint32_t quarters, uint32_t vec_ok)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t sA[2][FB_T * FB_PITCH];
-    __shared__ __attribute__((aligned(16))) uint8_t sW[2][FB_T * FB_PITCH];
+    constexpr int NWV = MW * NW, TM = 64 * MW, TN = 16 * TJ * NW;
+    constexpr int AL = TM / 8 / NWV, WL = TN / 8 / NWV;     // DMA loads per wave and stage
+    static_assert(TM / 8 % NWV == 0 && TN / 8 % NWV == 0 && AL % 2 == 0 && WL % 2 == 0, "whole DMA");
+    static_assert(128 % (16 * TJ) == 0 && TN % 128 == 0, "a wave's columns share a scale block");
+    constexpr int SLOT = (TM > TN ? TM : TN) * BIG_KB;
+    // separate variables: see gemm_fp8.hip
+    __shared__ __attribute__((aligned(1024))) uint8_t S0[SLOT];
+    __shared__ __attribute__((aligned(1024))) uint8_t S1[SLOT];
+    __shared__ __attribute__((aligned(1024))) uint8_t S2[SLOT];
+    __shared__ __attribute__((aligned(1024))) uint8_t S3[SLOT];
+    __shared__ __attribute__((aligned(1024))) uint8_t S4[SLOT];
 
-    uint32_t tm, tn;
-    tile_coords(mtiles, ntiles, tm, tn);
-    const uint32_t m0 = tm * FB_T, n0 = tn * FB_T;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = wave & 1, wn = wave >> 1;
-    const uint32_t kb = (K + FB_BK - 1) / FB_BK;
-
-    StageLoader<FB_T, FB_BK> la, lw;
-    f32x16 acc[2][2] = {};
-
-    // this lane's two rows of C and its tile's row of the weight's scale grid
-    uint32_t row[2];
-    const float *asr[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        row[t] = m0 + wm * 64 + 32 * t + (lane & 31);
-        asr[t] = as + (size_t)min(row[t], M - 1) * kb;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % MW, wn = wave / MW;
+    // Tiles first .. of the banded order, or, with `quarters`, four workgroups
+    // to each of them, one for each quarter of a tile twice as long and wide.
+    uint32_t tm, tn, id = xcd_remap(blockIdx.x, gridDim.x);
+    banded_tile(first + (quarters ? id / 4 : id), mtiles, ntiles, tm, tn);
+    if (quarters) {
+        tm = 2 * tm + (id & 1);
+        tn = 2 * tn + (id >> 1 & 1);
     }
-    const float *wsr = ws + (size_t)tn * kb;
+    const uint32_t m0 = tm * TM, n0 = tn * TN;
+    if (m0 >= M || n0 >= N)
+        return;                          // a quarter past the edge
+    const uint32_t nst = (K + 127) / 128;
 
-    la.load(A, K, m0, M, 0, K);
-    lw.load(W, K, n0, N, 0, K);
-    la.store(sA[0]);
-    lw.store(sW[0]);
+    const __amdgpu_buffer_rsrc_t ra = fb_rsrc(A, M * K), rw = fb_rsrc(W, N * K);
+    const __amdgpu_buffer_rsrc_t ras = fb_rsrc(as, M * nst * 4);
+
+    // DMA: load j of wave w fills kilobyte L*w + j of a slot, rows 8(Lw+j) +
+    // lane/8; the lane's physical chunk lane%8 takes logical chunk
+    // (lane%8) ^ ((row/2) % 8) of its row.
+    // The three lane offsets everything else follows from are hidden from the
+    // compiler once per block (launder): it would keep every sum of them and a
+    // row's or a slot's address in a register of its own across the loop.
+    const int r16 = lane & 15, g = lane >> 4;
+    uint32_t dcol = 16u * ((lane & 7) ^ (lane >> 4)), drow = (uint32_t)(lane >> 3) * K;
+    uint32_t f0 = r16 * BIG_KB + 16 * (g ^ ((r16 >> 1) & 7));
+    auto launder = [&]() { asm volatile("" : "+v"(dcol), "+v"(drow), "+v"(f0)); };
+    // loads [lo, hi) of a panel's AL (WL) per wave
+    auto dma_a = [&](uint32_t st, uint8_t *slot, int lo, int hi) {
+        const uint32_t k0 = st * 128;
+#pragma unroll
+        for (int j = lo; j < hi; ++j) {
+            const uint32_t c = k0 + (j & 1 ? dcol ^ 64 : dcol);
+            const uint32_t o = drow + c + (m0 + 8 * (AL * wave + j)) * K;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(slot + 1024 * (AL * wave + j)), 16,
+                                                     c < K ? o : FB_OOB, 0, 0, 0);
+        }
+    };
+    auto dma_w = [&](uint32_t st, uint8_t *slot, int lo, int hi) {
+#pragma unroll
+        for (int j = lo; j < hi; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rw, (lds_void *)(slot + 1024 * (WL * wave + j)), 16,
+                drow + (j & 1 ? dcol ^ 64 : dcol) + ((n0 + 8 * (WL * wave + j)) * K + st * 128), 0, 0, 0);
+    };
+
+    // Fragment of 16 rows: lane l takes row l%16 and chunks l/16 and l/16 + 4
+    // (both operands in the same order, so the sum over K is whole).
+    auto frag = [&](const uint8_t *rows16) {
+        const i32x4 p = *reinterpret_cast<const i32x4 *>(rows16 + f0);
+        const i32x4 q = *reinterpret_cast<const i32x4 *>(rows16 + (f0 ^ 64));
+        return (i32x8){p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
+    };
+    auto frag_a = [&](const uint8_t *slot, int t) { return frag(slot + (wm * 64 + 16 * t) * BIG_KB); };
+    auto frag_w = [&](const uint8_t *slot, int t) { return frag(slot + (wn * 16 * TJ + 16 * t) * BIG_KB); };
+
+    // A's scales of five blocks from b on, of the wave's row `lane` (past the
+    // end of the row: values of no use; past the buffer: zeros), and their
+    // products with the weight's
+    struct Scales {
+        f32x4 v;
+        float l;
+    };
+    const uint32_t oas = (m0 + wm * 64 + lane) * nst * 4;
+    auto load_scales = [&](uint32_t b) {
+        Scales s;
+        s.v = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ras, oas + 4 * b, 0, 0));
+        s.l = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ras, oas + 4 * b + 16, 0, 0));
+        return s;
+    };
+    const float *const wsr = ws + (size_t)min((n0 + wn * 16 * TJ) / 128, (N - 1) / 128) * nst;
+    auto times_ws = [&](Scales s, uint32_t b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            s.v[i] *= wsr[min(b + i, nst - 1)];
+        s.l *= wsr[min(b + 4, nst - 1)];
+        return s;
+    };
+
+    f32x4 acc[4][TJ];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+            acc[i][j] = (f32x4){0, 0, 0, 0};
+
+    i32x8 a[4], w0;
+    auto mfma = [&](const i32x8 &w, const i32x8 &x) {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, (f32x4){0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+    };
+    auto fold = [&](f32x4 &c, const f32x4 &p, float s) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            c[r] = __builtin_fmaf(p[r], s, c[r]);
+    };
+    // One K block: a[] and w0 hold its first fragments.  Its MFMAs run in the
+    // order j = 0 .. TJ-3, t = 0 .. 3, then t = 0 .. 3, j = TJ-2, TJ-1; the
+    // fold of each follows the fourth MFMA after it (from one block into the
+    // next), so no fold waits for its own.  After j = 0 a barrier: A's slot is
+    // read out and takes W(st+2).  After the last LDS read every wave waits for
+    // its part of the next block's panels, then for all waves; W's slot takes
+    // A(st+3), and the last eight MFMAs run while the next block's fragments
+    // replace a[].
+    constexpr int LAG = 4, NM = 4 * TJ;
+    f32x4 p[LAG];
+    float sp[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < LAG; ++i)
+        p[i] = (f32x4){0, 0, 0, 0};
+    constexpr auto tile_t = [](int i) { return i < NM - 8 ? i % 4 : (i - (NM - 8)) / 2; };
+    constexpr auto tile_j = [](int i) { return i < NM - 8 ? i / 4 : TJ - 2 + i % 2; };
+    Scales sq, sn;
+    auto stage = [&](auto in_five, uint32_t st, uint8_t *ca, uint8_t *cw, const uint8_t *na, const uint8_t *nw) {
+        constexpr int I5 = decltype(in_five)::value;
+        const float s64 = I5 == 4 ? sq.l : sq.v[I5 & 3];
+        float s[4];
+        launder();
+        spread_rows(s64, s);
+        auto step = [&](int i, const i32x8 &wf) {
+            const int f = i < LAG ? NM - LAG + i : i - LAG;
+            const float sf = i < LAG ? sp[tile_t(f)] : s[tile_t(f)];
+            const f32x4 old = p[i % LAG];
+            p[i % LAG] = mfma(wf, a[tile_t(i)]);
+            fold(acc[tile_t(f)][tile_j(f)], old, sf);
+        };
+        i32x8 w[TJ];
+        w[0] = w0;
+#pragma unroll
+        for (int j = 0; j < TJ - 2; ++j) {
+            w[j + 1] = frag_w(cw, j + 1);
+            if (j == TJ - 3)
+                w[TJ - 1] = frag_w(cw, TJ - 1);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                step(4 * j + t, w[j]);
+                if (j == 1) {
+                    // one load of the refill under each MFMA: the address unit
+                    // holds a burst of them, and the wave behind it
+                    dma_w(st + 2, ca, t * WL / 4, (t + 1) * WL / 4);
+                    if (t == 0)
+                        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            if (j != 1) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                if (j == TJ - 3)
+                    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (j == 0) {
+                // (a[] has been waited for by its MFMAs)
+                __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        // A(st+2) and W(st+2) may stay in flight.  Nothing is allowed for the
+        // scales' loads: the compiler may move those or drop them, and a
+        // count that expects them would then let the next panels be late.
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(AL + WL));
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if (I5 == 0)
+            sn = load_scales(st + 5);
+        if (I5 == 4)
+            sq = times_ws(sn, st + 1);
+        w0 = frag_w(nw, 0);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            step(NM - 8 + 2 * t, w[TJ - 2]);
+            step(NM - 8 + 2 * t + 1, w[TJ - 1]);
+            a[t] = frag_a(na, t);
+            dma_a(st + 3, cw, t * AL / 4, (t + 1) * AL / 4);
+            __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            if (t == 0)
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 13, 0);
+            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            sp[t] = s[t];
+    };
+
+    sq = load_scales(0);
+    dma_a(0, S0, 0, AL);
+    dma_w(0, S1, 0, WL);
+    dma_a(1, S2, 0, AL);
+    dma_w(1, S3, 0, WL);
+    dma_a(2, S4, 0, AL);
+    sq = times_ws(sq, 0);
+    sn = sq;
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(2 * AL + WL));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    w0 = frag_w(S1, 0);
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+        a[t] = frag_a(S0, t);
+    // (a loop left in its middle would join its exits with its back edge, and
+    // the compiler then waits for every load in flight at its head)
+    uint32_t st = 0;
+    for (; st + 5 <= nst; st += 5) {
+        stage(std::integral_constant<int, 0>(), st, S0, S1, S2, S3);
+        stage(std::integral_constant<int, 1>(), st + 1, S2, S3, S4, S0);
+        stage(std::integral_constant<int, 2>(), st + 2, S4, S0, S1, S2);
+        stage(std::integral_constant<int, 3>(), st + 3, S1, S2, S3, S4);
+        stage(std::integral_constant<int, 4>(), st + 4, S3, S4, S0, S1);
+    }
+    if (st < nst)
+        stage(std::integral_constant<int, 0>(), st, S0, S1, S2, S3);
+    if (st + 1 < nst)
+        stage(std::integral_constant<int, 1>(), st + 1, S2, S3, S4, S0);
+    if (st + 2 < nst)
+        stage(std::integral_constant<int, 2>(), st + 2, S4, S0, S1, S2);
+    if (st + 3 < nst)
+        stage(std::integral_constant<int, 3>(), st + 3, S1, S2, S3, S4);
+#pragma unroll
+    for (int i = 0; i < LAG; ++i)
+        fold(acc[tile_t(NM - LAG + i)][tile_j(NM - LAG + i)], p[i], sp[tile_t(NM - LAG + i)]);
+    // the loads past the end must land before the slots are used again
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
     __syncthreads();
 
-    const int arow = wm * 64 + (lane & 31), wrow = wn * 64 + (lane & 31);
-    const int koff = 32 * (lane >> 5);
-    for (uint32_t b = 0; b < kb; ++b) {
-        const int buf = b & 1;
-        if (b + 1 < kb) {
-            la.load(A, K, m0, M, (b + 1) * FB_BK, K);
-            lw.load(W, K, n0, N, (b + 1) * FB_BK, K);
-        }
-        i32x8 fa[2][2], fw[2][2];
+    // Lane l holds, of tile (t, j), row 16t + l%16 and columns 16j + 4(l/16) .. +3.
+    const uint32_t rb = m0 + wm * 64, cb = n0 + wn * 16 * TJ;
+    if (vec_ok) {
+        // Stage the wave's 64 x 16TJ block in LDS (RB = 32TJ bytes per row;
+        // 8-byte unit u of row r at u ^ x(r), so that 16 rows' writes spread
+        // over the banks) and store it in whole rows, 16 bytes per lane.
+        constexpr int RB = 32 * TJ, UN = RB / 8, PU = RB / 16, RPI = 64 / PU;
+        constexpr int OWN = 64 * RB;                       // this wave's bytes
+        constexpr int PS = SLOT / OWN;                     // waves per slot
+        static_assert(PS >= 1 && NWV <= 5 * PS, "fits");
+        const int es = wave / PS;
+        uint8_t *const ep = (es == 0 ? S0 : es == 1 ? S1 : es == 2 ? S2 : es == 3 ? S3 : S4) + wave % PS * OWN;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                fa[t][ks] = frag32(&sA[buf][(arow + 32 * t) * FB_PITCH + 64 * ks + koff]);
-                fw[t][ks] = frag32(&sW[buf][(wrow + 32 * t) * FB_PITCH + 64 * ks + koff]);
+            for (int j = 0; j < TJ; ++j) {
+                const f32x4 &c = acc[t][j];
+                const u32x2 v = {pk_bf16(c[0], c[1]), pk_bf16(c[2], c[3])};
+                const int r = 16 * t + r16;
+                *reinterpret_cast<u32x2 *>(ep + r * RB + 8 * ((4 * j + g) ^ (2 * (r & (UN / 2 - 1))))) = v;
             }
-        const float wsb = wsr[b];
-#pragma unroll
-        for (int ti = 0; ti < 2; ++ti) {
-            const float s = asr[ti][b] * wsb;
-#pragma unroll
-            for (int tj = 0; tj < 2; ++tj) {
-                f32x16 p = {};
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks)
-                    p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[tj][ks], fa[ti][ks], p,
-                                                                        0, 0, 0, 0, 0, 0);
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    acc[ti][tj][r] = __builtin_fmaf(p[r], s, acc[ti][tj][r]);
-            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        const int p = lane % PU;
+#pragma unroll 4
+        for (int it = 0; it < 64 / RPI; ++it) {
+            const int r = RPI * it + lane / PU;
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(ep + r * RB + 16 * (p ^ (r & (UN / 2 - 1))));
+            if (rb + r < M && cb + 8 * p < N)
+                *reinterpret_cast<u32x4 *>(out + (size_t)(rb + r) * N + cb + 8 * p) = v;
         }
-        if (b + 1 < kb) {
-            la.store(sA[buf ^ 1]);
-            lw.store(sW[buf ^ 1]);
-        }
-        __syncthreads();
+    } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < TJ; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint32_t gi = rb + 16 * t + r16, gj = cb + 16 * j + 4 * g + r;
+                    if (gi < M && gj < N)
+                        out[(size_t)gi * N + gj] = (uint16_t)f32_to_bf16(acc[t][j][r]);
+                }
     }
+}
+
+// ---------------------------------------------------------------------------
+// Small tiles, K split over the waves: 16*MT rows of A by rpw <= 16*NT rows of
+// W per workgroup (rpw a multiple of 4, so that a problem's columns can be
+// dealt evenly over the CUs), for problems with too few large tiles to fill
+// them.  Wave w takes K blocks w, w + NW, ...; each wave DMAs its blocks'
+// panels into its own ring of D slots and waits for nothing but its own loads,
+// so there is no barrier until the NW partial tiles are joined through LDS, in
+// wave order.
+// (Fragments loaded straight to registers, 16 rows of 64 bytes to an
+// instruction, were half as fast: 8 rows of whole 128-byte lines are what the
+// address unit and HBM serve best.)
+// Scales come four of the wave's blocks at a time, lane group g (quad lane
+// l%4) holding the g-th's: a load touches a cache line per row of A, and a line
+// holds many blocks' scales.
+// ---------------------------------------------------------------------------
+template <int MT, int NT, int NW, int D>
+__global__ __launch_bounds__(64 * NW) void k_fp8_gemm_block_ksplit(
+    const uint8_t *__restrict__ A, const float *__restrict__ as,
+    const uint8_t *__restrict__ W, const float *__restrict__ ws,
+    uint16_t *__restrict__ out, uint32_t M, uint32_t N, uint32_t K, uint32_t mtiles, uint32_t rpw)
+{
+    static_assert(D == 2 || D == 3, "ring");
+    constexpr int L = 2 * (MT + NT), SLOT = 1024 * L;      // DMA loads and bytes of a block
+    // one variable per ring position: see gemm_fp8.hip
+    __shared__ __attribute__((aligned(1024))) uint8_t R0[NW * SLOT];
+    __shared__ __attribute__((aligned(1024))) uint8_t R1[NW * SLOT];
+    __shared__ __attribute__((aligned(16))) uint8_t R2[D > 2 ? NW * SLOT : 16];
+    // (positions past D are never named, so their variables take no LDS)
+    auto ring = [&](int d) -> uint8_t * {
+        if constexpr (D > 2)
+            if (d == 2)
+                return R2;
+        return d == 1 ? R1 : R0;
+    };
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // workgroups that share W's rows are neighbours behind one L2
+    const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
+    const uint32_t m0 = id % mtiles * (16 * MT), n0 = id / mtiles * rpw;
+    const uint32_t nb = (K + 127) / 128;
+    const __amdgpu_buffer_rsrc_t ra = fb_rsrc(A, M * K), rw = fb_rsrc(W, N * K);
+    const __amdgpu_buffer_rsrc_t ras = fb_rsrc(as, M * nb * 4);
+    const __amdgpu_buffer_rsrc_t rws = fb_rsrc(ws, (N + 127) / 128 * nb * 4);
+
+    // 1 KB = 8 rows x 128 bytes per load, chunks swizzled as in gemm_common.hpp
+    const uint32_t dcol = 16u * ((lane & 7) ^ (lane >> 4)), drow = lane >> 3;
+    const uint32_t oa = (m0 + drow) * K, ow = (n0 + drow) * K;
+    auto dma = [&](uint32_t b, uint8_t *r) {
+        uint8_t *const slot = r + wave * SLOT;
 #pragma unroll
-    for (int ti = 0; ti < 2; ++ti)
+        for (int j = 0; j < L; ++j) {
+            const bool of_a = j < 2 * MT;
+            const int q = of_a ? j : j - 2 * MT;
+            const uint32_t c = b * 128 + (q & 1 ? dcol ^ 64 : dcol);
+            const uint32_t o = (of_a ? oa : ow) + 8 * q * K + c;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                of_a ? ra : rw, (lds_void *)(slot + 1024 * j), 16,
+                c < K && (of_a || drow + 8 * q < rpw) ? o : FB_OOB, 0, 0, 0);
+        }
+    };
+    // raw scales of the wave's blocks i .. i+3: a[t] of row 16t + l%16 and block
+    // i + l/16, w[j] of rows 16j + 4(l/16) .. +3 and block i + l%4
+    struct Scales {
+        float a[MT], w[NT];
+    } next;
+    auto load_scales = [&](uint32_t i) {
+        const uint32_t ba = wave + NW * (i + g), bw = wave + NW * (i + (lane & 3));
 #pragma unroll
-        for (int tj = 0; tj < 2; ++tj)
+        for (int t = 0; t < MT; ++t)
+            next.a[t] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                ras, ba < nb ? ((m0 + 16 * t + r16) * nb + ba) * 4 : FB_OOB, 0, 0));
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const uint32_t gj = n0 + wn * 64 + 32 * tj + mfma32_row(r, lane);
-                if (row[ti] < M && gj < N)
-                    out[(size_t)row[ti] * N + gj] = (uint16_t)f32_to_bf16(acc[ti][tj][r]);
+        for (int j = 0; j < NT; ++j)
+            next.w[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                rws, bw < nb ? ((n0 + 16 * j + 4 * g) / 128 * nb + bw) * 4 : FB_OOB, 0, 0));
+    };
+    const uint32_t f0 = r16 * BIG_KB + 16 * (g ^ ((r16 >> 1) & 7));
+    f32x4 acc[MT][NT] = {};
+    float sa[MT][4], sw[NT];
+    auto block = [&](auto u_, uint32_t i) {
+        constexpr int U = decltype(u_)::value, Q = U % 4;
+        const uint8_t *const slot = ring(U % D) + wave * SLOT;
+        if (Q == 0) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                spread_rows(next.a[t], sa[t]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                sw[j] = next.w[j];
+            load_scales(i + 4);
+        }
+        // all but the D - 1 newest blocks' panels have landed (the scales'
+        // loads are not counted on: the compiler may move them)
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm((D - 1) * L));
+        __builtin_amdgcn_sched_barrier(0);
+        i32x8 f[MT + NT];
+#pragma unroll
+        for (int e = 0; e < MT + NT; ++e) {
+            const i32x4 p = *reinterpret_cast<const i32x4 *>(slot + 2048 * e + f0);
+            const i32x4 q = *reinterpret_cast<const i32x4 *>(slot + 2048 * e + (f0 ^ 64));
+            f[e] = (i32x8){p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
+        }
+        // the slot is refilled only after its reads have returned
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);
+        __builtin_amdgcn_sched_barrier(0);
+        dma(wave + NW * (i + D), ring(U % D));
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const float swq = __int_as_float(__builtin_amdgcn_update_dpp(
+                0, __float_as_int(sw[j]), Q * 0x55, 0xF, 0xF, true));       // quad lane Q to its quad
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    f[MT + j], f[t], (f32x4){0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+                const float c = sa[t][Q] * swq;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    acc[t][j][r] = __builtin_fmaf(p[r], c, acc[t][j][r]);
             }
+        }
+    };
+    load_scales(0);
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        dma(wave + NW * d, ring(d));
+    const uint32_t mine = nb > (uint32_t)wave ? (nb - wave + NW - 1) / NW : 0;   // the wave's blocks
+    constexpr int UN = D == 3 ? 12 : 4;
+    uint32_t i = 0;
+    auto run = [&](auto self, auto u_) {
+        constexpr int U = decltype(u_)::value;
+        if constexpr (U < UN) {
+            if (i + U >= mine)
+                return;
+            block(u_, i + U);
+            self(self, std::integral_constant<int, U + 1>());
+        }
+    };
+    for (; i < mine; i += UN)
+        run(run, std::integral_constant<int, 0>());
+    // the loads past the end must land before the ring is used again
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+    __syncthreads();
+    constexpr int PB = MT * NT * 1024;                     // a wave's partial tile
+    constexpr int PER = NW * SLOT / PB;                    // of which a ring position holds
+    static_assert(PER * D >= NW, "partial tiles fit in the ring");
+    auto part = [&](int w) { return ring(w / PER) + w % PER * PB; };
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            *reinterpret_cast<f32x4 *>(part(wave) + (t * NT + j) * 1024 + 16 * lane) = acc[t][j];
+    __syncthreads();
+    // output e of the tile: row e / (16 NT), column e % (16 NT)
+    for (uint32_t e = threadIdx.x; e < 256 * MT * NT; e += 64 * NW) {
+        const uint32_t r = e / (16 * NT), c = e % (16 * NT);
+        const uint32_t tile = r / 16 * NT + c / 16, l = r % 16 + 16 * (c % 16 / 4);
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+            v += *reinterpret_cast<const float *>(part(w) + tile * 1024 + 16 * l + 4 * (c % 4));
+        if (m0 + r < M && c < rpw && n0 + c < N)
+            out[(size_t)(m0 + r) * N + n0 + c] = (uint16_t)f32_to_bf16(v);
+    }
+}
+
+// Waves and ring depth of a ksplit workgroup: what 160 KB of LDS hold of
+// 2 (MT + NT) KB blocks, waves first (measured at every MT + NT: more waves
+// beat a deeper ring).
+constexpr int ks_waves(int s) { return s <= 5 ? 8 : s == 6 ? 6 : s <= 8 ? 5 : 4; }
+constexpr int ks_depth(int s) { return s <= 3 ? 3 : 2; }
+
+struct GemmArgs {
+    const uint8_t *a;
+    const float *as;
+    const uint8_t *w;
+    const float *ws;
+    uint16_t *out;
+    uint32_t m, n, k;
+    hipStream_t st;
+};
+
+template <int MT, int NT>
+void launch_ksplit(const GemmArgs &g, uint32_t rpw)
+{
+    constexpr int NW = ks_waves(MT + NT), D = ks_depth(MT + NT);
+    const uint32_t mt = (g.m + 16 * MT - 1) / (16 * MT), nt = (g.n + rpw - 1) / rpw;
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_fp8_gemm_block_ksplit<MT, NT, NW, D>), dim3(mt * nt), dim3(64 * NW),
+                       0, g.st, g.a, g.as, g.w, g.ws, g.out, g.m, g.n, g.k, mt, rpw);
+}
+
+template <int MT>
+void launch_ksplit_rows(const GemmArgs &g, uint32_t rpw)
+{
+    if (rpw <= 32)
+        launch_ksplit<MT, 2>(g, rpw);
+    else if (rpw <= 48)
+        launch_ksplit<MT, 3>(g, rpw);
+    else
+        launch_ksplit<MT, 5>(g, rpw);
+}
+
+template <int MW, int NW, int TJ>
+hipError_t launch_tiles(const GemmArgs &g, uint32_t mt, uint32_t nt, uint32_t first, uint32_t tiles,
+                        bool quarters)
+{
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_fp8_gemm_block_tiles<MW, NW, TJ>), dim3(quarters ? 4 * tiles : tiles),
+                       dim3(64 * MW * NW), 0, g.st, g.a, g.as, g.w, g.ws, g.out, g.m, g.n, g.k, mt, nt,
+                       first, (uint32_t)quarters, (uint32_t)(g.n % 8 == 0));
+    count_launch();
+    return hipGetLastError();
 }
 
 } // namespace
@@ -118,11 +586,51 @@ hipError_t launch_fp8_gemm_blockscale(const uint8_t *a, const float *as, const u
                                       const float *ws, uint16_t *out, uint32_t m, uint32_t n,
                                       uint32_t k, hipStream_t st)
 {
-    const uint32_t mt = (m + FB_T - 1) / FB_T, nt = (n + FB_T - 1) / FB_T;
-    hipLaunchKernelGGL(k_fp8_gemm_block, dim3(mt * nt), dim3(256), 0, st, a, as, w, ws, out, m, n, k,
-                       mt, nt);
-    count_launch();
-    return hipGetLastError();
+    const GemmArgs g = {a, as, w, ws, out, m, n, k, st};
+    const uint32_t cus = cu_count() ? cu_count() : 256, nb = (k + 127) / 128;
+
+    // Time estimates in nanoseconds, from what the kernels take per K block
+    // (one MI355X, K = 5120 and 17408).  ksplit: 45 per 16 rows of A and of W a
+    // workgroup loads, one workgroup per CU.  128 x 128 tiles: 680 alone on a
+    // CU, 1150 for two.  256 x 256 tiles: 1680.
+    const uint32_t mtk = m <= 64 ? (m + 15) / 16 : 4, mwg = (m + 16 * mtk - 1) / (16 * mtk);
+    // ksplit's W rows per workgroup: the columns dealt over the CUs, at most
+    // 80, in as few rounds as that allows
+    const uint32_t per = cus > mwg ? cus / mwg : 1;
+    const uint32_t rounds_n = (n + 80 * per - 1) / (80 * per);
+    const uint32_t rpw = ((n + rounds_n * per - 1) / (rounds_n * per) + 3) / 4 * 4;
+    const uint64_t wgs = (uint64_t)mwg * ((n + rpw - 1) / rpw);
+    const uint32_t ntk = rpw <= 32 ? 2 : rpw <= 48 ? 3 : 5;
+    const uint64_t t_ks = (wgs + cus - 1) / cus * (45ull * (mtk + ntk) * nb);
+    auto t_small = [&](uint64_t tiles) {
+        return (tiles / (2 * cus) * 1150 + (tiles % (2 * cus) > cus ? 1150 : tiles % (2 * cus) ? 680 : 0)) * nb;
+    };
+    const uint32_t ms = (m + 127) / 128, ns = (n + 127) / 128, ml = (m + 255) / 256, nl = (n + 255) / 256;
+    const uint64_t small = (uint64_t)ms * ns, large = (uint64_t)ml * nl;
+    // the 256 x 256 tiles past the last whole round run as 128 x 128 quarters
+    // if that is faster than another round
+    const uint64_t tail = large % cus;
+    const bool quarter = tail && t_small(4 * tail) < 1680ull * nb;
+    const uint64_t full = quarter ? large - tail : large;
+    const uint64_t t_large = (full + cus - 1) / cus * 1680ull * nb + (quarter ? t_small(4 * tail) : 0);
+
+    if (t_ks <= t_small(small) && t_ks <= t_large) {
+        if (mtk == 1)
+            launch_ksplit_rows<1>(g, rpw);
+        else if (mtk == 2)
+            launch_ksplit_rows<2>(g, rpw);
+        else if (mtk == 3)
+            launch_ksplit_rows<3>(g, rpw);
+        else
+            launch_ksplit_rows<4>(g, rpw);
+        count_launch();
+        return hipGetLastError();
+    }
+    if (full == 0 || t_small(small) <= t_large)
+        return launch_tiles<2, 2, 4>(g, ms, ns, 0, (uint32_t)small, false);
+    if (const hipError_t e = launch_tiles<4, 2, 8>(g, ml, nl, 0, (uint32_t)full, false))
+        return e;
+    return quarter ? launch_tiles<2, 2, 4>(g, ml, nl, (uint32_t)full, (uint32_t)tail, true) : hipSuccess;
 }
 
 } // namespace qp
