@@ -23,9 +23,10 @@
 //    receives its own weight row for the four tokens; its 16 codes lie in one
 //    128-block, so a window's sums start from zero and join the running F32
 //    sums with one FMA by the lane's block scale.
-//  * h_e stays at F32's precision between the launches as a sum of two BF16
-//    planes, hi = bf16(h), lo = bf16(h - hi) (error 2^-17 of h): the second
-//    product then takes two MFMAs where one would read a rounded h.
+//  * h_e is kept between the launches as two BF16 rows, hi = bf16(h) and
+//    lo = bf16(h - hi) (error 2^-17 of h, where one row would leave 2^-9).  They
+//    are two of the four rows an MFMA takes, so one token costs the second
+//    product no more than one rounded row would.
 //  * The second launch's workgroups own output columns for all experts, so a
 //    token's sum over its experts needs no atomics and has a fixed order.
 #include "qp_device.hpp"
@@ -40,12 +41,23 @@ constexpr int MAX_T = 16, MAX_TOPK = 16, MAX_E = 512, MAX_PAIRS = MAX_T * MAX_TO
 constexpr int WIN = 256;                        // K elements per window
 // Past every buffer (each is below 2^31 bytes): such a load returns zero.
 constexpr uint32_t OOB = 0x80000000u;
+// Offset of a weight row that does not exist and size of the weights' buffers
+// (an expert's matrix is a multiple of 2^14 bytes below 2^31).
+constexpr uint32_t NOROW = 0x7FFFFF00u;
 
-// What the first launch leaves for the second (behind the two planes of h).
+// A part is an expert and at most S of its tokens: an expert with more has
+// several parts, side by side, whose waves read its weights together.  An MFMA
+// takes four operand rows: four tokens of x, or two of h (hi and lo).
+constexpr uint32_t S_UP = 4, S_DOWN = 2;
+
+struct Parts {
+    uint32_t n;
+    uint32_t expert[MAX_PAIRS];                 // of each part, ascending
+    uint32_t first[MAX_PAIRS + 1];              // its first pair (its last is before the next part's first)
+};
+// What the first launch leaves for the second (behind the rows of h).
 struct Plan {
-    uint32_t nact;
-    uint32_t expert[MAX_PAIRS];                 // active experts, ascending
-    uint32_t first[MAX_PAIRS + 1];              // their first pair
+    Parts down;
     uint32_t token[MAX_PAIRS];                  // of each pair
 };
 
@@ -60,14 +72,51 @@ __device__ __forceinline__ float dpp_f(float v)
     return __uint_as_float(dpp_u<CTRL>(__float_as_uint(v)));
 }
 
+// Both halves of a lane swap of v with itself: rows of 16 lanes 0 0 2 2 and
+// 1 1 3 3 (swap16), lanes 0 .. 31 twice and 32 .. 63 twice (swap32).
+__device__ __forceinline__ u32x2 swap16(uint32_t v)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return (u32x2){r[0], r[1]};
+}
+__device__ __forceinline__ u32x2 swap32(uint32_t v)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return (u32x2){r[0], r[1]};
+}
+__device__ __forceinline__ float add_halves(u32x2 h)
+{
+    return __uint_as_float(h[0]) + __uint_as_float(h[1]);
+}
+
 __device__ __forceinline__ uint32_t wave_max_u(uint32_t v)
 {
     v = max(v, dpp_u<0xB1>(v));                 // pairs, quads, eights, sixteens
     v = max(v, dpp_u<0x4E>(v));
     v = max(v, dpp_u<0x141>(v));
     v = max(v, dpp_u<0x140>(v));
-    v = max(v, (uint32_t)__shfl_xor((int)v, 16, WAVE));
-    return max(v, (uint32_t)__shfl_xor((int)v, 32, WAVE));
+    u32x2 h = swap16(v);
+    h = swap32(max(h[0], h[1]));
+    return max(h[0], h[1]);
+}
+__device__ __forceinline__ float wave_sum_f(float v)
+{
+    v += dpp_f<0xB1>(v);
+    v += dpp_f<0x4E>(v);
+    v += dpp_f<0x141>(v);
+    v += dpp_f<0x140>(v);
+    return add_halves(swap32(__float_as_uint(add_halves(swap16(__float_as_uint(v))))));
+}
+// Sum of v over the lanes up to and including this one.
+__device__ __forceinline__ uint32_t wave_scan_u(uint32_t v)
+{
+    v += dpp_u<0x111>(v);                       // shifts by 1, 2, 4, 8 in a row of 16
+    v += dpp_u<0x112>(v);
+    v += dpp_u<0x114>(v);
+    v += dpp_u<0x118>(v);
+    // the last lane of rows 0 and 2 to rows 1 and 3, then lane 31 to the upper half
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);
+    return v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);
 }
 
 // Monotone integer key of a logit; 0 only for -inf and for what is no expert.
@@ -83,6 +132,7 @@ __device__ __forceinline__ float value_of(uint32_t k)
 
 struct Routing {
     Plan plan;
+    Parts up;
     float weight[MAX_PAIRS];                    // p of each pair
     // scratch
     uint32_t sel_e[MAX_T][MAX_TOPK], nsel[MAX_T];
@@ -92,33 +142,21 @@ struct Routing {
 
 // The topk of one token by a wave: lane l holds experts l*EPL .. l*EPL+EPL-1,
 // so among equal keys the lowest lane, and in it the lowest slot, is the
-// lowest expert.
+// lowest expert.  Lane i < n (returned) gets the i-th chosen expert and its
+// weight.
 template <int EPL>
-__device__ __forceinline__ void route_token(const float *__restrict__ logits, uint32_t E,
-                                            uint32_t topk, bool renorm, uint32_t t, Routing &R)
+__device__ __forceinline__ uint32_t choose(const float *__restrict__ row, uint32_t E, uint32_t topk,
+                                           bool renorm, uint32_t &my_e, float &my_w)
 {
     const uint32_t lane = threadIdx.x & 63;
-    uint32_t key[EPL];
+    uint32_t key[EPL], had[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         const uint32_t e = lane * EPL + j;
-        key[j] = e < E ? key_of(logits[(size_t)t * E + e] + 0.0f) : 0u;   // (-0 ties with +0)
+        key[j] = had[j] = e < E ? key_of(row[e] + 0.0f) : 0u;   // (-0 ties with +0)
     }
-    float top = 0.0f, all = 0.0f;
-    if (!renorm) {
-        uint32_t b = 0;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            b = max(b, key[j]);
-        top = value_of(wave_max_u(b));
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            all += key[j] ? expf(value_of(key[j]) - top) : 0.0f;
-        for (int o = 1; o < 64; o <<= 1)
-            all += __shfl_xor(all, o, WAVE);
-    }
-    uint32_t n = 0, my_e = 0;
-    float sum = 0.0f, my_w = 0.0f;
+    uint32_t n = 0, my_k = 0, top_k = 0;
+    my_e = 0;
     for (uint32_t i = 0; i < topk; ++i) {
         uint32_t b = key[0], bj = 0;
 #pragma unroll
@@ -133,28 +171,54 @@ __device__ __forceinline__ void route_token(const float *__restrict__ logits, ui
         const uint32_t who = (uint32_t)__builtin_ctzll(__ballot(b == m));
         const uint32_t j = (uint32_t)__builtin_amdgcn_readlane((int)bj, (int)who);
         if (i == 0)
-            top = value_of(m);
-        const float w = expf(value_of(m) - top);
-        sum += w;
-        if (lane == i) {
-            my_e = who * EPL + j;
-            my_w = w;
-        }
-        if (lane == who) {
+            top_k = m;
+        my_e = lane == i ? who * EPL + j : my_e;
+        my_k = lane == i ? m : my_k;
 #pragma unroll
-            for (int q = 0; q < EPL; ++q)
-                if (q == (int)j)
-                    key[q] = 0;
-        }
+        for (int q = 0; q < EPL; ++q)
+            key[q] = lane == who && q == (int)j ? 0u : key[q];
         n = i + 1;
     }
-    if (lane < n) {
-        R.sel_e[t][lane] = my_e;
-        R.sel_w[t][lane] = my_w / (renorm ? sum : all);
-        atomicOr(&R.mask[my_e], 1u << t);       // an OR: order does not matter
+    const float top = value_of(top_k), w = lane < n ? expf(value_of(my_k) - top) : 0.0f;
+    float total = w;
+    if (!renorm) {
+        total = 0.0f;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            total += had[j] ? expf(value_of(had[j]) - top) : 0.0f;
     }
+    my_w = w / wave_sum_f(total);
+    return n;
+}
+
+__device__ __forceinline__ uint32_t choose_any(const float *__restrict__ row, uint32_t E, uint32_t topk,
+                                               bool renorm, uint32_t &my_e, float &my_w)
+{
+    return E <= 64    ? choose<1>(row, E, topk, renorm, my_e, my_w)
+           : E <= 128 ? choose<2>(row, E, topk, renorm, my_e, my_w)
+           : E <= 256 ? choose<4>(row, E, topk, renorm, my_e, my_w)
+                      : choose<8>(row, E, topk, renorm, my_e, my_w);
+}
+
+// One token: its experts are the parts and the pairs, in the order chosen.
+// Every wave finds and writes the same, so none waits for another.
+__device__ void route_one(const float *__restrict__ logits, uint32_t E, uint32_t topk, bool renorm,
+                          Routing &R)
+{
+    const uint32_t lane = threadIdx.x & 63;
+    uint32_t e;
+    float w;
+    const uint32_t n = choose_any(logits, E, topk, renorm, e, w);
+    if (lane < n) {
+        R.up.expert[lane] = R.plan.down.expert[lane] = e;
+        R.weight[lane] = w;
+        R.plan.token[lane] = 0;
+    }
+    if (lane <= n)
+        R.up.first[lane] = R.plan.down.first[lane] = lane;
     if (lane == 0)
-        R.nsel[t] = n;
+        R.up.n = R.plan.down.n = n;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
 // Fill R (every thread of the workgroup calls this; ends with a barrier).
@@ -166,42 +230,45 @@ __device__ void route(const float *__restrict__ logits, uint32_t T, uint32_t E, 
         R.mask[e] = 0;
     __syncthreads();
     for (uint32_t t = wave; t < T; t += nw) {
-        if (E <= 64)
-            route_token<1>(logits, E, topk, renorm, t, R);
-        else if (E <= 128)
-            route_token<2>(logits, E, topk, renorm, t, R);
-        else if (E <= 256)
-            route_token<4>(logits, E, topk, renorm, t, R);
-        else
-            route_token<8>(logits, E, topk, renorm, t, R);
+        uint32_t e;
+        float w;
+        const uint32_t n = choose_any(logits + (size_t)t * E, E, topk, renorm, e, w);
+        if (lane < n) {
+            R.sel_e[t][lane] = e;
+            R.sel_w[t][lane] = w;
+            atomicOr(&R.mask[e], 1u << t);      // an OR: order does not matter
+        }
+        if (lane == 0)
+            R.nsel[t] = n;
     }
     __syncthreads();
-    if (wave == 0) {
-        // lane l: experts 8l .. 8l+7; active experts (high half) and pairs
-        // (low half) before it, by an inclusive scan over the lanes
+    if (wave < 2) {
+        // wave 0 the parts of the first product, wave 1 of the second.  Lane l:
+        // experts 8l .. 8l+7; parts (high half) and pairs (low half) before it
+        // by an inclusive scan over the lanes
+        Parts &P = wave ? R.plan.down : R.up;
+        const uint32_t S = wave ? S_DOWN : S_UP;
         uint32_t mk[8], mine = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             mk[j] = R.mask[8 * lane + j];
-            mine += (mk[j] ? 0x10000u : 0u) + (uint32_t)__popc(mk[j]);
+            const uint32_t c = (uint32_t)__popc(mk[j]);
+            mine += ((c + S - 1) / S << 16) + c;
         }
-        uint32_t inc = mine;
-        for (int o = 1; o < 64; o <<= 1) {
-            const uint32_t v = (uint32_t)__shfl_up((int)inc, o, WAVE);
-            inc += lane >= (uint32_t)o ? v : 0u;
-        }
+        const uint32_t inc = wave_scan_u(mine);
         uint32_t at = inc - mine;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (mk[j]) {
-                R.plan.expert[at >> 16] = 8 * lane + j;
-                R.plan.first[at >> 16] = at & 0xFFFFu;
-                R.base[8 * lane + j] = at & 0xFFFFu;
-                at += 0x10000u + (uint32_t)__popc(mk[j]);
+        for (int j = 0; j < 8; ++j) {
+            R.base[8 * lane + j] = at & 0xFFFFu;    // (both waves write the same)
+            for (int left = __popc(mk[j]); left > 0; left -= S) {
+                P.expert[at >> 16] = 8 * lane + j;
+                P.first[at >> 16] = at & 0xFFFFu;
+                at += 0x10000u + min((uint32_t)left, S);
             }
+        }
         if (lane == 63) {
-            R.plan.nact = inc >> 16;
-            R.plan.first[inc >> 16] = inc & 0xFFFFu;
+            P.n = inc >> 16;
+            P.first[inc >> 16] = inc & 0xFFFFu;
         }
     }
     __syncthreads();
@@ -220,6 +287,11 @@ __device__ void route(const float *__restrict__ logits, uint32_t T, uint32_t E, 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, uint32_t bytes)
 {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, 0x00020000);
+}
+// (weights: nontemporal, they are read once)
+__device__ __forceinline__ u32x4 load16_nt(__amdgpu_buffer_rsrc_t r, uint32_t off)
+{
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 2));
 }
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off)
 {
@@ -258,8 +330,7 @@ __device__ __forceinline__ float sum_slices(float v)
 {
     v += dpp_f<0x128>(v);                       // rotate by 8 and by 4 in a row of 16
     v += dpp_f<0x124>(v);
-    v += __shfl_xor(v, 16, WAVE);
-    return v + __shfl_xor(v, 32, WAVE);
+    return add_halves(swap32(__float_as_uint(add_halves(swap16(__float_as_uint(v))))));
 }
 
 struct MoeArgs {
@@ -267,252 +338,329 @@ struct MoeArgs {
     const float *logits;
     const uint8_t *w13, *w2;
     const float *s13, *s2;
-    uint16_t *hi, *lo;                          // [pairs, I] planes of p * h
+    uint16_t *h;                                // [2 pairs, I]: hi and lo of p * h
     Plan *plan;
     uint16_t *out;
     uint32_t T, E, topk, H, I, renorm;
 };
 
-// Gate rows 4g .. 4g+3 and their up rows of one expert, for its cnt <= 4*TG
-// tokens.
-template <int TG>
-__device__ __forceinline__ void gate_up(const MoeArgs &A, const Routing &R, uint32_t e, uint32_t first,
-                                        uint32_t cnt, uint32_t g)
-{
-    constexpr int D = TG == 1 ? 4 : 2;          // windows in flight
-    const uint32_t lane = threadIdx.x & 63, r4 = lane & 3, c16 = lane >> 2;
-    const uint32_t HB = A.H / 128, IB = A.I / 128, nw = (A.H + WIN - 1) / WIN;
-    const __amdgpu_buffer_rsrc_t rw = rsrc(A.w13 + (size_t)e * 2 * A.I * A.H, 2 * A.I * A.H);
-    const __amdgpu_buffer_rsrc_t rs = rsrc(A.s13 + (size_t)e * 2 * IB * HB, 2 * IB * HB * 4);
-    const __amdgpu_buffer_rsrc_t rx = rsrc(A.x, A.T * A.H * 2);
-    const uint32_t og = (4 * g + r4) * A.H + 16 * c16, ou = og + A.I * A.H;
-    const uint32_t sg = (4 * g / 128) * HB * 4 + 4 * (lane >> 5), su = sg + IB * HB * 4;
-    uint32_t ox[TG];
-#pragma unroll
-    for (int t = 0; t < TG; ++t)
-        ox[t] = R.plan.token[first + min(4u * t + r4, cnt - 1)] * A.H * 2 + 32 * c16;
+// One wave's work: a run of units, each a few weight rows of one expert times
+// the operand rows of one part, over windows w0, w0 + WS, ... < w1 (past the K
+// range: zeros).
+struct Unit {
+    const uint8_t *w;                           // the weight rows' common base
+    uint32_t s0, s1;                            // byte offsets of their rows in the scale grid
+    uint32_t x;                                 // per lane: operand row l % 4 at chunk l / 4
+    uint32_t w0, w1;
+};
 
+// Walk the units u0, u0 + step, ... < n with D windows in flight, across the
+// units' ends: RW groups of 4 weight rows (lane l's row l % 4, chunk l / 4 at
+// base + ow[g]); unit(u) describes one; sink(u, acc) takes its sums acc[g][r]:
+// the lane's K slice of its row of group g with operand row r (r < NR).
+// Groups below split scale by the grid row s0, the others by s1.
+template <int RW, int NR, int D, int WS, class GetUnit, class Sink>
+__device__ __forceinline__ void stream(__amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t rx,
+                                       const uint32_t (&ow)[RW], uint32_t split, uint32_t kn,
+                                       uint32_t u0, uint32_t n, uint32_t step, GetUnit unit, Sink sink)
+{
+    const uint32_t lane = threadIdx.x & 63, c16 = lane >> 2;
     struct Stage {
-        u32x4 g, u, x[TG][2];
-        float sg, su;
+        u32x4 w[RW], x[2];
+        float s0, s1;
     } st[D];
-    auto fetch = [&](Stage &s, uint32_t w) {
-        const bool ok = w * WIN + 16 * c16 < A.H;
-        s.g = load16(rw, ok ? og + w * WIN : OOB);
-        s.u = load16(rw, ok ? ou + w * WIN : OOB);
-        s.sg = load4(rs, ok ? sg + 8 * w : OOB);
-        s.su = load4(rs, ok ? su + 8 * w : OOB);
+    // the next window to fetch: window fw of unit fu, described by f
+    uint32_t fu = u0, fw = 0;
+    Unit f = {};
+    f.w1 = 0;
+    if (fu < n) {
+        f = unit(fu);
+        fw = f.w0;
+    }
+    auto fetch = [&](Stage &s) {
+        // What a lane may not load is moved past the buffers by an addend that
+        // the compiler cannot see through: it would turn a select of offsets
+        // into branches around the loads, and the wave would then wait for
+        // every load in flight.  (No more units: w1 == 0.)
+        const bool ok = fw < f.w1 && fw * WIN + 16 * c16 < kn;
+        uint32_t dw = ok ? fw * WIN : OOB, dx = ok ? 2 * fw * WIN : OOB;
+        uint32_t ds = ok ? 8 * fw + 4 * (lane >> 5) : OOB;
+        asm volatile("" : "+v"(dw), "+v"(dx), "+v"(ds));
+        const __amdgpu_buffer_rsrc_t rw = rsrc(f.w, NOROW);
 #pragma unroll
-        for (int t = 0; t < TG; ++t) {
-            s.x[t][0] = load16(rx, ok ? ox[t] + 2 * w * WIN : OOB);
-            s.x[t][1] = load16(rx, ok ? ox[t] + 2 * w * WIN + 16 : OOB);
-        }
-    };
-    f32x4 ag[TG] = {}, au[TG] = {};
-    auto use = [&](const Stage &s) {
-        s16x4 wg[4], wu[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            wg[i] = fp8x4_bf16(s.g[i]);
-            wu[i] = fp8x4_bf16(s.u[i]);
-        }
-#pragma unroll
-        for (int t = 0; t < TG; ++t) {
-            const f32x4 pg = window(wg, s.x[t], (f32x4){});
-            const f32x4 pu = window(wu, s.x[t], (f32x4){});
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                ag[t][r] = __builtin_fmaf(pg[r], s.sg, ag[t][r]);
-                au[t][r] = __builtin_fmaf(pu[r], s.su, au[t][r]);
+        for (int g = 0; g < RW; ++g)
+            s.w[g] = load16_nt(rw, ow[g] + dw);
+        s.x[0] = load16(rx, f.x + dx);
+        s.x[1] = load16(rx, f.x + dx + 16);
+        s.s0 = load4(rs, f.s0 + ds);
+        s.s1 = load4(rs, f.s1 + ds);
+        fw += WS;
+        if (fw >= f.w1 && fu < n) {
+            fu += step;
+            f.w1 = 0;
+            if (fu < n) {
+                f = unit(fu);
+                fw = f.w0;
             }
         }
     };
+    f32x4 acc[RW] = {};
+    uint32_t uu = u0, left = 0;
+    if (uu < n) {
+        const Unit u = unit(uu);
+        left = (u.w1 - u.w0 + WS - 1) / WS;
+    }
 #pragma unroll
     for (int d = 0; d < D; ++d)
-        fetch(st[d], d);
-    for (uint32_t w = 0; w < nw; w += D) {
+        fetch(st[d]);
+    while (uu < n) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            use(st[d]);
-            fetch(st[d], w + d + D);
-        }
-    }
-    // lane l takes token l / 4 of weight row l % 4
-    float vg = 0.0f, vu = 0.0f;
+            const Stage &s = st[d];
 #pragma unroll
-    for (int t = 0; t < 4 * TG; ++t) {
-        const float a = sum_slices(ag[t / 4][t % 4]), b = sum_slices(au[t / 4][t % 4]);
-        vg = c16 == (uint32_t)t ? a : vg;
-        vu = c16 == (uint32_t)t ? b : vu;
-    }
-    if (c16 < cnt) {
-        const float h = vg / (1.0f + expf(-vg)) * vu * R.weight[first + c16];
-        const uint32_t hi = f32_to_bf16(h);
-        const size_t at = (size_t)(first + c16) * A.I + 4 * g + r4;
-        A.hi[at] = (uint16_t)hi;
-        A.lo[at] = (uint16_t)f32_to_bf16(h - bf16_lo(hi));
+            for (int g = 0; g < RW; ++g) {
+                s16x4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = fp8x4_bf16(s.w[g][i]);
+                const f32x4 p = window(v, s.x, (f32x4){0, 0, 0, 0});
+                const float sg = (uint32_t)g < split ? s.s0 : s.s1;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    float v = __builtin_fmaf(p[r], sg, acc[g][r]);
+                    // pinned here: sunk past the refill, it would make the
+                    // compiler copy (and so wait for) the registers being loaded
+                    asm volatile("" : "+v"(v));
+                    acc[g][r] = v;
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            fetch(st[d]);
+            __builtin_amdgcn_sched_barrier(0);
+            if (--left == 0 && uu < n) {
+                sink(uu, acc);
+#pragma unroll
+                for (int g = 0; g < RW; ++g)
+                    acc[g] = (f32x4){0, 0, 0, 0};
+                uu += step;
+                if (uu < n) {
+                    const Unit u = unit(uu);
+                    left = (u.w1 - u.w0 + WS - 1) / WS;
+                }
+            }
+        }
     }
 }
 
-// First launch: route, then gate/up tasks of 4 + 4 rows, one wave each.
+// First launch: route, then units of RG * (4 + 4) gate and up rows of a part.
+// A workgroup's four waves share a unit, wave w taking windows w, w + 4, ...,
+// and join their sums through LDS in wave order: the rows of a unit are one
+// contiguous block (two, gate and up) that is read at one time, which HBM
+// serves better than as many separate walks along K.
+template <int NTOK, int RG>
 __global__ __launch_bounds__(256) void k_moe_gate_up(MoeArgs A)
 {
     __shared__ Routing R;
-    route(A.logits, A.T, A.E, A.topk, A.renorm != 0, R);
+    __shared__ float part_sum[2][4][2 * RG][4 * NTOK];
+    if (NTOK == 1)
+        route_one(A.logits, A.E, A.topk, A.renorm != 0, R);
+    else
+        route(A.logits, A.T, A.E, A.topk, A.renorm != 0, R);
     if (blockIdx.x == 0) {
-        const uint32_t n = R.plan.nact, pairs = R.plan.first[n];
+        const uint32_t n = R.plan.down.n, pairs = R.plan.down.first[n];
         for (uint32_t i = threadIdx.x; i <= n; i += blockDim.x)
-            A.plan->first[i] = R.plan.first[i];
+            A.plan->down.first[i] = R.plan.down.first[i];
         for (uint32_t i = threadIdx.x; i < n; i += blockDim.x)
-            A.plan->expert[i] = R.plan.expert[i];
+            A.plan->down.expert[i] = R.plan.down.expert[i];
         for (uint32_t i = threadIdx.x; i < pairs; i += blockDim.x)
             A.plan->token[i] = R.plan.token[i];
         if (threadIdx.x == 0)
-            A.plan->nact = n;
+            A.plan->down.n = n;
     }
-    const uint32_t groups = A.I / 4, tasks = R.plan.nact * groups;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    for (uint32_t task = blockIdx.x * 4 + wave; task < tasks; task += gridDim.x * 4) {
-        const uint32_t slot = task / groups, g = task % groups;
-        const uint32_t e = __builtin_amdgcn_readfirstlane(R.plan.expert[slot]);
-        const uint32_t first = __builtin_amdgcn_readfirstlane(R.plan.first[slot]);
-        const uint32_t cnt = __builtin_amdgcn_readfirstlane(R.plan.first[slot + 1]) - first;
-        if (cnt <= 4)
-            gate_up<1>(A, R, e, first, cnt, g);
-        else if (cnt <= 8)
-            gate_up<2>(A, R, e, first, cnt, g);
-        else
-            gate_up<4>(A, R, e, first, cnt, g);
-    }
-}
-
-constexpr int DOWN_WAVES = 8, DOWN_ROWS = 8;
-
-// Columns c0 .. c0+7 of the output over windows [w0, w1) of one expert's I,
-// for its cnt <= 4*TG tokens, added to acc[token][column].
-template <int TG>
-__device__ __forceinline__ void down(const MoeArgs &A, const Plan &P, uint32_t e, uint32_t first,
-                                     uint32_t cnt, uint32_t c0, uint32_t w0, uint32_t w1,
-                                     float (*acc)[DOWN_ROWS])
-{
-    constexpr int D = 2;
     const uint32_t lane = threadIdx.x & 63, r4 = lane & 3, c16 = lane >> 2;
-    const uint32_t HB = A.H / 128, IB = A.I / 128;
-    const __amdgpu_buffer_rsrc_t rw = rsrc(A.w2 + (size_t)e * A.H * A.I, A.H * A.I);
-    const __amdgpu_buffer_rsrc_t rs = rsrc(A.s2 + (size_t)e * HB * IB, HB * IB * 4);
-    const uint32_t plane = A.T * A.topk * A.I * 2;
-    const __amdgpu_buffer_rsrc_t rhi = rsrc(A.hi, plane), rlo = rsrc(A.lo, plane);
-    const uint32_t ow = (c0 + r4) * A.I + 16 * c16;
-    const uint32_t os = (c0 / 128) * IB * 4 + 4 * (lane >> 5);
-    uint32_t ox[TG];
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t HB = A.H / 128, IB = A.I / 128, groups = A.I / (4 * RG);
+    const uint32_t nwq = ((A.H + WIN - 1) / WIN + 3) / 4;   // windows of each wave
+    uint32_t ow[2 * RG];
 #pragma unroll
-    for (int t = 0; t < TG; ++t)
-        ox[t] = (first + min(4u * t + r4, cnt - 1)) * A.I * 2 + 32 * c16;
-    struct Stage {
-        u32x4 w[2], hi[TG][2], lo[TG][2];
-        float s;
-    } st[D];
-    auto fetch = [&](Stage &s, uint32_t w) {
-        const bool ok = w < w1 && w * WIN + 16 * c16 < A.I;
-        s.w[0] = load16(rw, ok ? ow + w * WIN : OOB);
-        s.w[1] = load16(rw, ok ? ow + 4 * A.I + w * WIN : OOB);
-        s.s = load4(rs, ok ? os + 8 * w : OOB);
-#pragma unroll
-        for (int t = 0; t < TG; ++t)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                s.hi[t][q] = load16(rhi, ok ? ox[t] + 2 * w * WIN + 16 * q : OOB);
-                s.lo[t][q] = load16(rlo, ok ? ox[t] + 2 * w * WIN + 16 * q : OOB);
-            }
-    };
-    f32x4 a[TG][2] = {};
-    auto use = [&](const Stage &s) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            s16x4 w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = fp8x4_bf16(s.w[q][i]);
-#pragma unroll
-            for (int t = 0; t < TG; ++t) {
-                const f32x4 p = window(w, s.hi[t], window(w, s.lo[t], (f32x4){}));
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    a[t][q][r] = __builtin_fmaf(p[r], s.s, a[t][q][r]);
-            }
-        }
-    };
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-        fetch(st[d], w0 + d);
-    for (uint32_t w = w0; w < w1; w += D) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            use(st[d]);
-            fetch(st[d], w + d + D);
-        }
+    for (int q = 0; q < RG; ++q) {
+        ow[q] = (4 * q + r4) * A.H + 16 * c16;
+        ow[RG + q] = ow[q] + A.I * A.H;
     }
-    // other lanes of this wave may have added to the same sums before
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    // unit u: rows 4 RG (u % groups) of part u / groups
+    auto part = [&](uint32_t u, uint32_t &e, uint32_t &first, uint32_t &cnt) {
+        const uint32_t p = u / groups;
+        e = __builtin_amdgcn_readfirstlane(R.up.expert[p]);
+        first = __builtin_amdgcn_readfirstlane(R.up.first[p]);
+        cnt = __builtin_amdgcn_readfirstlane(R.up.first[p + 1]) - first;
+        return u % groups * (4 * RG);
+    };
+    auto unit = [&](uint32_t u) {
+        uint32_t e, first, cnt;
+        const uint32_t row = part(u, e, first, cnt);
+        Unit d;
+        d.w = A.w13 + ((size_t)e * 2 * A.I + row) * A.H;
+        d.s0 = (e * 2 * IB + row / 128) * HB * 4;
+        d.s1 = d.s0 + IB * HB * 4;
+        d.x = R.plan.token[first + min(r4, cnt - 1)] * A.H * 2 + 32 * c16;
+        d.w0 = wave;
+        d.w1 = wave + 4 * nwq;
+        return d;
+    };
+    uint32_t buf = 0;
+    auto sink = [&](uint32_t u, const f32x4 (&acc)[2 * RG]) {
+        uint32_t e, first, cnt;
+        const uint32_t row = part(u, e, first, cnt);
+        // lane l takes token l / 4 of weight row l % 4
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        float v = 0.0f;
+        for (int q = 0; q < 2 * RG; ++q) {
+            float v = 0.0f;
 #pragma unroll
-        for (int t = 0; t < 4 * TG; ++t) {
-            const float s = sum_slices(a[t / 4][q][t % 4]);
-            v = c16 == (uint32_t)t ? s : v;
+            for (int t = 0; t < NTOK; ++t) {
+                const float s = sum_slices(acc[q][t]);
+                v = c16 == (uint32_t)t ? s : v;
+            }
+            if (c16 < NTOK)
+                part_sum[buf][wave][q][lane] = v;
         }
-        if (c16 < cnt)
-            acc[P.token[first + c16]][4 * q + r4] += v;   // only this wave's, one lane each
-    }
+        // (the next unit takes the other buffer, so one barrier is enough)
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < RG; ++q) {
+            if (c16 >= cnt || (uint32_t)(q % 4) != wave)
+                continue;
+            float vg = 0.0f, vu = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                vg += part_sum[buf][w][q][lane];
+                vu += part_sum[buf][w][RG + q][lane];
+            }
+            const float h = vg / (1.0f + expf(-vg)) * vu * R.weight[first + c16];
+            const uint32_t hi = f32_to_bf16(h);
+            const size_t at = (size_t)(2 * (first + c16)) * A.I + row + 4 * q + r4;
+            A.h[at] = (uint16_t)hi;
+            A.h[at + A.I] = (uint16_t)f32_to_bf16(h - bf16_lo(hi));
+        }
+        buf ^= 1;
+    };
+    stream<2 * RG, NTOK, 2, 4>(rsrc(A.s13, A.E * 2 * IB * HB * 4), rsrc(A.x, A.T * A.H * 2), ow, RG, A.H,
+                                    blockIdx.x, R.up.n * groups, gridDim.x, unit, sink);
 }
 
-// Second launch: 8 output columns per workgroup; its waves take the active
-// experts in turn (in pieces of the K range where there are fewer experts
-// than two per wave), and their sums are joined in wave order.
-__global__ __launch_bounds__(64 * DOWN_WAVES) void k_moe_down(MoeArgs A)
+// Second launch: 4 RG output columns per workgroup; its waves take the parts'
+// windows in turn, a few at a time, so that all workgroups move through the
+// experts together, and their sums are joined in wave order.
+constexpr int NWV = 8;
+template <int NTOK, int RG>
+__global__ __launch_bounds__(64 * NWV) void k_moe_down(MoeArgs A)
 {
     __shared__ Plan P;
-    __shared__ float acc[DOWN_WAVES][MAX_T][DOWN_ROWS];
+    __shared__ float sums[NWV][NTOK == 1 ? 1 : MAX_T][4 * RG];
     const uint32_t tid = threadIdx.x;
-    const uint32_t n = A.plan->nact;
-    for (uint32_t i = tid; i <= n; i += blockDim.x)
-        P.first[i] = A.plan->first[i];
-    for (uint32_t i = tid; i < n; i += blockDim.x)
-        P.expert[i] = A.plan->expert[i];
-    for (uint32_t i = tid; i < A.T * A.topk; i += blockDim.x)
+    // (read whole, up to the most there can be: its length is then no wait of
+    // its own, and what lies past it is not used)
+    const uint32_t n = A.plan->down.n, pairs = A.T * A.topk;
+    for (uint32_t i = tid; i <= pairs; i += blockDim.x)
+        P.down.first[i] = A.plan->down.first[i];
+    for (uint32_t i = tid; i < pairs; i += blockDim.x) {
+        P.down.expert[i] = A.plan->down.expert[i];
         P.token[i] = A.plan->token[i];
-    for (uint32_t i = tid; i < DOWN_WAVES * MAX_T * DOWN_ROWS; i += blockDim.x)
-        (&acc[0][0][0])[i] = 0.0f;
-    __syncthreads();
-    const uint32_t nw = (A.I + WIN - 1) / WIN, c0 = blockIdx.x * DOWN_ROWS;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    uint32_t pieces = n ? (2 * DOWN_WAVES + n - 1) / n : 1;
-    pieces = min(pieces, nw);
-    const uint32_t per = (nw + pieces - 1) / pieces;
-    for (uint32_t u = wave; u < n * pieces; u += DOWN_WAVES) {
-        const uint32_t slot = u / pieces, w0 = (u % pieces) * per, w1 = min(w0 + per, nw);
-        if (w0 >= w1)
-            continue;
-        const uint32_t e = __builtin_amdgcn_readfirstlane(P.expert[slot]);
-        const uint32_t first = __builtin_amdgcn_readfirstlane(P.first[slot]);
-        const uint32_t cnt = __builtin_amdgcn_readfirstlane(P.first[slot + 1]) - first;
-        if (cnt <= 4)
-            down<1>(A, P, e, first, cnt, c0, w0, w1, acc[wave]);
-        else if (cnt <= 8)
-            down<2>(A, P, e, first, cnt, c0, w0, w1, acc[wave]);
-        else
-            down<4>(A, P, e, first, cnt, c0, w0, w1, acc[wave]);
     }
+    for (uint32_t i = tid; i < sizeof(sums) / sizeof(float); i += blockDim.x)
+        (&sums[0][0][0])[i] = 0.0f;
     __syncthreads();
-    for (uint32_t i = tid; i < A.T * DOWN_ROWS; i += blockDim.x) {
-        const uint32_t t = i / DOWN_ROWS, c = i % DOWN_ROWS;
+    const uint32_t lane = tid & 63, r4 = lane & 3, c16 = lane >> 2;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t HB = A.H / 128, IB = A.I / 128, nw = (A.I + WIN - 1) / WIN, c0 = blockIdx.x * 4 * RG;
+    // windows to a unit: six, or fewer where that would leave waves without one
+    const uint32_t per = min(nw, max(1u, min(6u, n * nw / NWV)));
+    const uint32_t live = (nw + per - 1) / per;             // pieces that hold windows
+    uint32_t ow[RG];
+#pragma unroll
+    for (int q = 0; q < RG; ++q)
+        ow[q] = c0 + 4 * q < A.H ? (4 * q + r4) * A.I + 16 * c16 : NOROW;
+    auto unit = [&](uint32_t u) {
+        const uint32_t p = u / live;
+        const uint32_t e = __builtin_amdgcn_readfirstlane(P.down.expert[p]);
+        const uint32_t first = __builtin_amdgcn_readfirstlane(P.down.first[p]);
+        const uint32_t cnt = __builtin_amdgcn_readfirstlane(P.down.first[p + 1]) - first;
+        Unit d;
+        d.w = A.w2 + ((size_t)e * A.H + c0) * A.I;
+        d.s0 = (e * HB + c0 / 128) * IB * 4;
+        d.s1 = d.s0 + (c0 / 128 + 1 < HB ? IB * 4 : 0);
+        d.x = (2 * first + min(r4, 2 * cnt - 1)) * A.I * 2 + 32 * c16;
+        d.w0 = u % live * per;
+        d.w1 = min(d.w0 + per, nw);
+        return d;
+    };
+    auto sink = [&](uint32_t u, const f32x4 (&acc)[RG]) {
+        const uint32_t p = u / live;
+        const uint32_t first = __builtin_amdgcn_readfirstlane(P.down.first[p]);
+        const uint32_t cnt = __builtin_amdgcn_readfirstlane(P.down.first[p + 1]) - first;
+        // other lanes of this wave may have added to the same sums before
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int q = 0; q < RG; ++q) {
+            float v = sum_slices(acc[q][0] + acc[q][1]);
+            if (NTOK > 1) {
+                const float b = sum_slices(acc[q][2] + acc[q][3]);
+                v = c16 == 1 ? b : v;
+            }
+            if (c16 < cnt)
+                sums[wave][P.token[first + c16]][4 * q + r4] += v;   // only this wave's, one lane each
+        }
+    };
+    stream<RG, NTOK == 1 ? 2 : 4, RG <= 5 ? 3 : 2, 1>(rsrc(A.s2, A.E * HB * IB * 4), rsrc(A.h, A.T * A.topk * A.I * 4), ow,
+                                         (128 - c0 % 128) / 4, A.I, wave, n * live, NWV, unit, sink);
+    __syncthreads();
+    for (uint32_t i = tid; i < A.T * 4 * RG; i += blockDim.x) {
+        const uint32_t t = i / (4 * RG), c = i % (4 * RG);
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < DOWN_WAVES; ++w)
-            v += acc[w][t][c];
-        A.out[(size_t)t * A.H + c0 + c] = (uint16_t)f32_to_bf16(v);
+        for (int w = 0; w < NWV; ++w)
+            v += sums[w][t][c];
+        if (c0 + c < A.H)
+            A.out[(size_t)t * A.H + c0 + c] = (uint16_t)f32_to_bf16(v);
     }
+}
+
+template <int NTOK, int RG>
+void launch_down(const MoeArgs &A, hipStream_t st)
+{
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_moe_down<NTOK, RG>), dim3((A.H + 4 * RG - 1) / (4 * RG)), dim3(64 * NWV),
+                       0, st, A);
+}
+
+template <int NTOK>
+hipError_t launch_moe(const MoeArgs &A, hipStream_t st)
+{
+    const uint32_t cus = cu_count() ? cu_count() : 256;
+    // a workgroup for every unit that may come about, at most four per CU
+    constexpr int RGU = 2;
+    const uint64_t pairs = A.T * A.topk, parts = A.E + pairs / S_UP < pairs ? A.E + pairs / S_UP : pairs;
+    const uint64_t units = parts * (A.I / (4 * RGU));
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_moe_gate_up<NTOK, RGU>), dim3(units < 4 * cus ? (uint32_t)units : 4 * cus),
+                       dim3(256), 0, st, A);
+    count_launch();
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess)
+        return err;
+    // The columns dealt evenly over the CUs, at most 32 to a workgroup: with
+    // 16 columns each, 5120 columns took 120 us where 20 take 76 (the CUs with
+    // two workgroups decide).
+    const uint32_t rounds = (A.H + 32 * cus - 1) / (32 * cus);
+    switch ((A.H + 4 * cus * rounds - 1) / (4 * cus * rounds)) {
+    case 1: launch_down<NTOK, 1>(A, st); break;
+    case 2: launch_down<NTOK, 2>(A, st); break;
+    case 3: launch_down<NTOK, 3>(A, st); break;
+    case 4: launch_down<NTOK, 4>(A, st); break;
+    case 5: launch_down<NTOK, 5>(A, st); break;
+    case 6: launch_down<NTOK, 6>(A, st); break;
+    case 7: launch_down<NTOK, 7>(A, st); break;
+    default: launch_down<NTOK, 8>(A, st); break;
+    }
+    count_launch();
+    return hipGetLastError();
 }
 
 inline uint64_t planes_bytes(uint64_t T, uint64_t topk, uint64_t I) { return 4 * T * topk * I; }
@@ -529,23 +677,12 @@ hipError_t launch_moe_fp8(const uint16_t *x, const float *logits, const uint8_t 
                           const uint8_t *w2, const float *s2, void *work, uint16_t *out, uint32_t T,
                           uint32_t E, uint32_t topk, uint32_t H, uint32_t I, bool renorm, hipStream_t st)
 {
-    const uint64_t planes = planes_bytes(T, topk, I);
     uint8_t *const wk = (uint8_t *)work;
-    const MoeArgs A = {x, logits, w13, w2, s13, s2, (uint16_t *)wk, (uint16_t *)(wk + planes / 2),
-                       (Plan *)(wk + planes), out, T, E, topk, H, I, renorm};
-    // one wave per task while the tasks of all experts that may be chosen
-    // leave CUs idle, else four workgroups per CU walk them
-    const uint64_t slots = E < T * topk ? E : T * topk;
-    const uint64_t groups = (slots * (I / 4) + 3) / 4;
-    const uint32_t cus = cu_count(), cap = 4 * (cus ? cus : 256);
-    hipLaunchKernelGGL(k_moe_gate_up, dim3(groups < cap ? (uint32_t)groups : cap), dim3(256), 0, st, A);
-    count_launch();
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess)
-        return err;
-    hipLaunchKernelGGL(k_moe_down, dim3(H / DOWN_ROWS), dim3(64 * DOWN_WAVES), 0, st, A);
-    count_launch();
-    return hipGetLastError();
+    const MoeArgs A = {x, logits, w13, w2, s13, s2, (uint16_t *)wk, (Plan *)(wk + planes_bytes(T, topk, I)),
+                       out, T, E, topk, H, I, renorm};
+    if (T == 1)
+        return launch_moe<1>(A, st);
+    return launch_moe<4>(A, st);
 }
 
 } // namespace qp
