@@ -80,7 +80,7 @@ int moe_fp8_blockscale(const uint16_t *x, const float *router_logits, const uint
     if (t < 1 || t > QP_MOE_MAX_T || topk < 1 || topk > QP_MOE_MAX_TOPK || topk > e)
         return QP_ERR_RANGE;
     if (e > QP_MOE_MAX_E || h == 0 || i == 0 || h % 128 != 0 || i % 128 != 0 ||
-        !fits(2 * (uint64_t)i, h) || !fits(2 * (uint64_t)t, h) || !fits(2 * (uint64_t)t * topk, i))
+        !fits(2 * (uint64_t)i, h) || !fits(2 * (uint64_t)t, h) || !fits(4 * (uint64_t)t * topk, i))
         return QP_ERR_SHAPE;
     if (workspace_bytes < qp::moe_fp8_workspace(t, topk, i))
         return QP_ERR_SCRATCH;

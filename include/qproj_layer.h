@@ -102,11 +102,12 @@ int fp8_gemm_blockscale(const uint8_t *a, const float *a_scale, const uint8_t *w
  * topk others takes those, one with none gets a row of zeros.  Sums are F32
  * in a fixed order (no atomics); between the two launches an activation is
  * held to 2^-17 of itself.  Which tokens share a batch may change the order
- * of a token's sum.  Only the chosen experts' weights are read, once each.
+ * of a token's sum.  Only the chosen experts' weights are read, w13 once for
+ * every four tokens of an expert and w2 once for every two.
  * 1 <= t <= QP_MOE_MAX_T, 1 <= topk <= min(e, QP_MOE_MAX_TOPK) (else
  * QP_ERR_RANGE); e <= QP_MOE_MAX_E, h and i multiples of 128, 2*i*h < 2^31
- * (the limit is per expert: all of them together may be larger), else
- * QP_ERR_SHAPE.  workspace: caller-owned scratch of
+ * (the limit is per expert: all of them together may be larger) and
+ * 4*t*topk*i < 2^31, else QP_ERR_SHAPE.  workspace: caller-owned scratch of
  * moe_fp8_blockscale_workspace(t, topk, i) <= 4*t*topk*i + 65536 bytes (fewer
  * is QP_ERR_SCRATCH), its contents before and after the call unspecified.
  * ---------------------------------------------------------------------- */

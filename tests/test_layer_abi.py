@@ -113,6 +113,8 @@ def test_moe_refusals():
         assert _moe(**bad) == qp.QP_ERR_RANGE, bad
     for bad in (dict(e=513), dict(h=192), dict(i=64), dict(h=1 << 16, i=1 << 14)):
         assert _moe(**bad) == qp.QP_ERR_SHAPE, bad
+    # the rows between the two launches pass 2^31 bytes before an expert's weight does
+    assert _moe(t=16, topk=16, h=128, i=1 << 21, work=1 << 40) == qp.QP_ERR_SHAPE
     need = qp.moe_fp8_blockscale_workspace(4, 2, 256)
     assert 4 * 4 * 2 * 256 < need <= 4 * 4 * 2 * 256 + 65536
     assert _moe(work=need - 1) == qp.QP_ERR_SCRATCH
