@@ -7,6 +7,7 @@
 // encode.  A thread owns 16-byte chunks of 8 elements, neighbouring lanes
 // neighbouring chunks, so a 128-block is one DPP row of 16 lanes and a
 // 32-block one quad; block maxima never leave the registers.
+#include <algorithm>
 #include <type_traits>
 
 #include "qp_device.hpp"
@@ -197,6 +198,7 @@ struct RowArgs {
     float *s;
     float eps;
     uint32_t rows, k;
+    uint32_t parts;             // workgroups per row
 };
 
 // 1 / sqrt(mean + eps) from the block sums sm[0 .. nb): lane l adds blocks l,
@@ -211,101 +213,126 @@ __device__ __forceinline__ float rstd_of(const float *sm, uint32_t nb, uint32_t 
     return 1.0f / __builtin_sqrtf(sum64(v) / (float)k + eps);
 }
 
-// TPR threads per row (64: one wave, four rows per workgroup), CPL chunks per
-// thread, the row held in registers.
-template <bool NORM, int FMT, int TPR, int CPL>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_row_quant(RowArgs A)
+// Scales and codes of a thread's chunks; m is its maximum (row format).
+template <int FMT, int CPL, class V>
+__device__ __forceinline__ void finish(const RowArgs &A, uint32_t row, uint32_t first, uint32_t T,
+                                       float m, float *tops, V value)
 {
-    constexpr int RPG = TPR == 64 ? 4 : 1, NB = TPR * CPL / 16;
-    __shared__ float sums[RPG][NB];
-    __shared__ float tops[TPR / 64];
-    const int sub = RPG == 1 ? 0 : threadIdx.x >> 6;
-    const uint32_t row = blockIdx.x * RPG + sub;
-    if (RPG > 1 && row >= A.rows)
-        return;                          // the whole wave; waves share nothing
-    const uint32_t t = threadIdx.x & (TPR - 1), nch = A.k / 8;
-    const size_t at = (size_t)row * A.k;
-    float y[CPL][8];
-    if (NORM) {
-        u32x4 h[CPL], r[CPL];
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-            const uint32_t c = t + TPR * j;
-            h[j] = r[j] = (u32x4){0, 0, 0, 0};
-            if (c < nch) {
-                h[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(A.x + at + 8 * (size_t)c));
-                if (A.res)
-                    r[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(A.res + at + 8 * (size_t)c));
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-            const uint32_t c = t + TPR * j;
-            if (A.res) {
-                h[j] = add_bf16(h[j], r[j]);
-                if (c < nch)
-                    *reinterpret_cast<u32x4 *>(A.res_out + at + 8 * (size_t)c) = h[j];
-            }
-            const float s = sum16(ssq8(h[j]));
-            if ((t & 15) == 0)
-                sums[sub][c >> 4] = s;   // c / 16 < NB; past the row: 0
-        }
-        if (TPR > 64)
-            __syncthreads();
-        else
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        const float rstd = rstd_of(sums[sub], NB, A.k, A.eps);
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-            const uint32_t c = t + TPR * j;
-            u32x4 w = (u32x4){0, 0, 0, 0};
-            if (c < nch)
-                w = *reinterpret_cast<const u32x4 *>(A.w + 8 * (size_t)c);
-            norm8(h[j], w, rstd, y[j]);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-            const uint32_t c = t + TPR * j;
-            u32x4 g = (u32x4){0, 0, 0, 0}, u = g;
-            if (c < nch) {
-                g = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(A.x + 2 * at + 8 * (size_t)c));
-                u = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(A.x + 2 * at + A.k + 8 * (size_t)c));
-            }
-            silu8(g, u, y[j]);
-        }
-    }
+    const uint32_t nch = A.k / 8;
     float sc = 0.0f;
     if (FMT == FMT_ROW) {
-        float m = 0.0f;
-#pragma unroll
-        for (int j = 0; j < CPL; ++j)
-            m = __builtin_fmaxf(m, amax8(y[j]));
         m = max64(m);
-        if (TPR > 64) {
-            if ((threadIdx.x & 63) == 0)
-                tops[threadIdx.x >> 6] = m;
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < TPR / 64; ++i)
-                m = __builtin_fmaxf(m, tops[i]);
-        }
+        if ((threadIdx.x & 63) == 0)
+            tops[threadIdx.x >> 6] = m;
+        __syncthreads();
+        for (uint32_t i = 0; i < T / 64; ++i)
+            m = __builtin_fmaxf(m, tops[i]);
         sc = scale_of<FMT>(m);
-        if (t == 0)
+        if (first == 0)
             A.s[row] = sc;
     }
     float *sr = A.s + (size_t)row * scales_per_row<FMT>(A.k);
 #pragma unroll
     for (int j = 0; j < CPL; ++j) {
-        const uint32_t c = t + TPR * j;
-        emit8<FMT>(y[j], sc, c, c < nch, A.q + at, sr);
+        const uint32_t c = first + T * j;
+        float y[8];
+        value(j, y);
+        emit8<FMT>(y, sc, c, c < nch, A.q + (size_t)row * A.k, sr);
     }
 }
 
-// Rows longer than the registers hold: 1024 threads walk the row once per
-// step (sum, for the row format the maximum, encode) and recompute y.  With a
-// residual, h is read back from residual_out: each thread reads only what it
-// wrote itself.
+// The row held in registers, CPL chunks per thread: chunk t + T j of the row,
+// T threads, a workgroup.  An activation whose scales are per block has no sum
+// over its row, so its rows are also cut into `parts` pieces of T CPL chunks.
+//
+// Bound by HBM: what counts is that every load of the row is in flight before
+// the first use and that no lane idles, so T follows the row (a fixed 256
+// threads of 8 chunks left 5 of 8 idle at k = 5120: 8192 x 5120 took 60 us).
+// 8192 x 5120 (norm, residual): 49 us, 6.0 TB/s; 4096 x 17408 (activation):
+// 57 us, 6.3 TB/s; one row of 5120: 2.9 us in a graph, of which an empty
+// kernel is about 2.
+template <bool NORM, int FMT, int CPL>
+__global__ __launch_bounds__(1024) void k_row_quant(RowArgs A)
+{
+    constexpr bool ALONE = !NORM && FMT != FMT_ROW;       // no sum over the row
+    __shared__ float sm[NORM ? 1024 * CPL / 16 : 1];
+    __shared__ float tops[16];
+    const uint32_t T = blockDim.x, t = threadIdx.x, nch = A.k / 8;
+    const uint32_t row = ALONE ? blockIdx.x / A.parts : blockIdx.x;
+    const uint32_t first = t + (ALONE ? blockIdx.x % A.parts * (T * CPL) : 0);
+    const size_t at = (size_t)row * A.k;
+    const u32x4 z = (u32x4){0, 0, 0, 0};
+    u32x4 h[CPL], w[CPL];                // norm: h and the weight; activation: g and u
+    if (NORM) {
+        u32x4 r[CPL];
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+            const uint32_t c = first + T * j;
+            h[j] = r[j] = w[j] = z;
+            if (c < nch) {
+                h[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(A.x + at + 8 * (size_t)c));
+                if (A.res)
+                    r[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(A.res + at + 8 * (size_t)c));
+                w[j] = *reinterpret_cast<const u32x4 *>(A.w + 8 * (size_t)c);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+            const uint32_t c = first + T * j;
+            if (A.res) {
+                h[j] = add_bf16(h[j], r[j]);
+                if (c < nch)
+                    __builtin_nontemporal_store(h[j], reinterpret_cast<u32x4 *>(A.res_out + at + 8 * (size_t)c));
+            }
+            const float s = sum16(ssq8(h[j]));
+            if ((t & 15) == 0)
+                sm[c >> 4] = s;          // c / 16 < T CPL / 16; past the row: 0
+        }
+        __syncthreads();
+        const float rstd = rstd_of(sm, T * CPL / 16, A.k, A.eps);
+        float m = 0.0f, y[8];
+        if (FMT == FMT_ROW) {
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) {
+                norm8(h[j], w[j], rstd, y);
+                m = __builtin_fmaxf(m, amax8(y));
+            }
+        }
+        finish<FMT, CPL>(A, row, first, T, m, tops,
+                               [&](int j, float *v) { norm8(h[j], w[j], rstd, v); });
+    } else {
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+            const uint32_t c = first + T * j;
+            h[j] = w[j] = z;
+            if (c < nch) {
+                h[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(A.x + 2 * at + 8 * (size_t)c));
+                w[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(A.x + 2 * at + A.k + 8 * (size_t)c));
+            }
+        }
+        if (FMT == FMT_ROW) {
+            float y[CPL][8], m = 0.0f;
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) {
+                silu8(h[j], w[j], y[j]);
+                m = __builtin_fmaxf(m, amax8(y[j]));
+            }
+            finish<FMT, CPL>(A, row, first, T, m, tops, [&](int j, float *v) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] = y[j][i];
+            });
+        } else {
+            finish<FMT, CPL>(A, row, first, T, 0.0f, tops,
+                                   [&](int j, float *v) { silu8(h[j], w[j], v); });
+        }
+    }
+}
+
+// Rows of more than 32768 values, which the registers do not hold (and which
+// are not cut): 1024 threads walk the row once per step (sum, for the row
+// format the maximum, encode) and recompute y.  With a residual, h is read
+// back from residual_out: each thread reads only what it wrote itself.
 template <bool NORM, int FMT>
 __global__ __launch_bounds__(1024) void k_row_quant_long(RowArgs A)
 {
@@ -373,24 +400,43 @@ __global__ __launch_bounds__(1024) void k_row_quant_long(RowArgs A)
     }
 }
 
-template <bool NORM, int FMT, int TPR, int CPL>
-void launch_row(const RowArgs &A, hipStream_t st)
+template <bool NORM, int FMT, int CPL>
+void launch_row(RowArgs A, uint32_t threads, hipStream_t st)
 {
-    constexpr int RPG = TPR == 64 ? 4 : 1;
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_row_quant<NORM, FMT, TPR, CPL>), dim3((A.rows + RPG - 1) / RPG),
-                       dim3(TPR < 256 ? 256 : TPR), 0, st, A);
+    A.parts = (A.k / 8 + threads * CPL - 1) / (threads * CPL);   // 1 unless the row may be cut
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_row_quant<NORM, FMT, CPL>), dim3(A.rows * A.parts), dim3(threads), 0,
+                       st, A);
 }
 
+// Chunks per thread: one while the whole grid is resident at once (8192
+// waves): then the call is latency, and a second chunk only adds to it (16 x
+// 5120, norm: 3.5 against 3.9 us; 16 x 17408, activation per 128: 2.5 against
+// 3.0).  Two beyond (8192 x 5120: 49.2 against 55.7; 4 chunks 51.3; 4096 x
+// 17408: 56.7 against 59.5; 4 chunks 59.9), more only for rows that 1024
+// threads do not cover with two; 8 would spill.
 template <bool NORM, int FMT>
 hipError_t launch_fmt(const RowArgs &A, hipStream_t st)
 {
-    const uint32_t nch = A.k / 8;
-    if (nch <= 256 * 2)
-        launch_row<NORM, FMT, 256, 2>(A, st);
-    else if (nch <= 256 * 8)
-        launch_row<NORM, FMT, 256, 8>(A, st);
-    else
-        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_row_quant_long<NORM, FMT>), dim3(A.rows), dim3(1024), 0, st, A);
+    const uint32_t nch = A.k / 8, waves = (nch + 63) / 64;
+    constexpr bool cut = !NORM && FMT != FMT_ROW;
+    uint32_t cpl = waves > 1 && (uint64_t)A.rows * waves > 8192 ? 2 : 1;
+    if constexpr (cut) {
+        const uint32_t threads = std::min((waves + cpl - 1) / cpl * 64, 256u);
+        cpl == 1 ? launch_row<NORM, FMT, 1>(A, threads, st) : launch_row<NORM, FMT, 2>(A, threads, st);
+    } else {
+        cpl = std::max(cpl, (nch + 1023) / 1024);
+        const uint32_t threads = (waves + cpl - 1) / cpl * 64;
+        if (cpl == 1)
+            launch_row<NORM, FMT, 1>(A, threads, st);
+        else if (cpl == 2)
+            launch_row<NORM, FMT, 2>(A, threads, st);
+        else if (cpl == 3)
+            launch_row<NORM, FMT, 3>(A, threads, st);
+        else if (cpl == 4)
+            launch_row<NORM, FMT, 4>(A, threads, st);
+        else
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_row_quant_long<NORM, FMT>), dim3(A.rows), dim3(1024), 0, st, A);
+    }
     count_launch();
     return hipGetLastError();
 }
@@ -409,13 +455,13 @@ hipError_t launch_rmsnorm_residual_quant(const uint16_t *x, const uint16_t *res,
                                          float eps, int fmt, void *q, float *s, uint16_t *res_out,
                                          uint32_t rows, uint32_t k, hipStream_t st)
 {
-    return launch_any<true>({x, res, w, res_out, (uint8_t *)q, s, eps, rows, k}, fmt, st);
+    return launch_any<true>({x, res, w, res_out, (uint8_t *)q, s, eps, rows, k, 1}, fmt, st);
 }
 
 hipError_t launch_silu_mul_quant(const uint16_t *gate_up, int fmt, void *q, float *s, uint32_t rows,
                                  uint32_t k, hipStream_t st)
 {
-    return launch_any<false>({gate_up, nullptr, nullptr, nullptr, (uint8_t *)q, s, 0.0f, rows, k}, fmt, st);
+    return launch_any<false>({gate_up, nullptr, nullptr, nullptr, (uint8_t *)q, s, 0.0f, rows, k, 1}, fmt, st);
 }
 
 } // namespace qp
