@@ -41,6 +41,7 @@ QP_NVFP4 = 4
 QP_ACT_FP8_ROW = 0
 QP_ACT_FP8_BLOCK128 = 1
 QP_ACT_INT8_BLOCK32 = 2
+QP_ACT_BF16 = 16
 
 QP_TILES_BANDED = 0
 QP_TILES_MFAST = 1
@@ -417,7 +418,7 @@ def w4a16_gemv(x, w_packed, w_e4m3, scale2, out, stream=None):
 
 
 def _need_act(q, scale, fmt, rows, k):
-    """Check the output pair of an 8-bit activation format (qp_act_format)."""
+    """Check the output pair of an activation format (qp_act_format)."""
     if fmt == QP_ACT_FP8_BLOCK128:
         _need(q, "q", U8, (rows, k))
         _need(scale, "scale", F32, (rows, (k + 127) // 128))
@@ -427,13 +428,18 @@ def _need_act(q, scale, fmt, rows, k):
     elif fmt == QP_ACT_INT8_BLOCK32:
         _need(q, "q", I8, (rows, k))
         _need(scale, "scale", F32, (rows, k // 32))
+    elif fmt == QP_ACT_BF16:
+        _need(q, "q", BF16, (rows, k))
+        if scale is not None:
+            raise ValueError("scale: QP_ACT_BF16 has none")
 
 
 def rmsnorm_residual_quant(x, residual, weight, eps, fmt, q, scale, residual_out=None,
                            stream=None):
-    """q, scale = the 8-bit form `fmt` (QP_ACT_*) of the RMS norm of
+    """q, scale = the form `fmt` (QP_ACT_*) of the RMS norm of
     h = bf16(x + residual), which is written to residual_out (it may be
-    residual itself).  residual None: h = x, and no residual_out."""
+    residual itself).  residual None: h = x, and no residual_out.
+    QP_ACT_BF16: q is BF16 and scale None."""
     rows, k = x.shape
     _need(x, "x", BF16, (rows, k))
     _need(weight, "weight", BF16, (k,))
@@ -444,19 +450,21 @@ def rmsnorm_residual_quant(x, residual, weight, eps, fmt, q, scale, residual_out
         _need(residual_out, "residual_out", BF16, (rows, k))
     _check("rmsnorm_residual_quant", lib().rmsnorm_residual_quant(
         _ptr(x), None if residual is None else _ptr(residual), _ptr(weight), float(eps),
-        int(fmt), _ptr(q), _ptr(scale), None if residual_out is None else _ptr(residual_out),
+        int(fmt), _ptr(q), None if scale is None else _ptr(scale), None if residual_out is None else _ptr(residual_out),
         rows, k, _stream(stream)))
 
 
 def silu_mul_quant(gate_up, fmt, q, scale, stream=None):
-    """q, scale = the 8-bit form `fmt` (QP_ACT_*) of silu(gate) * up, where a
-    row of gate_up holds its gate values and then its up values."""
+    """q, scale = the form `fmt` (QP_ACT_*) of silu(gate) * up, where a row of
+    gate_up holds its gate values and then its up values.  QP_ACT_BF16: q is
+    BF16 and scale None."""
     rows, k2 = gate_up.shape
     k = k2 // 2
     _need(gate_up, "gate_up", BF16, (rows, 2 * k))
     _need_act(q, scale, fmt, rows, k)
     _check("silu_mul_quant", lib().silu_mul_quant(
-        _ptr(gate_up), int(fmt), _ptr(q), _ptr(scale), rows, k, _stream(stream)))
+        _ptr(gate_up), int(fmt), _ptr(q), None if scale is None else _ptr(scale), rows, k,
+        _stream(stream)))
 
 
 def fp8_gemm_blockscale(a, a_scale, w, block_scale, out, stream=None):

@@ -14,7 +14,7 @@ namespace {
 // blocks), and rows * wide elements (the widest tensor) below 2^31.
 int check_act(int fmt, uint32_t rows, uint32_t k, uint64_t wide)
 {
-    if (fmt != QP_ACT_FP8_ROW && fmt != QP_ACT_FP8_BLOCK128 && fmt != QP_ACT_INT8_BLOCK32)
+    if (fmt != QP_ACT_FP8_ROW && fmt != QP_ACT_FP8_BLOCK128 && fmt != QP_ACT_INT8_BLOCK32 && fmt != QP_ACT_BF16)
         return QP_ERR_FORMAT;
     if (rows == 0 || k == 0 || k > QP_LAYER_MAX_K || k % (fmt == QP_ACT_INT8_BLOCK32 ? 32 : 16) != 0 ||
         !fits(rows, wide))
@@ -30,7 +30,7 @@ int rmsnorm_residual_quant(const uint16_t *x, const uint16_t *residual, const ui
                            float eps, int fmt, void *q, float *scale, uint16_t *residual_out,
                            uint32_t rows, uint32_t k, void *stream)
 {
-    if (int e = check_ptrs({x, weight, q, scale}))
+    if (int e = check_ptrs({x, weight, q, fmt == QP_ACT_BF16 ? q : scale}))
         return e;
     if ((residual == nullptr) != (residual_out == nullptr))
         return QP_ERR_NULL;
@@ -47,7 +47,7 @@ int rmsnorm_residual_quant(const uint16_t *x, const uint16_t *residual, const ui
 int silu_mul_quant(const uint16_t *gate_up, int fmt, void *q, float *scale, uint32_t rows,
                    uint32_t k, void *stream)
 {
-    if (int e = check_ptrs({gate_up, q, scale}))
+    if (int e = check_ptrs({gate_up, q, fmt == QP_ACT_BF16 ? q : scale}))
         return e;
     if (int e = check_act(fmt, rows, k, 2 * (uint64_t)k))
         return e;

@@ -1,6 +1,6 @@
-// layer_quant.hip -- the two operators that feed a quantized product:
-// residual addition + RMS norm, and the gated activation silu(g) * u, each
-// with an 8-bit output (E4M3 per row or per 128, int8 per 32) in the same pass.
+// layer_quant.hip -- the two operators that feed a product: residual addition
+// + RMS norm, and the gated activation silu(g) * u, each with an 8-bit output
+// (E4M3 per row or per 128, int8 per 32) in the same pass, or a BF16 one.
 //
 // Both stream HBM (7 and 5 bytes per element), so every input byte is read
 // once: a row's values stay in registers between its reductions and the
@@ -16,7 +16,7 @@
 namespace qp {
 namespace {
 
-enum { FMT_ROW = 0, FMT_BLOCK128 = 1, FMT_INT8 = 2 };
+enum { FMT_ROW = 0, FMT_BLOCK128 = 1, FMT_INT8 = 2, FMT_BF16 = 16 };
 
 template <int CTRL>
 __device__ __forceinline__ float dpp_mov(float v)
@@ -165,15 +165,25 @@ __device__ __forceinline__ u32x2 encode8(const float *y, float sc)
 template <int FMT>
 __device__ __forceinline__ uint32_t scales_per_row(uint32_t k)
 {
-    return FMT == FMT_ROW ? 1 : FMT == FMT_BLOCK128 ? (k + 127) / 128 : k / 32;
+    return FMT == FMT_ROW ? 1 : FMT == FMT_BLOCK128 ? (k + 127) / 128 : FMT == FMT_INT8 ? k / 32 : 0;
 }
 
 // Quantize and store chunk c of a row: block formats find their own scale,
-// the row format gets it.  Every lane of the wave calls this (DPP).
+// the row format gets it, BF16 has none.  Every lane of the wave calls this
+// (DPP).
 template <int FMT>
 __device__ __forceinline__ void emit8(const float *y, float row_scale, uint32_t c, bool live,
                                       uint8_t *__restrict__ qr, float *__restrict__ sr)
 {
+    if (FMT == FMT_BF16) {
+        u32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = pk_bf16(y[2 * i], y[2 * i + 1]);
+        if (live)
+            __builtin_nontemporal_store(o, reinterpret_cast<u32x4 *>(qr + (size_t)c * 16));
+        return;
+    }
     float sc = row_scale;
     if (FMT == FMT_BLOCK128)
         sc = scale_of<FMT>(max16(amax8(y)));
@@ -232,12 +242,13 @@ __device__ __forceinline__ void finish(const RowArgs &A, uint32_t row, uint32_t 
             A.s[row] = sc;
     }
     float *sr = A.s + (size_t)row * scales_per_row<FMT>(A.k);
+    uint8_t *qr = A.q + (size_t)row * A.k * (FMT == FMT_BF16 ? 2 : 1);
 #pragma unroll
     for (int j = 0; j < CPL; ++j) {
         const uint32_t c = first + T * j;
         float y[8];
         value(j, y);
-        emit8<FMT>(y, sc, c, c < nch, A.q + (size_t)row * A.k, sr);
+        emit8<FMT>(y, sc, c, c < nch, qr, sr);
     }
 }
 
@@ -393,10 +404,11 @@ __global__ __launch_bounds__(1024) void k_row_quant_long(RowArgs A)
             A.s[row] = sc;
     }
     float *sr = A.s + (size_t)row * scales_per_row<FMT>(A.k);
+    uint8_t *qr = A.q + at * (FMT == FMT_BF16 ? 2 : 1);
     for (uint32_t i = 0; i < steps; ++i) {
         const uint32_t c = t + 1024 * i;
         value(c, y);
-        emit8<FMT>(y, sc, c, c < nch, A.q + at, sr);
+        emit8<FMT>(y, sc, c, c < nch, qr, sr);
     }
 }
 
@@ -446,7 +458,8 @@ hipError_t launch_any(const RowArgs &A, int fmt, hipStream_t st)
 {
     return fmt == FMT_ROW        ? launch_fmt<NORM, FMT_ROW>(A, st)
            : fmt == FMT_BLOCK128 ? launch_fmt<NORM, FMT_BLOCK128>(A, st)
-                                 : launch_fmt<NORM, FMT_INT8>(A, st);
+           : fmt == FMT_INT8     ? launch_fmt<NORM, FMT_INT8>(A, st)
+                                 : launch_fmt<NORM, FMT_BF16>(A, st);
 }
 
 } // namespace

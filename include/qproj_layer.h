@@ -20,30 +20,33 @@
 extern "C" {
 #endif
 
-/* 8-bit activation formats, each the operand of one GEMM of the library:
+/* Activation formats, each the operand of products of the library:
  *   QP_ACT_FP8_ROW      E4M3 [rows,k], F32 scale [rows]: fp8_gemm_rowscale;
  *   QP_ACT_FP8_BLOCK128 E4M3 [rows,k], F32 scale [rows, ceil(k/128)] (the last
  *                       block is shorter where 128 does not divide k):
  *                       fp8_gemm_blockscale;
  *   QP_ACT_INT8_BLOCK32 int8 [rows,k], F32 scale [rows, k/32]:
- *                       int8_gemm_blockscaled.
+ *                       int8_gemm_blockscaled;
+ *   QP_ACT_BF16         BF16 [rows,k], no scale (the pointer is not used and
+ *                       may be NULL): the GEMVs, moe_fp8_blockscale.
  * Rounding as in qproj.h: scale = amax/448 (127), one IEEE division of the
  * F32 value by the stored scale, round to nearest even, a zero scale encoded
- * as scale 0 with +0 codes. */
+ * as scale 0 with +0 codes; BF16 rounded to nearest even. */
 enum qp_act_format {
     QP_ACT_FP8_ROW = 0,
     QP_ACT_FP8_BLOCK128 = 1,
-    QP_ACT_INT8_BLOCK32 = 2
+    QP_ACT_INT8_BLOCK32 = 2,
+    QP_ACT_BF16 = 16
 };
 
-/* Longest row of the two quantizing operators below. */
+/* Longest row of the two operators below. */
 #define QP_LAYER_MAX_K (1u << 18)
 
 /* ------------------------------------------------------------------------
- * Residual addition, RMS norm and 8-bit quantizer in one pass:
+ * Residual addition, RMS norm and quantizer in one pass:
  *   h = bf16(x + residual)                       (written to residual_out)
  *   y = h * (1 / sqrt(mean(h^2) + eps)) * weight      in F32, never stored
- *   q, scale = y quantized per `fmt`.
+ *   q, scale = y in the form `fmt`.
  *   x [rows,k], residual [rows,k] and weight [k] BF16; q [rows,k];
  *   residual_out [rows,k] BF16.
  * residual and residual_out are both given or both NULL (then h = x);
@@ -61,9 +64,9 @@ int rmsnorm_residual_quant(const uint16_t *x, const uint16_t *residual,
                            uint32_t k, void *stream);
 
 /* ------------------------------------------------------------------------
- * Gated activation and 8-bit quantizer in one pass:
+ * Gated activation and quantizer in one pass:
  *   y = silu(gate) * up,  silu(g) = g / (1 + exp(-g))      in F32
- *   q, scale = y quantized per `fmt`.
+ *   q, scale = y in the form `fmt`.
  *   gate_up [rows, 2k] BF16: a row's k gate values, then its k up values (the
  *   output of one product with the gate and up weights stacked);
  *   q [rows,k].  Sizes and errors as above, and rows * 2k < 2^31.

@@ -95,6 +95,13 @@ def test_silu_refusals():
     assert call(BLOCK, 1 << 20, 1 << 10) == qp.QP_ERR_SHAPE        # gate_up holds 2^31 elements
 
 
+def test_only_the_bf16_form_has_no_scale():
+    for fmt, code in ((qp.QP_ACT_BF16, qp.QP_ERR_SHAPE), (BLOCK, qp.QP_ERR_NULL), (ROW, qp.QP_ERR_NULL),
+                      (INT8, qp.QP_ERR_NULL)):
+        assert L.rmsnorm_residual_quant(A, None, B, 1e-6, fmt, A, None, None, 4, 8, None) == code
+        assert L.silu_mul_quant(A, fmt, B, None, 4, 8, None) == code
+
+
 def test_gemm_refusals():
     call = lambda m, n, k: L.fp8_gemm_blockscale(A, B, A, B, A, m, n, k, None)  # noqa: E731
     for k in (8, 24, 100):
