@@ -89,23 +89,29 @@ __device__ __forceinline__ float add_halves(u32x2 h)
     return __uint_as_float(h[0]) + __uint_as_float(h[1]);
 }
 
-__device__ __forceinline__ uint32_t wave_max_u(uint32_t v)
+__device__ __forceinline__ uint32_t row_max_u(uint32_t v)
 {
     v = max(v, dpp_u<0xB1>(v));                 // pairs, quads, eights, sixteens
     v = max(v, dpp_u<0x4E>(v));
     v = max(v, dpp_u<0x141>(v));
-    v = max(v, dpp_u<0x140>(v));
-    u32x2 h = swap16(v);
+    return max(v, dpp_u<0x140>(v));
+}
+__device__ __forceinline__ uint32_t wave_max_u(uint32_t v)
+{
+    u32x2 h = swap16(row_max_u(v));
     h = swap32(max(h[0], h[1]));
     return max(h[0], h[1]);
 }
-__device__ __forceinline__ float wave_sum_f(float v)
+__device__ __forceinline__ float row_sum_f(float v)
 {
     v += dpp_f<0xB1>(v);
     v += dpp_f<0x4E>(v);
     v += dpp_f<0x141>(v);
-    v += dpp_f<0x140>(v);
-    return add_halves(swap32(__float_as_uint(add_halves(swap16(__float_as_uint(v))))));
+    return v + dpp_f<0x140>(v);
+}
+__device__ __forceinline__ float wave_sum_f(float v)
+{
+    return add_halves(swap32(__float_as_uint(add_halves(swap16(__float_as_uint(row_sum_f(v)))))));
 }
 // Sum of v over the lanes up to and including this one.
 __device__ __forceinline__ uint32_t wave_scan_u(uint32_t v)
@@ -117,6 +123,24 @@ __device__ __forceinline__ uint32_t wave_scan_u(uint32_t v)
     // the last lane of rows 0 and 2 to rows 1 and 3, then lane 31 to the upper half
     v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);
     return v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, 0x00020000);
+}
+// (weights: nontemporal, they are read once)
+__device__ __forceinline__ u32x4 load16_nt(__amdgpu_buffer_rsrc_t r, uint32_t off)
+{
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 2));
+}
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off)
+{
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+}
+__device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t r, uint32_t off)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0));
 }
 
 // Monotone integer key of a logit; 0 only for -inf and for what is no expert.
@@ -140,46 +164,48 @@ struct Routing {
     uint32_t mask[MAX_E], base[MAX_E];          // tokens of an expert; its first pair
 };
 
-// The topk of one token by a wave: lane l holds experts l*EPL .. l*EPL+EPL-1,
-// so among equal keys the lowest lane, and in it the lowest slot, is the
-// lowest expert.  Lane i < n (returned) gets the i-th chosen expert and its
-// weight.
+// Logits past the table's end (bytes) read as zeros and take key 0: a load
+// under a condition of its own would be waited for before the next is issued.
+__device__ __forceinline__ uint32_t load_key(__amdgpu_buffer_rsrc_t logits, uint32_t at, bool live)
+{
+    const uint32_t k = key_of(load4(logits, 4 * at) + 0.0f);    // (-0 ties with +0)
+    return live ? k : 0u;
+}
+
+// The topk of a single token by a wave: lane l holds experts l*EPL .. , so
+// among equal keys the lowest lane, and in it the lowest slot, is the lowest
+// expert.  Lane i < n (returned) gets the i-th chosen expert and its weight.
 template <int EPL>
-__device__ __forceinline__ uint32_t choose(const float *__restrict__ row, uint32_t E, uint32_t topk,
-                                           bool renorm, uint32_t &my_e, float &my_w)
+__device__ __forceinline__ uint32_t choose_one(__amdgpu_buffer_rsrc_t logits, uint32_t E, uint32_t topk,
+                                               bool renorm, uint32_t &my_e, float &my_w)
 {
     const uint32_t lane = threadIdx.x & 63;
     uint32_t key[EPL], had[EPL];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        const uint32_t e = lane * EPL + j;
-        key[j] = had[j] = e < E ? key_of(row[e] + 0.0f) : 0u;   // (-0 ties with +0)
-    }
-    uint32_t n = 0, my_k = 0, top_k = 0;
-    my_e = 0;
-    for (uint32_t i = 0; i < topk; ++i) {
+    for (int j = 0; j < EPL; ++j)
+        key[j] = had[j] = load_key(logits, lane * EPL + j, lane * EPL + j < E);
+    uint32_t n = 0, e = 0, k = 0, top_k = 0;
+    while (n < topk) {
         uint32_t b = key[0], bj = 0;
 #pragma unroll
-        for (int j = 1; j < EPL; ++j)
-            if (key[j] > b) {
-                b = key[j];
-                bj = j;
-            }
-        const uint32_t m = wave_max_u(b);
+        for (int j = 1; j < EPL; ++j) {
+            bj = key[j] > b ? j : bj;
+            b = max(b, key[j]);
+        }
+        const uint32_t m = __builtin_amdgcn_readfirstlane(wave_max_u(b));
         if (m == 0)
-            break;                              // uniform: nothing left to choose
+            break;                              // nothing left to choose
         const uint32_t who = (uint32_t)__builtin_ctzll(__ballot(b == m));
         const uint32_t j = (uint32_t)__builtin_amdgcn_readlane((int)bj, (int)who);
-        if (i == 0)
-            top_k = m;
-        my_e = lane == i ? who * EPL + j : my_e;
-        my_k = lane == i ? m : my_k;
+        top_k = n == 0 ? m : top_k;
+        e = lane == n ? who * EPL + j : e;
+        k = lane == n ? m : k;
 #pragma unroll
         for (int q = 0; q < EPL; ++q)
-            key[q] = lane == who && q == (int)j ? 0u : key[q];
-        n = i + 1;
+            key[q] = lane * EPL + q == who * EPL + j ? 0u : key[q];
+        ++n;
     }
-    const float top = value_of(top_k), w = lane < n ? expf(value_of(my_k) - top) : 0.0f;
+    const float top = value_of(top_k), w = lane < n ? expf(value_of(k) - top) : 0.0f;
     float total = w;
     if (!renorm) {
         total = 0.0f;
@@ -187,17 +213,53 @@ __device__ __forceinline__ uint32_t choose(const float *__restrict__ row, uint32
         for (int j = 0; j < EPL; ++j)
             total += had[j] ? expf(value_of(had[j]) - top) : 0.0f;
     }
+    my_e = e;
     my_w = w / wave_sum_f(total);
     return n;
 }
 
-__device__ __forceinline__ uint32_t choose_any(const float *__restrict__ row, uint32_t E, uint32_t topk,
-                                               bool renorm, uint32_t &my_e, float &my_w)
+// The topk of four tokens by a wave, one to each row of 16 lanes: lane l of
+// the row holds experts l, l + 16, ..., and of equal keys the lowest expert is
+// found by a second reduction.  Lane i < n (of the row) gets the row's i-th.
+template <int EPL>
+__device__ __forceinline__ uint32_t choose_four(__amdgpu_buffer_rsrc_t logits, uint32_t t, uint32_t T,
+                                                uint32_t E, uint32_t topk, bool renorm, uint32_t &my_e,
+                                                float &my_w)
 {
-    return E <= 64    ? choose<1>(row, E, topk, renorm, my_e, my_w)
-           : E <= 128 ? choose<2>(row, E, topk, renorm, my_e, my_w)
-           : E <= 256 ? choose<4>(row, E, topk, renorm, my_e, my_w)
-                      : choose<8>(row, E, topk, renorm, my_e, my_w);
+    const uint32_t l = threadIdx.x & 15;
+    uint32_t key[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+        key[j] = load_key(logits, t * E + l + 16 * j, t < T && l + 16 * j < E);
+    uint32_t n = 0, e = 0, k = 0, top_k = 0;
+    float rest = 0.0f;
+    for (uint32_t i = 0; i < topk; ++i) {
+        uint32_t b = key[0], bj = 0;
+#pragma unroll
+        for (int j = 1; j < EPL; ++j) {
+            bj = key[j] > b ? j : bj;
+            b = max(b, key[j]);
+        }
+        const uint32_t m = row_max_u(b);
+        const uint32_t won = ~row_max_u(b == m ? ~(l + 16 * bj) : 0u);
+        if (i == 0) {
+            top_k = m;
+            if (!renorm)
+#pragma unroll
+                for (int j = 0; j < EPL; ++j)
+                    rest += key[j] ? expf(value_of(key[j]) - value_of(m)) : 0.0f;
+        }
+        e = l == i ? won : e;
+        k = l == i ? m : k;
+        n += m != 0;                            // once nothing is left, m stays 0
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            key[j] = l + 16 * j == won ? 0u : key[j];
+    }
+    const float w = l < n ? expf(value_of(k) - value_of(top_k)) : 0.0f;
+    my_e = e;
+    my_w = w / row_sum_f(renorm ? w : rest);
+    return n;
 }
 
 // One token: its experts are the parts and the pairs, in the order chosen.
@@ -208,7 +270,11 @@ __device__ void route_one(const float *__restrict__ logits, uint32_t E, uint32_t
     const uint32_t lane = threadIdx.x & 63;
     uint32_t e;
     float w;
-    const uint32_t n = choose_any(logits, E, topk, renorm, e, w);
+    const __amdgpu_buffer_rsrc_t lg = rsrc(logits, E * 4);
+    const uint32_t n = E <= 64    ? choose_one<1>(lg, E, topk, renorm, e, w)
+                       : E <= 128 ? choose_one<2>(lg, E, topk, renorm, e, w)
+                       : E <= 256 ? choose_one<4>(lg, E, topk, renorm, e, w)
+                                  : choose_one<8>(lg, E, topk, renorm, e, w);
     if (lane < n) {
         R.up.expert[lane] = R.plan.down.expert[lane] = e;
         R.weight[lane] = w;
@@ -225,21 +291,28 @@ __device__ void route_one(const float *__restrict__ logits, uint32_t E, uint32_t
 __device__ void route(const float *__restrict__ logits, uint32_t T, uint32_t E, uint32_t topk,
                       bool renorm, Routing &R)
 {
-    const uint32_t tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, nw = blockDim.x >> 6;
+    const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const uint32_t mine_t = 4 * wave + (lane >> 4), l16 = lane & 15;
     for (uint32_t e = tid; e < MAX_E; e += blockDim.x)
         R.mask[e] = 0;
     __syncthreads();
-    for (uint32_t t = wave; t < T; t += nw) {
-        uint32_t e;
+    if (4 * wave < T) {
+        uint32_t e, n;
         float w;
-        const uint32_t n = choose_any(logits + (size_t)t * E, E, topk, renorm, e, w);
-        if (lane < n) {
-            R.sel_e[t][lane] = e;
-            R.sel_w[t][lane] = w;
-            atomicOr(&R.mask[e], 1u << t);      // an OR: order does not matter
+        const __amdgpu_buffer_rsrc_t lg = rsrc(logits, T * E * 4);
+        n = E <= 64    ? choose_four<4>(lg, mine_t, T, E, topk, renorm, e, w)
+            : E <= 128 ? choose_four<8>(lg, mine_t, T, E, topk, renorm, e, w)
+            : E <= 256 ? choose_four<16>(lg, mine_t, T, E, topk, renorm, e, w)
+                       : choose_four<32>(lg, mine_t, T, E, topk, renorm, e, w);
+        if (mine_t < T) {
+            if (l16 < n) {
+                R.sel_e[mine_t][l16] = e;
+                R.sel_w[mine_t][l16] = w;
+                atomicOr(&R.mask[e], 1u << mine_t); // an OR: order does not matter
+            }
+            if (l16 == 0)
+                R.nsel[mine_t] = n;
         }
-        if (lane == 0)
-            R.nsel[t] = n;
     }
     __syncthreads();
     if (wave < 2) {
@@ -282,24 +355,6 @@ __device__ void route(const float *__restrict__ logits, uint32_t T, uint32_t E, 
         }
     }
     __syncthreads();
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, uint32_t bytes)
-{
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, 0x00020000);
-}
-// (weights: nontemporal, they are read once)
-__device__ __forceinline__ u32x4 load16_nt(__amdgpu_buffer_rsrc_t r, uint32_t off)
-{
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 2));
-}
-__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off)
-{
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
-}
-__device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t r, uint32_t off)
-{
-    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0));
 }
 
 // Four E4M3 codes as BF16, exactly.
