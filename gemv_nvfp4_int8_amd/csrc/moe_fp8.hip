@@ -174,49 +174,62 @@ __device__ __forceinline__ uint32_t load_key(__amdgpu_buffer_rsrc_t logits, uint
 
 // The topk of a single token by a wave: lane l holds experts l*EPL .. , so
 // among equal keys the lowest lane, and in it the lowest slot, is the lowest
-// expert.  Lane i < n (returned) gets the i-th chosen expert and its weight.
+// expert.  Lane i < n holds the i-th chosen expert.
 template <int EPL>
-__device__ __forceinline__ uint32_t choose_one(__amdgpu_buffer_rsrc_t logits, uint32_t E, uint32_t topk,
-                                               bool renorm, uint32_t &my_e, float &my_w)
-{
-    const uint32_t lane = threadIdx.x & 63;
-    uint32_t key[EPL], had[EPL];
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-        key[j] = had[j] = load_key(logits, lane * EPL + j, lane * EPL + j < E);
-    uint32_t n = 0, e = 0, k = 0, top_k = 0;
-    while (n < topk) {
-        uint32_t b = key[0], bj = 0;
-#pragma unroll
-        for (int j = 1; j < EPL; ++j) {
-            bj = key[j] > b ? j : bj;
-            b = max(b, key[j]);
-        }
-        const uint32_t m = __builtin_amdgcn_readfirstlane(wave_max_u(b));
-        if (m == 0)
-            break;                              // nothing left to choose
-        const uint32_t who = (uint32_t)__builtin_ctzll(__ballot(b == m));
-        const uint32_t j = (uint32_t)__builtin_amdgcn_readlane((int)bj, (int)who);
-        top_k = n == 0 ? m : top_k;
-        e = lane == n ? who * EPL + j : e;
-        k = lane == n ? m : k;
-#pragma unroll
-        for (int q = 0; q < EPL; ++q)
-            key[q] = lane * EPL + q == who * EPL + j ? 0u : key[q];
-        ++n;
-    }
-    const float top = value_of(top_k), w = lane < n ? expf(value_of(k) - top) : 0.0f;
-    float total = w;
-    if (!renorm) {
-        total = 0.0f;
+struct ChooseOne {
+    uint32_t key[EPL], had[EPL], n, e, k, top_k;
+    bool done;                                  // nothing left to choose
+
+    __device__ __forceinline__ ChooseOne(__amdgpu_buffer_rsrc_t logits, uint32_t E)
+        : n(0), e(0), k(0), top_k(0), done(false)
+    {
+        const uint32_t lane = threadIdx.x & 63;
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
-            total += had[j] ? expf(value_of(had[j]) - top) : 0.0f;
+            key[j] = had[j] = load_key(logits, lane * EPL + j, lane * EPL + j < E);
     }
-    my_e = e;
-    my_w = w / wave_sum_f(total);
-    return n;
-}
+    // choose until there are `want`
+    __device__ __forceinline__ void until(uint32_t want)
+    {
+        const uint32_t lane = threadIdx.x & 63;
+        while (n < want && !done) {
+            uint32_t b = key[0], bj = 0;
+#pragma unroll
+            for (int j = 1; j < EPL; ++j) {
+                bj = key[j] > b ? j : bj;
+                b = max(b, key[j]);
+            }
+            const uint32_t m = __builtin_amdgcn_readfirstlane(wave_max_u(b));
+            if (m == 0) {
+                done = true;
+                break;
+            }
+            const uint32_t who = (uint32_t)__builtin_ctzll(__ballot(b == m));
+            const uint32_t j = (uint32_t)__builtin_amdgcn_readlane((int)bj, (int)who);
+            top_k = n == 0 ? m : top_k;
+            e = lane == n ? who * EPL + j : e;
+            k = lane == n ? m : k;
+#pragma unroll
+            for (int q = 0; q < EPL; ++q)
+                key[q] = lane * EPL + q == who * EPL + j ? 0u : key[q];
+            ++n;
+        }
+    }
+    // this lane's weight, when all are chosen
+    __device__ __forceinline__ float weight(bool renorm) const
+    {
+        const uint32_t lane = threadIdx.x & 63;
+        const float top = value_of(top_k), w = lane < n ? expf(value_of(k) - top) : 0.0f;
+        float total = w;
+        if (!renorm) {
+            total = 0.0f;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j)
+                total += had[j] ? expf(value_of(had[j]) - top) : 0.0f;
+        }
+        return w / wave_sum_f(total);
+    }
+};
 
 // The topk of four tokens by a wave, one to each row of 16 lanes: lane l of
 // the row holds experts l, l + 16, ..., and of equal keys the lowest expert is
@@ -263,27 +276,18 @@ __device__ __forceinline__ uint32_t choose_four(__amdgpu_buffer_rsrc_t logits, u
 }
 
 // One token: its experts are the parts and the pairs, in the order chosen.
-// Every wave finds and writes the same, so none waits for another.
-__device__ void route_one(const float *__restrict__ logits, uint32_t E, uint32_t topk, bool renorm,
-                          Routing &R)
+// Every wave finds and writes the same, so none waits for another; how many
+// there are so far is each wave's own (R.up.n and R.plan.down.n are not used).
+template <int EPL>
+__device__ __forceinline__ void publish(const ChooseOne<EPL> &c, Routing &R)
 {
     const uint32_t lane = threadIdx.x & 63;
-    uint32_t e;
-    float w;
-    const __amdgpu_buffer_rsrc_t lg = rsrc(logits, E * 4);
-    const uint32_t n = E <= 64    ? choose_one<1>(lg, E, topk, renorm, e, w)
-                       : E <= 128 ? choose_one<2>(lg, E, topk, renorm, e, w)
-                       : E <= 256 ? choose_one<4>(lg, E, topk, renorm, e, w)
-                                  : choose_one<8>(lg, E, topk, renorm, e, w);
-    if (lane < n) {
-        R.up.expert[lane] = R.plan.down.expert[lane] = e;
-        R.weight[lane] = w;
+    if (lane < c.n) {
+        R.up.expert[lane] = R.plan.down.expert[lane] = c.e;
         R.plan.token[lane] = 0;
     }
-    if (lane <= n)
+    if (lane <= c.n)
         R.up.first[lane] = R.plan.down.first[lane] = lane;
-    if (lane == 0)
-        R.up.n = R.plan.down.n = n;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
@@ -413,11 +417,13 @@ struct Unit {
 // units' ends: RW groups of 4 weight rows (lane l's row l % 4, chunk l / 4 at
 // base + ow[g]); unit(u) describes one; sink(u, acc) takes its sums acc[g][r]:
 // the lane's K slice of its row of group g with operand row r (r < NR).
-// Groups below split scale by the grid row s0, the others by s1.
-template <int RW, int NR, int D, int WS, class GetUnit, class Sink>
+// Groups below split scale by the grid row s0, the others by s1.  started() runs
+// once the first D windows are on their way and may change n above those.
+template <int RW, int NR, int D, int WS, class Started, class GetUnit, class Sink>
 __device__ __forceinline__ void stream(__amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t rx,
                                        const uint32_t (&ow)[RW], uint32_t split, uint32_t kn,
-                                       uint32_t u0, uint32_t n, uint32_t step, GetUnit unit, Sink sink)
+                                       uint32_t u0, const uint32_t &n, uint32_t step, Started started, GetUnit unit,
+                                       Sink sink)
 {
     const uint32_t lane = threadIdx.x & 63, c16 = lane >> 2;
     struct Stage {
@@ -468,6 +474,7 @@ __device__ __forceinline__ void stream(__amdgpu_buffer_rsrc_t rs, __amdgpu_buffe
 #pragma unroll
     for (int d = 0; d < D; ++d)
         fetch(st[d]);
+    started();
     while (uu < n) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
@@ -512,29 +519,56 @@ __device__ __forceinline__ void stream(__amdgpu_buffer_rsrc_t rs, __amdgpu_buffe
 // and join their sums through LDS in wave order: the rows of a unit are one
 // contiguous block (two, gate and up) that is read at one time, which HBM
 // serves better than as many separate walks along K.
-template <int NTOK, int RG>
+//
+// A single token's experts are known one after another, the last some 1.5 us
+// after the first, so a workgroup starts on its unit as soon as that unit's
+// expert is chosen and ends the choice under its loads (EPL: of ChooseOne; 0
+// for more tokens).
+template <int NTOK, int RG, int EPL>
 __global__ __launch_bounds__(256) void k_moe_gate_up(MoeArgs A)
 {
     __shared__ Routing R;
     __shared__ float part_sum[2][4][2 * RG][4 * NTOK];
-    if (NTOK == 1)
-        route_one(A.logits, A.E, A.topk, A.renorm != 0, R);
-    else
+    constexpr int D = 2;                        // windows in flight
+    const uint32_t groups = A.I / (4 * RG);
+    uint32_t units = 0;
+    ChooseOne<EPL ? EPL : 1> one(rsrc(A.logits, A.E * 4), EPL ? A.E : 0);
+    if (EPL) {
+        // the experts of this workgroup's first D + 1 units
+        uint32_t last = blockIdx.x;
+        for (int d = 0; d < D; ++d)
+            last += last + gridDim.x < A.topk * groups ? gridDim.x : 0;
+        one.until(min(last / groups + 1, A.topk));
+        publish(one, R);
+    } else {
         route(A.logits, A.T, A.E, A.topk, A.renorm != 0, R);
-    if (blockIdx.x == 0) {
-        const uint32_t n = R.plan.down.n, pairs = R.plan.down.first[n];
-        for (uint32_t i = threadIdx.x; i <= n; i += blockDim.x)
-            A.plan->down.first[i] = R.plan.down.first[i];
-        for (uint32_t i = threadIdx.x; i < n; i += blockDim.x)
-            A.plan->down.expert[i] = R.plan.down.expert[i];
-        for (uint32_t i = threadIdx.x; i < pairs; i += blockDim.x)
-            A.plan->token[i] = R.plan.token[i];
-        if (threadIdx.x == 0)
-            A.plan->down.n = n;
     }
+    units = (EPL ? one.n : R.up.n) * groups;
+    auto started = [&]() {
+        if (EPL) {
+            one.until(A.topk);
+            publish(one, R);
+            const float w = one.weight(A.renorm != 0);
+            if ((threadIdx.x & 63) < one.n)
+                R.weight[threadIdx.x & 63] = w;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            units = one.n * groups;
+        }
+        if (blockIdx.x == 0) {
+            const uint32_t n = EPL ? one.n : R.plan.down.n, pairs = R.plan.down.first[n];
+            for (uint32_t i = threadIdx.x; i <= n; i += blockDim.x)
+                A.plan->down.first[i] = R.plan.down.first[i];
+            for (uint32_t i = threadIdx.x; i < n; i += blockDim.x)
+                A.plan->down.expert[i] = R.plan.down.expert[i];
+            for (uint32_t i = threadIdx.x; i < pairs; i += blockDim.x)
+                A.plan->token[i] = R.plan.token[i];
+            if (threadIdx.x == 0)
+                A.plan->down.n = n;
+        }
+    };
     const uint32_t lane = threadIdx.x & 63, r4 = lane & 3, c16 = lane >> 2;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t HB = A.H / 128, IB = A.I / 128, groups = A.I / (4 * RG);
+    const uint32_t HB = A.H / 128, IB = A.I / 128;
     const uint32_t nwq = ((A.H + WIN - 1) / WIN + 3) / 4;   // windows of each wave
     uint32_t ow[2 * RG];
 #pragma unroll
@@ -598,8 +632,8 @@ __global__ __launch_bounds__(256) void k_moe_gate_up(MoeArgs A)
         }
         buf ^= 1;
     };
-    stream<2 * RG, NTOK, 2, 4>(rsrc(A.s13, A.E * 2 * IB * HB * 4), rsrc(A.x, A.T * A.H * 2), ow, RG, A.H,
-                                    blockIdx.x, R.up.n * groups, gridDim.x, unit, sink);
+    stream<2 * RG, NTOK, D, 4>(rsrc(A.s13, A.E * 2 * IB * HB * 4), rsrc(A.x, A.T * A.H * 2), ow, RG, A.H,
+                               blockIdx.x, units, gridDim.x, started, unit, sink);
 }
 
 // Second launch: 4 RG output columns per workgroup; its waves take the parts'
@@ -665,8 +699,9 @@ __global__ __launch_bounds__(64 * NWV) void k_moe_down(MoeArgs A)
                 sums[wave][P.token[first + c16]][4 * q + r4] += v;   // only this wave's, one lane each
         }
     };
-    stream<RG, NTOK == 1 ? 2 : 4, RG <= 5 ? 3 : 2, 1>(rsrc(A.s2, A.E * HB * IB * 4), rsrc(A.h, A.T * A.topk * A.I * 4), ow,
-                                         (128 - c0 % 128) / 4, A.I, wave, n * live, NWV, unit, sink);
+    stream<RG, NTOK == 1 ? 2 : 4, RG <= 5 ? 3 : 2, 1>(
+        rsrc(A.s2, A.E * HB * IB * 4), rsrc(A.h, A.T * A.topk * A.I * 4), ow, (128 - c0 % 128) / 4, A.I, wave,
+        n * live, NWV, [] {}, unit, sink);
     __syncthreads();
     for (uint32_t i = tid; i < A.T * 4 * RG; i += blockDim.x) {
         const uint32_t t = i / (4 * RG), c = i % (4 * RG);
@@ -694,8 +729,19 @@ hipError_t launch_moe(const MoeArgs &A, hipStream_t st)
     constexpr int RGU = 2;
     const uint64_t pairs = A.T * A.topk, parts = A.E + pairs / S_UP < pairs ? A.E + pairs / S_UP : pairs;
     const uint64_t units = parts * (A.I / (4 * RGU));
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_moe_gate_up<NTOK, RGU>), dim3(units < 4 * cus ? (uint32_t)units : 4 * cus),
-                       dim3(256), 0, st, A);
+    const dim3 grid(units < 4 * cus ? (uint32_t)units : 4 * cus);
+    if constexpr (NTOK == 1) {
+        if (A.E <= 64)
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_moe_gate_up<1, RGU, 1>), grid, dim3(256), 0, st, A);
+        else if (A.E <= 128)
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_moe_gate_up<1, RGU, 2>), grid, dim3(256), 0, st, A);
+        else if (A.E <= 256)
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_moe_gate_up<1, RGU, 4>), grid, dim3(256), 0, st, A);
+        else
+            hipLaunchKernelGGL(HIP_KERNEL_NAME(k_moe_gate_up<1, RGU, 8>), grid, dim3(256), 0, st, A);
+    } else {
+        hipLaunchKernelGGL(HIP_KERNEL_NAME(k_moe_gate_up<NTOK, RGU, 0>), grid, dim3(256), 0, st, A);
+    }
     count_launch();
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess)
