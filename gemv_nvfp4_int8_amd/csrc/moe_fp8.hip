@@ -46,9 +46,9 @@ constexpr uint32_t OOB = 0x80000000u;
 constexpr uint32_t NOROW = 0x7FFFFF00u;
 
 // A part is an expert and at most S of its tokens: an expert with more has
-// several parts, side by side, whose waves read its weights together.  An MFMA
-// takes four operand rows: four tokens of x, or two of h (hi and lo).
-constexpr uint32_t S_UP = 4, S_DOWN = 2;
+// several parts, which each read its weights.  An MFMA takes four operand rows:
+// four tokens of x, or two of h (hi and lo).  A part has one such group (S = 4
+// and 2) or two (S = 8 and 4), see launch_moe_fp8.
 
 struct Parts {
     uint32_t n;
@@ -291,7 +291,9 @@ __device__ __forceinline__ void publish(const ChooseOne<EPL> &c, Routing &R)
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
-// Fill R (every thread of the workgroup calls this; ends with a barrier).
+// Fill R with parts of at most SU tokens for the first product and SD for the
+// second (every thread of the workgroup calls this; ends with a barrier).
+template <uint32_t SU, uint32_t SD>
 __device__ void route(const float *__restrict__ logits, uint32_t T, uint32_t E, uint32_t topk,
                       bool renorm, Routing &R)
 {
@@ -324,7 +326,7 @@ __device__ void route(const float *__restrict__ logits, uint32_t T, uint32_t E, 
         // experts 8l .. 8l+7; parts (high half) and pairs (low half) before it
         // by an inclusive scan over the lanes
         Parts &P = wave ? R.plan.down : R.up;
-        const uint32_t S = wave ? S_DOWN : S_UP;
+        const uint32_t S = wave ? SD : SU;
         uint32_t mk[8], mine = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -384,12 +386,54 @@ __device__ __forceinline__ f32x4 window(const s16x4 *w, const u32x4 *x, f32x4 p)
     return p;
 }
 
-// The sum over the 16 K slices (lanes of equal l % 4), in every lane.
-__device__ __forceinline__ float sum_slices(float v)
+// v of lane l ^ 4, by two moves that write alternate quads.
+__device__ __forceinline__ float xor4(float v)
 {
-    v += dpp_f<0x128>(v);                       // rotate by 8 and by 4 in a row of 16
-    v += dpp_f<0x124>(v);
-    return add_halves(swap32(__float_as_uint(add_halves(swap16(__float_as_uint(v))))));
+    const int u = __float_as_int(v);
+    const int down = __builtin_amdgcn_update_dpp(0, u, 0x104, 0xF, 0x5, false);
+    return __int_as_float(__builtin_amdgcn_update_dpp(down, u, 0x114, 0xF, 0xA, false));
+}
+// v of lane l ^ 8: a rotation by half a row.
+__device__ __forceinline__ float xor8(float v) { return dpp_f<0x128>(v); }
+
+// Sums of N values (a power of two) over the 16 K slices, lanes of equal l % 4.
+// A lane ends with the sums of values first .. first + max(N / 16, 1) - 1 in
+// v[0] .. (first is returned), which costs 2 to 3 instructions a pair instead
+// of a whole butterfly for each; N < 16: lanes share them, and `owner` is true
+// in one of those.
+template <int N>
+__device__ __forceinline__ uint32_t sum_slices(float *v, bool &owner)
+{
+    const uint32_t lane = threadIdx.x & 63;
+    constexpr int N1 = N > 1 ? N / 2 : 1, N2 = N1 > 1 ? N1 / 2 : 1, N3 = N2 > 1 ? N2 / 2 : 1;
+    const bool b5 = lane & 32, b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
+#pragma unroll
+    for (int i = 0; i < N1; ++i) {              // (halves exchanged: the lower lanes' sum, the upper lanes')
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[N > 1 ? i + N1 : 0]),
+                                                        false, false);
+        v[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < N2; ++i) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[N1 > 1 ? i + N2 : 0]),
+                                                        false, false);
+        v[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < N3; ++i) {
+        const float keep = N2 > 1 && b3 ? v[N2 > 1 ? i + N3 : 0] : v[i],
+                    give = N2 > 1 && !b3 ? v[N2 > 1 ? i + N3 : 0] : v[i];
+        v[i] = keep + xor8(give);
+    }
+    constexpr int N4 = N3 > 1 ? N3 / 2 : 1;
+#pragma unroll
+    for (int i = 0; i < N4; ++i) {
+        const float keep = N3 > 1 && b2 ? v[N3 > 1 ? i + N4 : 0] : v[i],
+                    give = N3 > 1 && !b2 ? v[N3 > 1 ? i + N4 : 0] : v[i];
+        v[i] = keep + xor4(give);
+    }
+    owner = (N > 1 || !b5) && (N1 > 1 || !b4) && (N2 > 1 || !b3) && (N3 > 1 || !b2);
+    return (N > 1 && b5 ? N1 : 0) + (N1 > 1 && b4 ? N2 : 0) + (N2 > 1 && b3 ? N3 : 0) + (N3 > 1 && b2 ? N4 : 0);
 }
 
 struct MoeArgs {
@@ -406,20 +450,22 @@ struct MoeArgs {
 // One wave's work: a run of units, each a few weight rows of one expert times
 // the operand rows of one part, over windows w0, w0 + WS, ... < w1 (past the K
 // range: zeros).
+template <int NG>
 struct Unit {
     const uint8_t *w;                           // the weight rows' common base
     uint32_t s0, s1;                            // byte offsets of their rows in the scale grid
-    uint32_t x;                                 // per lane: operand row l % 4 at chunk l / 4
+    uint32_t x[NG];                             // per lane and group: operand row l % 4 at chunk l / 4
     uint32_t w0, w1;
 };
 
 // Walk the units u0, u0 + step, ... < n with D windows in flight, across the
 // units' ends: RW groups of 4 weight rows (lane l's row l % 4, chunk l / 4 at
-// base + ow[g]); unit(u) describes one; sink(u, acc) takes its sums acc[g][r]:
-// the lane's K slice of its row of group g with operand row r (r < NR).
+// base + ow[g]); unit(u) describes one; sink(u, acc) takes its sums
+// acc[g][n][r]: the lane's K slice of its row of weight group g with row r < NR
+// of operand group n < NG.
 // Groups below split scale by the grid row s0, the others by s1.  started() runs
 // once the first D windows are on their way and may change n above those.
-template <int RW, int NR, int D, int WS, class Started, class GetUnit, class Sink>
+template <int RW, int NG, int NR, int D, int WS, class Started, class GetUnit, class Sink>
 __device__ __forceinline__ void stream(__amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t rx,
                                        const uint32_t (&ow)[RW], uint32_t split, uint32_t kn,
                                        uint32_t u0, const uint32_t &n, uint32_t step, Started started, GetUnit unit,
@@ -427,13 +473,12 @@ __device__ __forceinline__ void stream(__amdgpu_buffer_rsrc_t rs, __amdgpu_buffe
 {
     const uint32_t lane = threadIdx.x & 63, c16 = lane >> 2;
     struct Stage {
-        u32x4 w[RW], x[2];
+        u32x4 w[RW], x[NG][2];
         float s0, s1;
     } st[D];
     // the next window to fetch: window fw of unit fu, described by f
     uint32_t fu = u0, fw = 0;
-    Unit f = {};
-    f.w1 = 0;
+    Unit<NG> f = {};
     if (fu < n) {
         f = unit(fu);
         fw = f.w0;
@@ -451,8 +496,11 @@ __device__ __forceinline__ void stream(__amdgpu_buffer_rsrc_t rs, __amdgpu_buffe
 #pragma unroll
         for (int g = 0; g < RW; ++g)
             s.w[g] = load16_nt(rw, ow[g] + dw);
-        s.x[0] = load16(rx, f.x + dx);
-        s.x[1] = load16(rx, f.x + dx + 16);
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            s.x[n][0] = load16(rx, f.x[n] + dx);
+            s.x[n][1] = load16(rx, f.x[n] + dx + 16);
+        }
         s.s0 = load4(rs, f.s0 + ds);
         s.s1 = load4(rs, f.s1 + ds);
         fw += WS;
@@ -465,10 +513,10 @@ __device__ __forceinline__ void stream(__amdgpu_buffer_rsrc_t rs, __amdgpu_buffe
             }
         }
     };
-    f32x4 acc[RW] = {};
+    f32x4 acc[RW][NG] = {};
     uint32_t uu = u0, left = 0;
     if (uu < n) {
-        const Unit u = unit(uu);
+        const Unit<NG> u = unit(uu);
         left = (u.w1 - u.w0 + WS - 1) / WS;
     }
 #pragma unroll
@@ -485,15 +533,18 @@ __device__ __forceinline__ void stream(__amdgpu_buffer_rsrc_t rs, __amdgpu_buffe
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     v[i] = fp8x4_bf16(s.w[g][i]);
-                const f32x4 p = window(v, s.x, (f32x4){0, 0, 0, 0});
                 const float sg = (uint32_t)g < split ? s.s0 : s.s1;
 #pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    float v = __builtin_fmaf(p[r], sg, acc[g][r]);
-                    // pinned here: sunk past the refill, it would make the
-                    // compiler copy (and so wait for) the registers being loaded
-                    asm volatile("" : "+v"(v));
-                    acc[g][r] = v;
+                for (int n = 0; n < NG; ++n) {
+                    const f32x4 p = window(v, s.x[n], (f32x4){0, 0, 0, 0});
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+                        float a = __builtin_fmaf(p[r], sg, acc[g][n][r]);
+                        // pinned here: sunk past the refill, it would make the
+                        // compiler copy (and so wait for) the registers being loaded
+                        asm volatile("" : "+v"(a));
+                        acc[g][n][r] = a;
+                    }
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -503,10 +554,12 @@ __device__ __forceinline__ void stream(__amdgpu_buffer_rsrc_t rs, __amdgpu_buffe
                 sink(uu, acc);
 #pragma unroll
                 for (int g = 0; g < RW; ++g)
-                    acc[g] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+                    for (int n = 0; n < NG; ++n)
+                        acc[g][n] = (f32x4){0, 0, 0, 0};
                 uu += step;
                 if (uu < n) {
-                    const Unit u = unit(uu);
+                    const Unit<NG> u = unit(uu);
                     left = (u.w1 - u.w0 + WS - 1) / WS;
                 }
             }
@@ -514,7 +567,8 @@ __device__ __forceinline__ void stream(__amdgpu_buffer_rsrc_t rs, __amdgpu_buffe
     }
 }
 
-// First launch: route, then units of RG * (4 + 4) gate and up rows of a part.
+// First launch: route, then units of RG * (4 + 4) gate and up rows of a part
+// (NTOK tokens at most; in the second launch a part has NTOK / 2).
 // A workgroup's four waves share a unit, wave w taking windows w, w + 4, ...,
 // and join their sums through LDS in wave order: the rows of a unit are one
 // contiguous block (two, gate and up) that is read at one time, which HBM
@@ -529,7 +583,7 @@ __global__ __launch_bounds__(256) void k_moe_gate_up(MoeArgs A)
 {
     __shared__ Routing R;
     __shared__ float part_sum[2][4][2 * RG][4 * NTOK];
-    constexpr int D = 2;                        // windows in flight
+    constexpr int D = 2, NG = (NTOK + 3) / 4;   // windows in flight, operand groups
     const uint32_t groups = A.I / (4 * RG);
     uint32_t units = 0;
     ChooseOne<EPL ? EPL : 1> one(rsrc(A.logits, A.E * 4), EPL ? A.E : 0);
@@ -541,7 +595,7 @@ __global__ __launch_bounds__(256) void k_moe_gate_up(MoeArgs A)
         one.until(min(last / groups + 1, A.topk));
         publish(one, R);
     } else {
-        route(A.logits, A.T, A.E, A.topk, A.renorm != 0, R);
+        route<NTOK, NTOK / 2>(A.logits, A.T, A.E, A.topk, A.renorm != 0, R);
     }
     units = (EPL ? one.n : R.up.n) * groups;
     auto started = [&]() {
@@ -587,31 +641,32 @@ __global__ __launch_bounds__(256) void k_moe_gate_up(MoeArgs A)
     auto unit = [&](uint32_t u) {
         uint32_t e, first, cnt;
         const uint32_t row = part(u, e, first, cnt);
-        Unit d;
+        Unit<NG> d;
         d.w = A.w13 + ((size_t)e * 2 * A.I + row) * A.H;
         d.s0 = (e * 2 * IB + row / 128) * HB * 4;
         d.s1 = d.s0 + IB * HB * 4;
-        d.x = R.plan.token[first + min(r4, cnt - 1)] * A.H * 2 + 32 * c16;
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+            d.x[n] = n && 4u * n >= cnt ? NOROW : R.plan.token[first + min(4 * n + r4, cnt - 1)] * A.H * 2 + 32 * c16;
         d.w0 = wave;
         d.w1 = wave + 4 * nwq;
         return d;
     };
     uint32_t buf = 0;
-    auto sink = [&](uint32_t u, const f32x4 (&acc)[2 * RG]) {
+    auto sink = [&](uint32_t u, const f32x4 (&acc)[2 * RG][NG]) {
         uint32_t e, first, cnt;
         const uint32_t row = part(u, e, first, cnt);
-        // lane l takes token l / 4 of weight row l % 4
+        // value NTOK q + t, of weight row l % 4: in its place as lane 4 t + l % 4 below
+        float v[2 * RG * NTOK];
 #pragma unroll
-        for (int q = 0; q < 2 * RG; ++q) {
-            float v = 0.0f;
+        for (int i = 0; i < 2 * RG * NTOK; ++i)
+            v[i] = acc[i / NTOK][i % NTOK / 4][i % 4 * (NTOK > 1)];
+        bool owner;
+        const uint32_t first_v = sum_slices<2 * RG * NTOK>(v, owner);
+        if (owner)
 #pragma unroll
-            for (int t = 0; t < NTOK; ++t) {
-                const float s = sum_slices(acc[q][t]);
-                v = c16 == (uint32_t)t ? s : v;
-            }
-            if (c16 < NTOK)
-                part_sum[buf][wave][q][lane] = v;
-        }
+            for (int i = 0; i < (2 * RG * NTOK + 15) / 16; ++i)
+                (&part_sum[buf][wave][0][0])[4 * (first_v + i) + r4] = v[i];
         // (the next unit takes the other buffer, so one barrier is enough)
         __syncthreads();
 #pragma unroll
@@ -632,7 +687,7 @@ __global__ __launch_bounds__(256) void k_moe_gate_up(MoeArgs A)
         }
         buf ^= 1;
     };
-    stream<2 * RG, NTOK, D, 4>(rsrc(A.s13, A.E * 2 * IB * HB * 4), rsrc(A.x, A.T * A.H * 2), ow, RG, A.H,
+    stream<2 * RG, NG, NTOK == 1 ? 1 : 4, D, 4>(rsrc(A.s13, A.E * 2 * IB * HB * 4), rsrc(A.x, A.T * A.H * 2), ow, RG, A.H,
                                blockIdx.x, units, gridDim.x, started, unit, sink);
 }
 
@@ -640,6 +695,7 @@ __global__ __launch_bounds__(256) void k_moe_gate_up(MoeArgs A)
 // windows in turn, a few at a time, so that all workgroups move through the
 // experts together, and their sums are joined in wave order.
 constexpr int NWV = 8;
+constexpr int pow2(int n) { return n <= 1 ? 1 : 2 * pow2((n + 1) / 2); }
 template <int NTOK, int RG>
 __global__ __launch_bounds__(64 * NWV) void k_moe_down(MoeArgs A)
 {
@@ -668,38 +724,47 @@ __global__ __launch_bounds__(64 * NWV) void k_moe_down(MoeArgs A)
 #pragma unroll
     for (int q = 0; q < RG; ++q)
         ow[q] = c0 + 4 * q < A.H ? (4 * q + r4) * A.I + 16 * c16 : NOROW;
+    constexpr int NG = (2 * NTOK + 7) / 8;      // operand groups: two rows for each of NTOK / 2 tokens
     auto unit = [&](uint32_t u) {
         const uint32_t p = u / live;
         const uint32_t e = __builtin_amdgcn_readfirstlane(P.down.expert[p]);
         const uint32_t first = __builtin_amdgcn_readfirstlane(P.down.first[p]);
         const uint32_t cnt = __builtin_amdgcn_readfirstlane(P.down.first[p + 1]) - first;
-        Unit d;
+        Unit<NG> d;
         d.w = A.w2 + ((size_t)e * A.H + c0) * A.I;
         d.s0 = (e * HB + c0 / 128) * IB * 4;
         d.s1 = d.s0 + (c0 / 128 + 1 < HB ? IB * 4 : 0);
-        d.x = (2 * first + min(r4, 2 * cnt - 1)) * A.I * 2 + 32 * c16;
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+            d.x[n] = n && 2u * n >= cnt ? NOROW : (2 * first + min(4 * n + r4, 2 * cnt - 1)) * A.I * 2 + 32 * c16;
         d.w0 = u % live * per;
         d.w1 = min(d.w0 + per, nw);
         return d;
     };
-    auto sink = [&](uint32_t u, const f32x4 (&acc)[RG]) {
+    auto sink = [&](uint32_t u, const f32x4 (&acc)[RG][NG]) {
         const uint32_t p = u / live;
         const uint32_t first = __builtin_amdgcn_readfirstlane(P.down.first[p]);
         const uint32_t cnt = __builtin_amdgcn_readfirstlane(P.down.first[p + 1]) - first;
         // other lanes of this wave may have added to the same sums before
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        // value PER q + i: token i of the part, weight row 4 q + l % 4
+        constexpr int PER = NTOK == 1 ? 1 : NTOK / 2, NV = pow2(RG * PER);
+        float v[NV];
 #pragma unroll
-        for (int q = 0; q < RG; ++q) {
-            float v = sum_slices(acc[q][0] + acc[q][1]);
-            if (NTOK > 1) {
-                const float b = sum_slices(acc[q][2] + acc[q][3]);
-                v = c16 == 1 ? b : v;
-            }
-            if (c16 < cnt)
-                sums[wave][P.token[first + c16]][4 * q + r4] += v;   // only this wave's, one lane each
+        for (int i = 0; i < NV; ++i) {
+            const int q = i / PER, s = i % PER;
+            v[i] = q < RG ? acc[q < RG ? q : 0][s / 2][s % 2 * 2] + acc[q < RG ? q : 0][s / 2][s % 2 * 2 + 1] : 0.0f;
+        }
+        bool owner;
+        const uint32_t first_v = sum_slices<NV>(v, owner);
+#pragma unroll
+        for (int i = 0; i < (NV + 15) / 16; ++i) {
+            const uint32_t q = (first_v + i) / PER, s = (first_v + i) % PER;
+            if (owner && q < RG && s < cnt)
+                sums[wave][P.token[first + s]][4 * q + r4] += v[i];  // only this wave's, one lane each
         }
     };
-    stream<RG, NTOK == 1 ? 2 : 4, RG <= 5 ? 3 : 2, 1>(
+    stream<RG, NG, NTOK == 1 ? 2 : 4, RG * NG <= 5 ? 3 : 2, 1>(
         rsrc(A.s2, A.E * HB * IB * 4), rsrc(A.h, A.T * A.topk * A.I * 4), ow, (128 - c0 % 128) / 4, A.I, wave,
         n * live, NWV, [] {}, unit, sink);
     __syncthreads();
@@ -727,7 +792,7 @@ hipError_t launch_moe(const MoeArgs &A, hipStream_t st)
     const uint32_t cus = cu_count() ? cu_count() : 256;
     // a workgroup for every unit that may come about, at most four per CU
     constexpr int RGU = 2;
-    const uint64_t pairs = A.T * A.topk, parts = A.E + pairs / S_UP < pairs ? A.E + pairs / S_UP : pairs;
+    const uint64_t pairs = A.T * A.topk, parts = A.E + pairs / NTOK < pairs ? A.E + pairs / NTOK : pairs;
     const uint64_t units = parts * (A.I / (4 * RGU));
     const dim3 grid(units < 4 * cus ? (uint32_t)units : 4 * cus);
     if constexpr (NTOK == 1) {
@@ -783,6 +848,14 @@ hipError_t launch_moe_fp8(const uint16_t *x, const float *logits, const uint8_t 
                        out, T, E, topk, H, I, renorm};
     if (T == 1)
         return launch_moe<1>(A, st);
+    // Parts of eight tokens from a mean of three tokens an expert on: the second
+    // group of operand rows costs loads and MFMAs whether it holds tokens or
+    // not, a second part the weights again.  16 tokens of 8x2, 4096x2048 (mean
+    // 4): 56 us against 65; 8 of 16x6, 5120x1024 (3): 57.7 against 62.6; 16 of
+    // 48x8, 2048x768 (2.7): 63.0 against 60.4; 16 of 64x6, 5120x1408 (1.5): 196
+    // against 192.
+    if (T * topk >= 3 * E)
+        return launch_moe<8>(A, st);
     return launch_moe<4>(A, st);
 }
 

@@ -106,7 +106,8 @@ int fp8_gemm_blockscale(const uint8_t *a, const float *a_scale, const uint8_t *w
  * in a fixed order (no atomics); between the two launches an activation is
  * held to 2^-17 of itself.  Which tokens share a batch may change the order
  * of a token's sum.  Only the chosen experts' weights are read, w13 once for
- * every four tokens of an expert and w2 once for every two.
+ * every four (where t*topk >= 3*e, eight) tokens of an expert and w2 once for
+ * every two (four).
  * 1 <= t <= QP_MOE_MAX_T, 1 <= topk <= min(e, QP_MOE_MAX_TOPK) (else
  * QP_ERR_RANGE); e <= QP_MOE_MAX_E, h and i multiples of 128, 2*i*h < 2^31
  * (the limit is per expert: all of them together may be larger) and

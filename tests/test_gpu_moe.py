@@ -119,3 +119,19 @@ def test_experts_past_32_bit_offsets():
     logits = torch.full((2, e), -INF, device=DEV)
     logits[0, 0], logits[0, 47], logits[1, 46], logits[1, 47] = 1.0, 2.0, 0.5, 0.25
     _check((x, logits, w13, grid(e, 2 * i // 128, h // 128), w2, grid(e, h // 128, i // 128)), 2, True)
+
+
+# every number of columns a workgroup can own, with one token, few and many
+# tokens an expert
+@pytest.mark.parametrize("h", [1024, 2048, 2560, 4096, 5120, 6144, 7168, 8192, 8320])
+@pytest.mark.parametrize("t,e,topk", [(1, 5, 2), (5, 7, 2), (16, 6, 4), (9, 3, 1)])
+def test_every_split_of_the_columns(t, e, topk, h):
+    _check(_layer(t, e, h, 128, seed=h), topk, True)
+
+
+@pytest.mark.parametrize("t,topk", [(2, 3), (4, 3), (5, 2), (8, 1), (9, 3), (13, 2), (16, 3), (16, 1)])
+@pytest.mark.parametrize("i", [128, 640])
+def test_experts_with_parts_of_every_size(t, topk, i):
+    """Few experts: parts of one to eight tokens, whole and ragged groups."""
+    for e in (3, 4):
+        _check(_layer(t, e, 640, i, seed=t), topk, False)
