@@ -370,8 +370,9 @@ __global__ __launch_bounds__(64 * MW * NW) void k_fp8_gemm_block_tiles(
 // Small tiles, K split over the waves: 16*MT rows of A by rpw <= 16*NT rows of
 // W per workgroup (rpw a multiple of 4, so that a problem's columns can be
 // dealt evenly over the CUs), for problems with too few large tiles to fill
-// them.  Wave w takes K blocks w, w + NW, ...; each wave DMAs its blocks'
-// panels into its own ring of D slots and waits for nothing but its own loads,
+// them.  The waves take runs of four K blocks in turn (512 bytes of a row, some
+// of it in flight at once: 28.2 us against 29.0 with single blocks in turn, 28.9
+// with runs of eight; 37 x 5120 x 17408); each wave DMAs its blocks' panels into its own ring of D slots and waits for nothing but its own loads,
 // so there is no barrier until the NW partial tiles are joined through LDS, in
 // wave order.
 // (Fragments loaded straight to registers, 16 rows of 64 bytes to an
@@ -380,8 +381,13 @@ __global__ __launch_bounds__(64 * MW * NW) void k_fp8_gemm_block_tiles(
 // Scales come four of the wave's blocks at a time, lane group g (quad lane
 // l%4) holding the g-th's: a load touches a cache line per row of A, and a line
 // holds many blocks' scales.
+//
+// Bound by W's way from HBM and, behind that, the waves' own work on a block,
+// which overlap in part: 37 x 5120 x 17408 takes 28 us, with W in the caches
+// (the same instructions) 18; the bytes alone 14.5.  4 x 17408 x 5120: 16.5 us,
+// 5.4 TB/s; 16 x 152064 x 5120: 136 us, 5.8 TB/s.
 // ---------------------------------------------------------------------------
-template <int MT, int NT, int NW, int D>
+template <int MT, int NT, int NW, int D, bool ONCE>
 __global__ __launch_bounds__(64 * NW) void k_fp8_gemm_block_ksplit(
     const uint8_t *__restrict__ A, const float *__restrict__ as,
     const uint8_t *__restrict__ W, const float *__restrict__ ws,
@@ -421,18 +427,23 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_gemm_block_ksplit(
             const int q = of_a ? j : j - 2 * MT;
             const uint32_t c = b * 128 + (q & 1 ? dcol ^ 64 : dcol);
             const uint32_t o = (of_a ? oa : ow) + 8 * q * K + c;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                of_a ? ra : rw, (lds_void *)(slot + 1024 * j), 16,
-                c < K && (of_a || drow + 8 * q < rpw) ? o : FB_OOB, 0, 0, 0);
+            if (of_a)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(slot + 1024 * j), 16,
+                                                         c < K ? o : FB_OOB, 0, 0, 0);
+            else                         // (aux 2: nontemporal)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void *)(slot + 1024 * j), 16,
+                                                         c < K && drow + 8 * q < rpw ? o : FB_OOB, 0, 0, ONCE ? 2 : 0);
         }
     };
+    // the wave's i-th block; past the last: blocks past K, which are zeros
+    auto nth = [&](uint32_t i) { return i / 4 * (4 * NW) + 4 * wave + i % 4; };
     // raw scales of the wave's blocks i .. i+3: a[t] of row 16t + l%16 and block
     // i + l/16, w[j] of rows 16j + 4(l/16) .. +3 and block i + l%4
     struct Scales {
         float a[MT], w[NT];
     } next;
     auto load_scales = [&](uint32_t i) {
-        const uint32_t ba = wave + NW * (i + g), bw = wave + NW * (i + (lane & 3));
+        const uint32_t ba = nth(i + g), bw = nth(i + (lane & 3));
 #pragma unroll
         for (int t = 0; t < MT; ++t)
             next.a[t] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
@@ -473,7 +484,7 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_gemm_block_ksplit(
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);
         __builtin_amdgcn_sched_barrier(0);
-        dma(wave + NW * (i + D), ring(U % D));
+        dma(nth(i + D), ring(U % D));
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             const float swq = __int_as_float(__builtin_amdgcn_update_dpp(
@@ -492,8 +503,8 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_gemm_block_ksplit(
     load_scales(0);
 #pragma unroll
     for (int d = 0; d < D; ++d)
-        dma(wave + NW * d, ring(d));
-    const uint32_t mine = nb > (uint32_t)wave ? (nb - wave + NW - 1) / NW : 0;   // the wave's blocks
+        dma(nth(d), ring(d));
+    const uint32_t runs = (nb + 3) / 4, mine = runs > (uint32_t)wave ? (runs - wave + NW - 1) / NW * 4 : 0;
     constexpr int UN = D == 3 ? 12 : 4;
     uint32_t i = 0;
     auto run = [&](auto self, auto u_) {
@@ -554,8 +565,21 @@ void launch_ksplit(const GemmArgs &g, uint32_t rpw)
 {
     constexpr int NW = ks_waves(MT + NT), D = ks_depth(MT + NT);
     const uint32_t mt = (g.m + 16 * MT - 1) / (16 * MT), nt = (g.n + rpw - 1) / rpw;
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_fp8_gemm_block_ksplit<MT, NT, NW, D>), dim3(mt * nt), dim3(64 * NW),
-                       0, g.st, g.a, g.as, g.w, g.ws, g.out, g.m, g.n, g.k, mt, rpw);
+    // W past the caches (nontemporal) where it is read once and no cache would
+    // have kept it: 16 x 152064 x 5120 136 us against 151; 4 x 17408 x 5120, cold,
+    // 17.1 against 19.1.  A small weight that is in the 256 MB memory-side cache
+    // stays there otherwise (1 x 5120 x 5120: 6.7 us against 8.0), and with more
+    // rows the gain is small (37 x 5120 x 17408, cold: 27.6 against 28.6; cached:
+    // 26.6 against 24.1), so those pass it only when larger than that cache.
+    const bool once = mt == 1 && (uint64_t)g.n * g.k >= (MT == 1 ? 1u << 26 : 1u << 28);
+    auto go = [&](auto k) {
+        hipLaunchKernelGGL(k, dim3(mt * nt), dim3(64 * NW), 0, g.st, g.a, g.as, g.w, g.ws, g.out, g.m, g.n, g.k, mt,
+                           rpw);
+    };
+    if (once)
+        go(k_fp8_gemm_block_ksplit<MT, NT, NW, D, true>);
+    else
+        go(k_fp8_gemm_block_ksplit<MT, NT, NW, D, false>);
 }
 
 template <int MT>

@@ -118,3 +118,16 @@ def test_agrees_with_the_blockscaled_gemv():
     ref.assert_gemm(_run(a, sa, w, sw), csg, k)
     torch.cuda.synchronize()
     ref.assert_gemm(y, csg, k)
+
+
+@pytest.mark.parametrize("m,n,k", [(2, 8208, 8192), (16, 131072, 528), (20, 16416, 16384), (64, 65600, 4112)])
+def test_weights_larger_than_the_caches(m, n, k):
+    _check(m, n, k)
+
+
+@pytest.mark.parametrize("nb", [1, 2, 3, 4, 5, 7, 8, 9, 31, 32, 33, 36, 63])
+@pytest.mark.parametrize("m", [2, 40])
+def test_every_remainder_of_the_k_blocks(m, nb):
+    """A wave takes runs of K blocks: none, some or all of a run may exist."""
+    _check(m, 160, 128 * nb, seed=nb)
+    _check(m, 160, 128 * nb - 48, seed=nb)
