@@ -12,6 +12,7 @@
 // no broadcast.
 #include "gemm_common.hpp"
 #include "qp_launch.hpp"
+#include <algorithm>
 #include <type_traits>
 
 namespace qp {
@@ -77,7 +78,7 @@ __global__ __launch_bounds__(64 * MW * NW) void k_fp8_gemm_block_tiles(
     const uint8_t *__restrict__ A, const float *__restrict__ as,
     const uint8_t *__restrict__ W, const float *__restrict__ ws,
     uint16_t *__restrict__ out, uint32_t M, uint32_t N, uint32_t K,
-    uint32_t mtiles, uint32_t ntiles, uint32_t first, uint32_t quarters, uint32_t vec_ok)
+    uint32_t mtiles, uint32_t ntiles, uint32_t first, uint32_t quarters)
 {
     constexpr int NWV = MW * NW, TM = 64 * MW, TN = 16 * TJ * NW;
     constexpr int AL = TM / 8 / NWV, WL = TN / 8 / NWV;     // DMA loads per wave and stage
@@ -329,45 +330,57 @@ __global__ __launch_bounds__(64 * MW * NW) void k_fp8_gemm_block_tiles(
 
     // Lane l holds, of tile (t, j), row 16t + l%16 and columns 16j + 4(l/16) .. +3.
     const uint32_t rb = m0 + wm * 64, cb = n0 + wn * 16 * TJ;
-    if (vec_ok) {
-        // Stage the wave's 64 x 16TJ block in LDS (RB = 32TJ bytes per row;
-        // 8-byte unit u of row r at u ^ x(r), so that 16 rows' writes spread
-        // over the banks) and store it in whole rows, 16 bytes per lane.
-        constexpr int RB = 32 * TJ, UN = RB / 8, PU = RB / 16, RPI = 64 / PU;
-        constexpr int OWN = 64 * RB;                       // this wave's bytes
-        constexpr int PS = SLOT / OWN;                     // waves per slot
-        static_assert(PS >= 1 && NWV <= 5 * PS, "fits");
-        const int es = wave / PS;
-        uint8_t *const ep = (es == 0 ? S0 : es == 1 ? S1 : es == 2 ? S2 : es == 3 ? S3 : S4) + wave % PS * OWN;
+    // Stage the wave's 64 x 16TJ block in LDS (RB = 32TJ bytes per row;
+    // 8-byte unit u of row r at u ^ x(r), so that 16 rows' writes spread over
+    // the banks) and store it in whole rows, 16 bytes per lane.
+    constexpr int RB = 32 * TJ, UN = RB / 8, PU = RB / 16, RPI = 64 / PU;
+    constexpr int OWN = 64 * RB;                       // this wave's bytes
+    constexpr int PS = SLOT / OWN;                     // waves per slot
+    static_assert(PS >= 1 && NWV <= 5 * PS, "fits");
+    const int es = wave / PS;
+    uint8_t *const ep = (es == 0 ? S0 : es == 1 ? S1 : es == 2 ? S2 : es == 3 ? S3 : S4) + wave % PS * OWN;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int j = 0; j < TJ; ++j) {
-                const f32x4 &c = acc[t][j];
-                const u32x2 v = {pk_bf16(c[0], c[1]), pk_bf16(c[2], c[3])};
-                const int r = 16 * t + r16;
-                *reinterpret_cast<u32x2 *>(ep + r * RB + 8 * ((4 * j + g) ^ (2 * (r & (UN / 2 - 1))))) = v;
-            }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        const int p = lane % PU;
+        for (int j = 0; j < TJ; ++j) {
+            const f32x4 &c = acc[t][j];
+            const u32x2 v = {pk_bf16(c[0], c[1]), pk_bf16(c[2], c[3])};
+            const int r = 16 * t + r16;
+            *reinterpret_cast<u32x2 *>(ep + r * RB + 8 * ((4 * j + g) ^ (2 * (r & (UN / 2 - 1))))) = v;
+        }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int pu = lane % PU;
+    const uint32_t col = cb + 8 * pu;
+    auto row = [&](int it) { return RPI * it + lane / PU; };
+    auto chunk = [&](int r) {
+        return *reinterpret_cast<const u32x4 *>(ep + r * RB + 16 * (pu ^ (r & (UN / 2 - 1))));
+    };
+    if (N % 8 == 0) {
 #pragma unroll 4
         for (int it = 0; it < 64 / RPI; ++it) {
-            const int r = RPI * it + lane / PU;
-            const u32x4 v = *reinterpret_cast<const u32x4 *>(ep + r * RB + 16 * (p ^ (r & (UN / 2 - 1))));
-            if (rb + r < M && cb + 8 * p < N)
-                *reinterpret_cast<u32x4 *>(out + (size_t)(rb + r) * N + cb + 8 * p) = v;
+            const int r = row(it);
+            const u32x4 v = chunk(r);
+            if (rb + r < M && col < N)
+                *reinterpret_cast<u32x4 *>(out + (size_t)(rb + r) * N + col) = v;
         }
-    } else {
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int j = 0; j < TJ; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint32_t gi = rb + 16 * t + r16, gj = cb + 16 * j + 4 * g + r;
-                    if (gi < M && gj < N)
-                        out[(size_t)gi * N + gj] = (uint16_t)f32_to_bf16(acc[t][j][r]);
-                }
+        return;
+    }
+    // Rows of C are aligned to 2 bytes only.  Global stores need no more; element
+    // by element 7218 x 1641 x 384 took 31.7 us, where this takes 13.4.
+    typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4_any;
+    const uint32_t live = col < N ? min(N - col, 8u) : 0;
+#pragma unroll 4
+    for (int it = 0; it < 64 / RPI; ++it) {
+        const int r = row(it);
+        const u32x4 v = chunk(r);
+        uint16_t *const to = out + (size_t)(rb + r) * N + col;
+        if (rb + r >= M)
+            continue;
+        if (live == 8)
+            *reinterpret_cast<u32x4_any *>(to) = v;
+        else
+            for (uint32_t i = 0; i < live; ++i)        // the row's last chunk
+                to[i] = (uint16_t)(v[i / 2] >> 16 * (i % 2));
     }
 }
 
@@ -377,9 +390,10 @@ __global__ __launch_bounds__(64 * MW * NW) void k_fp8_gemm_block_tiles(
 // dealt evenly over the CUs), for problems with too few large tiles to fill
 // them.  The waves take runs of four K blocks in turn (512 bytes of a row, some
 // of it in flight at once: 28.2 us against 29.0 with single blocks in turn, 28.9
-// with runs of eight; 37 x 5120 x 17408); each wave DMAs its blocks' panels into its own ring of D slots and waits for nothing but its own loads,
-// so there is no barrier until the NW partial tiles are joined through LDS, in
-// wave order.
+// with runs of eight; 37 x 5120 x 17408), or single ones where there is at most
+// one for each (75 x 4224 x 224: 6.1 against 7.4); each wave DMAs its blocks' panels into
+// its own ring of D slots and waits for nothing but its own loads, so there is
+// no barrier until the NW partial tiles are joined through LDS, in wave order.
 // (Fragments loaded straight to registers, 16 rows of 64 bytes to an
 // instruction, were half as fast: 8 rows of whole 128-byte lines are what the
 // address unit and HBM serve best.)
@@ -441,7 +455,8 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_gemm_block_ksplit(
         }
     };
     // the wave's i-th block; past the last: blocks past K, which are zeros
-    auto nth = [&](uint32_t i) { return i / 4 * (4 * NW) + 4 * wave + i % 4; };
+    const uint32_t rlog = nb > NW ? 2 : 0, rlen = 1u << rlog;
+    auto nth = [&](uint32_t i) { return (i >> rlog) * (rlen * NW) + rlen * wave + (i & (rlen - 1)); };
     // raw scales of the wave's blocks i .. i+3: a[t] of row 16t + l%16 and block
     // i + l/16, w[j] of rows 16j + 4(l/16) .. +3 and block i + l%4
     struct Scales {
@@ -509,7 +524,8 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_gemm_block_ksplit(
 #pragma unroll
     for (int d = 0; d < D; ++d)
         dma(nth(d), ring(d));
-    const uint32_t runs = (nb + 3) / 4, mine = runs > (uint32_t)wave ? (runs - wave + NW - 1) / NW * 4 : 0;
+    const uint32_t runs = (nb + rlen - 1) >> rlog;
+    const uint32_t mine = runs > (uint32_t)wave ? (runs - wave + NW - 1) / NW * rlen : 0;
     constexpr int UN = D == 3 ? 12 : 4;
     uint32_t i = 0;
     auto run = [&](auto self, auto u_) {
@@ -590,7 +606,9 @@ void launch_ksplit(const GemmArgs &g, uint32_t rpw)
 template <int MT>
 void launch_ksplit_rows(const GemmArgs &g, uint32_t rpw)
 {
-    if (rpw <= 32)
+    if (rpw <= 16)
+        launch_ksplit<MT, 1>(g, rpw);
+    else if (rpw <= 32)
         launch_ksplit<MT, 2>(g, rpw);
     else if (rpw <= 48)
         launch_ksplit<MT, 3>(g, rpw);
@@ -604,7 +622,7 @@ hipError_t launch_tiles(const GemmArgs &g, uint32_t mt, uint32_t nt, uint32_t fi
 {
     hipLaunchKernelGGL(HIP_KERNEL_NAME(k_fp8_gemm_block_tiles<MW, NW, TJ>), dim3(quarters ? 4 * tiles : tiles),
                        dim3(64 * MW * NW), 0, g.st, g.a, g.as, g.w, g.ws, g.out, g.m, g.n, g.k, mt, nt,
-                       first, (uint32_t)quarters, (uint32_t)(g.n % 8 == 0));
+                       first, (uint32_t)quarters);
     count_launch();
     return hipGetLastError();
 }
@@ -618,30 +636,46 @@ hipError_t launch_fp8_gemm_blockscale(const uint8_t *a, const float *as, const u
     const GemmArgs g = {a, as, w, ws, out, m, n, k, st};
     const uint32_t cus = cu_count() ? cu_count() : 256, nb = (k + 127) / 128;
 
-    // Time estimates in nanoseconds, from what the kernels take per K block
-    // (one MI355X, K = 5120 and 17408).  ksplit: 45 per 16 rows of A and of W a
-    // workgroup loads, one workgroup per CU.  128 x 128 tiles: 680 alone on a
-    // CU, 1150 for two.  256 x 256 tiles: 1680.
-    const uint32_t mtk = m <= 64 ? (m + 15) / 16 : 4, mwg = (m + 16 * mtk - 1) / (16 * mtk);
-    // ksplit's W rows per workgroup: the columns dealt over the CUs, at most
-    // 80, in as few rounds as that allows
-    const uint32_t per = cus > mwg ? cus / mwg : 1;
-    const uint32_t rounds_n = (n + 80 * per - 1) / (80 * per);
-    const uint32_t rpw = ((n + rounds_n * per - 1) / (rounds_n * per) + 3) / 4 * 4;
-    const uint64_t wgs = (uint64_t)mwg * ((n + rpw - 1) / rpw);
-    const uint32_t ntk = rpw <= 32 ? 2 : rpw <= 48 ? 3 : 5;
-    const uint64_t t_ks = (wgs + cus - 1) / cus * (45ull * (mtk + ntk) * nb);
+    // Time estimates in tenths of a nanosecond, fitted to 34 shapes from 17 x 512
+    // x 4096 to 6599 x 256 x 8448 with every kernel on each (one MI355X; the
+    // choice costs 1% against the best of them).  ksplit, per round of its
+    // workgroups: a start and an end that grow with the tile, and per K block
+    // 7.7 ns for 8 rows of A, 13.4 for 8 of W and 9.2 for a 16 x 16 tile.  It
+    // takes 16 to 64 rows of A a workgroup, whatever suits the shape: 64 x 5120
+    // x 17408 37 us with 64, 31 with 32; 284 x 223 x 14336 17 with 64, 9 with 16.
+    // 128 x 128 tiles: 596 ns a K block alone on a CU, 1100 for two.  256 x 256
+    // tiles: 1680.
+    uint64_t t_ks = ~0ull;
+    uint32_t mtk = 1, rpw = 16;
+    for (uint32_t mt = 1; mt <= 4 && 16 * (mt - 1) < m; ++mt) {
+        // W rows per workgroup: the columns dealt over the CUs, at most 80, in
+        // as few rounds as that allows
+        const uint32_t mwg = (m + 16 * mt - 1) / (16 * mt), per = cus > mwg ? cus / mwg : 1;
+        const uint32_t rounds_n = (uint32_t)((n + 80ull * per - 1) / (80ull * per));
+        const uint32_t share = (uint32_t)((n + (uint64_t)rounds_n * per - 1) / ((uint64_t)rounds_n * per));
+        const uint32_t rows = (share + 3) / 4 * 4, nt = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 48 ? 3 : 5;
+        const uint64_t wgs = (uint64_t)mwg * ((n + rows - 1) / rows);
+        const uint64_t t = 23000 + (wgs + cus - 1) / cus *
+                                       (7700 + 2360 * mt * nt +
+                                        nb * (77ull * ((std::min(16 * mt, m) + 7) / 8) + 134 * ((rows + 7) / 8) + 92 * mt * nt));
+        if (t < t_ks) {
+            t_ks = t;
+            mtk = mt;
+            rpw = rows;
+        }
+    }
     auto t_small = [&](uint64_t tiles) {
-        return (tiles / (2 * cus) * 1150 + (tiles % (2 * cus) > cus ? 1150 : tiles % (2 * cus) ? 680 : 0)) * nb;
+        const uint64_t last = tiles % (2 * cus);
+        return 35600 + (tiles / (2 * cus) * 11000 + (last > cus ? 11000 : last ? 5960 : 0)) * nb;
     };
     const uint32_t ms = (m + 127) / 128, ns = (n + 127) / 128, ml = (m + 255) / 256, nl = (n + 255) / 256;
     const uint64_t small = (uint64_t)ms * ns, large = (uint64_t)ml * nl;
     // the 256 x 256 tiles past the last whole round run as 128 x 128 quarters
     // if that is faster than another round
     const uint64_t tail = large % cus;
-    const bool quarter = tail && t_small(4 * tail) < 1680ull * nb;
+    const bool quarter = tail && t_small(4 * tail) < 16800ull * nb;
     const uint64_t full = quarter ? large - tail : large;
-    const uint64_t t_large = (full + cus - 1) / cus * 1680ull * nb + (quarter ? t_small(4 * tail) : 0);
+    const uint64_t t_large = 58000 + (full + cus - 1) / cus * 16800ull * nb + (quarter ? t_small(4 * tail) : 0);
 
     if (t_ks <= t_small(small) && t_ks <= t_large) {
         if (mtk == 1)

@@ -131,3 +131,17 @@ def test_every_remainder_of_the_k_blocks(m, nb):
     """A wave takes runs of K blocks: none, some or all of a run may exist."""
     _check(m, 160, 128 * nb, seed=nb)
     _check(m, 160, 128 * nb - 48, seed=nb)
+
+
+@pytest.mark.parametrize("m,n,k", [(4200, 4353, 144), (7000, 1276, 128), (2100, 2091, 272), (700, 1030, 1040),
+                                   (284, 223, 2048), (989, 100, 1536), (500, 12, 4096), (70, 5000, 640)])
+def test_rows_at_any_alignment(m, n, k):
+    """N of every remainder by 8; nothing is written past the last row."""
+    a, sa, w, sw = _operands(m, n, k, seed=7)
+    room = torch.full((m * n + 64,), 3.0, dtype=torch.bfloat16, device=DEV)
+    out = room[:m * n].view(m, n)
+    out.fill_(float("nan"))
+    qp.fp8_gemm_blockscale(a, sa, w, sw, out)
+    torch.cuda.synchronize()
+    ref.assert_gemm(out, ref.gemm_blockscale(a, sa, w, sw), k)
+    assert torch.all(room[m * n:] == 3.0)
