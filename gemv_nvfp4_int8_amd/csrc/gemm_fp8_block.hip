@@ -51,6 +51,10 @@ namespace {
 // ---------------------------------------------------------------------------
 constexpr uint32_t FB_OOB = 0x80000000u;
 
+// C's rows start at any multiple of 2 bytes, which global stores allow.
+typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4_any;
+typedef __attribute__((ext_vector_type(2), aligned(2))) uint32_t u32x2_any;
+
 // s_waitcnt immediates: vmcnt <= n alone, lgkmcnt == 0 alone
 constexpr int waitcnt_vm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
 constexpr int WAIT_LGKM0 = 15 | (7 << 4) | (3 << 14);
@@ -367,7 +371,6 @@ __global__ __launch_bounds__(64 * MW * NW) void k_fp8_gemm_block_tiles(
     }
     // Rows of C are aligned to 2 bytes only.  Global stores need no more; element
     // by element 7218 x 1641 x 384 took 31.7 us, where this takes 13.4.
-    typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4_any;
     const uint32_t live = col < N ? min(N - col, 8u) : 0;
 #pragma unroll 4
     for (int it = 0; it < 64 / RPI; ++it) {
@@ -552,16 +555,23 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_gemm_block_ksplit(
         for (int j = 0; j < NT; ++j)
             *reinterpret_cast<f32x4 *>(part(wave) + (t * NT + j) * 1024 + 16 * lane) = acc[t][j];
     __syncthreads();
-    // output e of the tile: row e / (16 NT), column e % (16 NT)
-    for (uint32_t e = threadIdx.x; e < 256 * MT * NT; e += 64 * NW) {
-        const uint32_t r = e / (16 * NT), c = e % (16 * NT);
-        const uint32_t tile = r / 16 * NT + c / 16, l = r % 16 + 16 * (c % 16 / 4);
-        float v = 0.0f;
+    // unit e of the tile: a lane's four columns of one row
+    for (uint32_t e = threadIdx.x; e < 64 * MT * NT; e += 64 * NW) {
+        const uint32_t tile = e / 64, l = e % 64;
+        const uint32_t r = m0 + tile / NT * 16 + l % 16, c = tile % NT * 16 + l / 16 * 4;
+        f32x4 v = {0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < NW; ++w)
-            v += *reinterpret_cast<const float *>(part(w) + tile * 1024 + 16 * l + 4 * (c % 4));
-        if (m0 + r < M && c < rpw && n0 + c < N)
-            out[(size_t)(m0 + r) * N + n0 + c] = (uint16_t)f32_to_bf16(v);
+            v += *reinterpret_cast<const f32x4 *>(part(w) + tile * 1024 + 16 * l);
+        if (r >= M || c >= rpw || n0 + c >= N)
+            continue;
+        uint16_t *const to = out + (size_t)r * N + n0 + c;
+        const u32x2 o = {pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+        if (n0 + c + 4 <= N)                 // (rpw is a multiple of 4; rows of C are aligned to 2 bytes)
+            *reinterpret_cast<u32x2_any *>(to) = o;
+        else
+            for (uint32_t i = 0; i < N - (n0 + c); ++i)
+                to[i] = (uint16_t)(o[i / 2] >> 16 * (i % 2));
     }
 }
 
