@@ -646,14 +646,14 @@ hipError_t launch_fp8_gemm_blockscale(const uint8_t *a, const float *as, const u
     const GemmArgs g = {a, as, w, ws, out, m, n, k, st};
     const uint32_t cus = cu_count() ? cu_count() : 256, nb = (k + 127) / 128;
 
-    // Time estimates in tenths of a nanosecond, fitted to 34 shapes from 17 x 512
+    // Time estimates in tenths of a nanosecond, fitted to 36 shapes from 17 x 512
     // x 4096 to 6599 x 256 x 8448 with every kernel on each (one MI355X; the
     // choice costs 1% against the best of them).  ksplit, per round of its
     // workgroups: a start and an end that grow with the tile, and per K block
-    // 7.7 ns for 8 rows of A, 13.4 for 8 of W and 9.2 for a 16 x 16 tile.  It
+    // 8.5 ns for 8 rows of A, 12.9 for 8 of W and 9.1 for a 16 x 16 tile.  It
     // takes 16 to 64 rows of A a workgroup, whatever suits the shape: 64 x 5120
-    // x 17408 37 us with 64, 31 with 32; 284 x 223 x 14336 17 with 64, 9 with 16.
-    // 128 x 128 tiles: 596 ns a K block alone on a CU, 1100 for two.  256 x 256
+    // x 17408 36 us with 64, 30 with 32; 284 x 223 x 14336 17 with 64, 9 with 16.
+    // 128 x 128 tiles: 598 ns a K block alone on a CU, 1100 for two.  256 x 256
     // tiles: 1680.
     uint64_t t_ks = ~0ull;
     uint32_t mtk = 1, rpw = 16;
@@ -666,8 +666,9 @@ hipError_t launch_fp8_gemm_blockscale(const uint8_t *a, const float *as, const u
         const uint32_t rows = (share + 3) / 4 * 4, nt = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 48 ? 3 : 5;
         const uint64_t wgs = (uint64_t)mwg * ((n + rows - 1) / rows);
         const uint64_t t = 23000 + (wgs + cus - 1) / cus *
-                                       (7700 + 2360 * mt * nt +
-                                        nb * (77ull * ((std::min(16 * mt, m) + 7) / 8) + 134 * ((rows + 7) / 8) + 92 * mt * nt));
+                                       (8800 + 1180 * mt * nt +
+                                        nb * (85ull * ((std::min(16 * mt, m) + 7) / 8) +
+                                              129 * ((rows + 7) / 8) + 91 * mt * nt));
         if (t < t_ks) {
             t_ks = t;
             mtk = mt;
@@ -676,7 +677,7 @@ hipError_t launch_fp8_gemm_blockscale(const uint8_t *a, const float *as, const u
     }
     auto t_small = [&](uint64_t tiles) {
         const uint64_t last = tiles % (2 * cus);
-        return 35600 + (tiles / (2 * cus) * 11000 + (last > cus ? 11000 : last ? 5960 : 0)) * nb;
+        return 35100 + (tiles / (2 * cus) * 11000 + (last > cus ? 11000 : last ? 5980 : 0)) * nb;
     };
     const uint32_t ms = (m + 127) / 128, ns = (n + 127) / 128, ml = (m + 255) / 256, nl = (n + 255) / 256;
     const uint64_t small = (uint64_t)ms * ns, large = (uint64_t)ml * nl;
