@@ -162,10 +162,9 @@ __device__ __forceinline__ u32x2 encode8(const float *y, float sc)
     return sc == 0.0f ? (u32x2){0, 0} : o;
 }
 
-template <int FMT>
-__device__ __forceinline__ uint32_t scales_per_row(uint32_t k)
+__host__ __device__ __forceinline__ constexpr uint32_t scales_per_row(int fmt, uint32_t k)
 {
-    return FMT == FMT_ROW ? 1 : FMT == FMT_BLOCK128 ? (k + 127) / 128 : FMT == FMT_INT8 ? k / 32 : 0;
+    return fmt == FMT_ROW ? 1 : fmt == FMT_BLOCK128 ? (k + 127) / 128 : fmt == FMT_INT8 ? k / 32 : 0;
 }
 
 // Quantize and store chunk c of a row: block formats find their own scale,
@@ -241,7 +240,7 @@ __device__ __forceinline__ void finish(const RowArgs &A, uint32_t row, uint32_t 
         if (first == 0)
             A.s[row] = sc;
     }
-    float *sr = A.s + (size_t)row * scales_per_row<FMT>(A.k);
+    float *sr = A.s + (size_t)row * scales_per_row(FMT, A.k);
     uint8_t *qr = A.q + (size_t)row * A.k * (FMT == FMT_BF16 ? 2 : 1);
 #pragma unroll
     for (int j = 0; j < CPL; ++j) {
@@ -403,7 +402,7 @@ __global__ __launch_bounds__(1024) void k_row_quant_long(RowArgs A)
         if (t == 0)
             A.s[row] = sc;
     }
-    float *sr = A.s + (size_t)row * scales_per_row<FMT>(A.k);
+    float *sr = A.s + (size_t)row * scales_per_row(FMT, A.k);
     uint8_t *qr = A.q + at * (FMT == FMT_BF16 ? 2 : 1);
     for (uint32_t i = 0; i < steps; ++i) {
         const uint32_t c = t + 1024 * i;
@@ -468,7 +467,19 @@ hipError_t launch_rmsnorm_residual_quant(const uint16_t *x, const uint16_t *res,
                                          float eps, int fmt, void *q, float *s, uint16_t *res_out,
                                          uint32_t rows, uint32_t k, hipStream_t st)
 {
-    return launch_any<true>({x, res, w, res_out, (uint8_t *)q, s, eps, rows, k, 1}, fmt, st);
+    // A launch holds fewer than 2^32 threads (one with more loses rows without
+    // an error), and a row takes 64 of them or more: rows of 16 values, which
+    // may number 2^26 and more, go in several launches.
+    constexpr uint32_t MOST = 1u << 25;
+    for (uint32_t at = 0; at < rows; at += MOST) {
+        const size_t e = (size_t)at * k;
+        const RowArgs A = {x + e, res ? res + e : nullptr, w, res ? res_out + e : nullptr,
+                           (uint8_t *)q + e * (fmt == FMT_BF16 ? 2 : 1), s + (size_t)at * scales_per_row(fmt, k), eps,
+                           std::min(rows - at, MOST), k, 1};
+        if (const hipError_t err = launch_any<true>(A, fmt, st))
+            return err;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_silu_mul_quant(const uint16_t *gate_up, int fmt, void *q, float *s, uint32_t rows,
