@@ -112,7 +112,10 @@ __device__ __forceinline__ void norm8(u32x4 h, u32x4 w, float rstd, float *y)
 // silu(g) * u with the hardware's exp2 and reciprocal (1 ulp each).  The
 // argument's rounding costs |g| * 2^-24 relative on exp(-g): at most 2e-7 of
 // y where exp(-g) <= 1 counts, and only for negative g, whose y is small,
-// more.  exp(-g) = inf gives -0, the limit.
+// more.  exp(-g) = inf gives -0, the limit.  The reciprocal is that of a
+// quarter of 1 + exp(-g), and g enters as a quarter (both exact): of the whole
+// it would be subnormal from g = -87.4 down to where exp(-g) is inf, -88.7,
+// and the instruction returns 0 in place of a subnormal.
 __device__ __forceinline__ void silu8(u32x4 g, u32x4 u, float *y)
 {
     float a[8], b[8];
@@ -121,7 +124,7 @@ __device__ __forceinline__ void silu8(u32x4 g, u32x4 u, float *y)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float e = __builtin_amdgcn_exp2f(a[i] * -0x1.715476p+0f);
-        y[i] = a[i] * __builtin_amdgcn_rcpf(1.0f + e) * b[i];
+        y[i] = a[i] * 0.25f * __builtin_amdgcn_rcpf(__builtin_fmaf(e, 0.25f, 0.25f)) * b[i];
     }
 }
 

@@ -65,7 +65,8 @@ int rmsnorm_residual_quant(const uint16_t *x, const uint16_t *residual,
 
 /* ------------------------------------------------------------------------
  * Gated activation and quantizer in one pass:
- *   y = silu(gate) * up,  silu(g) = g / (1 + exp(-g))      in F32
+ *   y = silu(gate) * up,  silu(g) = g / (1 + exp(-g))      in F32 (so silu is
+ *   0 where exp(-g) passes F32's range, for gates below -88.7)
  *   q, scale = y in the form `fmt`.
  *   gate_up [rows, 2k] BF16: a row's k gate values, then its k up values (the
  *   output of one product with the gate and up weights stacked);
