@@ -88,7 +88,8 @@ int silu_mul_quant(const uint16_t *gate_up, int fmt, void *q, float *scale,
  * neighbouring products and add the groups of 8 in F32), the scaled blocks are
  * added in F32, and BF16 rounding happens once.  Any m is served, from one row on.  The order in
  * which the blocks are added follows m, n and k, so a row's last bits may differ
- * between batch sizes.
+ * between batch sizes.  A NaN in a row of A or W (or in a scale) stays in the
+ * outputs of that row (of the rows that the scale is for).
  * ---------------------------------------------------------------------- */
 int fp8_gemm_blockscale(const uint8_t *a, const float *a_scale, const uint8_t *w,
                         const float *block_scale, uint16_t *out, uint32_t m,
