@@ -424,7 +424,8 @@ def _need_act(q, scale, fmt, rows, k):
         _need(scale, "scale", F32, (rows, (k + 127) // 128))
     elif fmt == QP_ACT_FP8_ROW:
         _need(q, "q", U8, (rows, k))
-        _need(scale, "scale", F32, (rows,) if scale.dim() == 1 else (rows, 1))
+        flat = isinstance(scale, torch.Tensor) and scale.dim() == 1
+        _need(scale, "scale", F32, (rows,) if flat else (rows, 1))
     elif fmt == QP_ACT_INT8_BLOCK32:
         _need(q, "q", I8, (rows, k))
         _need(scale, "scale", F32, (rows, k // 32))

@@ -1,4 +1,5 @@
-"""Calls at the ends of the accepted sizes."""
+"""Calls at the ends of the accepted sizes, and the binding's refusal of a
+missing scale."""
 import pytest
 import torch
 
@@ -34,3 +35,13 @@ def test_norm_of_more_rows_than_one_launch_holds(fmt):
         assert torch.equal(q1, q[part]) and torch.equal(o1, out[part])
         assert bf16 or torch.equal(s1, s[part])
     assert bf16 or bool(torch.isfinite(s).all())
+
+
+@pytest.mark.parametrize("fmt", [qp.QP_ACT_FP8_ROW, qp.QP_ACT_FP8_BLOCK128, qp.QP_ACT_INT8_BLOCK32])
+def test_a_missing_scale_is_a_type_error(fmt):
+    x, w = _normal((2, 256), 3), _normal((256,), 4)
+    q = torch.empty((2, 256), dtype=torch.int8 if fmt == qp.QP_ACT_INT8_BLOCK32 else torch.uint8, device=DEV)
+    with pytest.raises(TypeError, match="scale"):
+        qp.rmsnorm_residual_quant(x, None, w, 1e-6, fmt, q, None)
+    with pytest.raises(TypeError, match="scale"):
+        qp.silu_mul_quant(_normal((2, 512), 5), fmt, q, None)
