@@ -43,6 +43,11 @@ QP_ACT_FP8_BLOCK128 = 1
 QP_ACT_INT8_BLOCK32 = 2
 QP_ACT_BF16 = 16
 
+QP_BLOCKSCALE_TILES_128 = 1
+QP_BLOCKSCALE_TILES_256 = 2
+QP_BLOCKSCALE_TILES_256_QUARTERS = 3
+QP_BLOCKSCALE_KSPLIT = 256
+
 QP_TILES_BANDED = 0
 QP_TILES_MFAST = 1
 QP_TILES_NFAST = 2
@@ -91,6 +96,7 @@ def lib() -> ctypes.CDLL:
             "rmsnorm_residual_quant": [P, P, P, F, I, P, P, P, U, U, P],
             "silu_mul_quant": [P, I, P, P, U, U, P],
             "fp8_gemm_blockscale": [P, P, P, P, P, U, U, U, P],
+            "fp8_gemm_blockscale_kernel": [U, U, U],
             "moe_fp8_blockscale": [P, P, P, P, P, P, P, ctypes.c_uint64, P, U, U, U, U, U, I, P],
             "qproj_cache_create": [PP],
             "qproj_cache_destroy": [P],
@@ -484,6 +490,16 @@ def fp8_gemm_blockscale(a, a_scale, w, block_scale, out, stream=None):
         _stream(stream)))
 
 
+def fp8_gemm_blockscale_kernel(m, n, k) -> int:
+    """The kernel fp8_gemm_blockscale runs for a shape: QP_BLOCKSCALE_TILES_*, or
+    QP_BLOCKSCALE_KSPLIT + 16s of rows of A + 8 * 16s of rows of W (+ 64: W past
+    the caches) of a workgroup."""
+    kernel = lib().fp8_gemm_blockscale_kernel(m, n, k)
+    if kernel < 0:
+        raise QProjError("fp8_gemm_blockscale_kernel", kernel)
+    return kernel
+
+
 def moe_fp8_blockscale_workspace(t, topk, i) -> int:
     """Bytes of scratch moe_fp8_blockscale needs for t tokens, topk experts a
     token and an intermediate size i."""
@@ -603,7 +619,7 @@ __all__ = [
     "w4a4_gemm", "requant_w_blockfp8_rowwise", "quant_rowwise_fp8",
     "fp8_gemm_rowscale", "fp8_rowwise_proj", "fp8_gemv_rowscale",
     "fp8_gemv_blockscale", "w4a16_gemv", "rmsnorm_residual_quant",
-    "silu_mul_quant", "fp8_gemm_blockscale", "moe_fp8_blockscale",
-    "moe_fp8_blockscale_workspace", "DerivedWeights",
+    "silu_mul_quant", "fp8_gemm_blockscale", "fp8_gemm_blockscale_kernel",
+    "moe_fp8_blockscale", "moe_fp8_blockscale_workspace", "DerivedWeights",
     "launch_count", "status_string", "abi_version", "lib", "QProjError",
 ]

@@ -22,6 +22,11 @@ int check_act(int fmt, uint32_t rows, uint32_t k, uint64_t wide)
     return QP_OK;
 }
 
+bool blockscale_shape(uint32_t m, uint32_t n, uint32_t k)
+{
+    return m != 0 && n != 0 && k != 0 && k % 16 == 0 && fits(m, k) && fits(n, k) && fits(m, n);
+}
+
 } // namespace
 
 extern "C" {
@@ -60,9 +65,14 @@ int fp8_gemm_blockscale(const uint8_t *a, const float *a_scale, const uint8_t *w
 {
     if (int e = check_ptrs({a, a_scale, w, block_scale, out}))
         return e;
-    if (m == 0 || n == 0 || k == 0 || k % 16 != 0 || !fits(m, k) || !fits(n, k) || !fits(m, n))
+    if (!blockscale_shape(m, n, k))
         return QP_ERR_SHAPE;
     return done(qp::launch_fp8_gemm_blockscale(a, a_scale, w, block_scale, out, m, n, k, S(stream)));
+}
+
+int fp8_gemm_blockscale_kernel(uint32_t m, uint32_t n, uint32_t k)
+{
+    return blockscale_shape(m, n, k) ? qp::fp8_gemm_blockscale_kernel(m, n, k) : QP_ERR_SHAPE;
 }
 
 uint64_t moe_fp8_blockscale_workspace(uint32_t t, uint32_t topk, uint32_t i)

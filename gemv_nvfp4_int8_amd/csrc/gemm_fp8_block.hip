@@ -12,6 +12,7 @@
 // no broadcast.
 #include "gemm_common.hpp"
 #include "qp_launch.hpp"
+#include "../../include/qproj_layer.h"
 #include <algorithm>
 #include <type_traits>
 
@@ -586,6 +587,8 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_gemm_block_ksplit(
 // beat a deeper ring).
 constexpr int ks_waves(int s) { return s <= 5 ? 8 : s == 6 ? 6 : s <= 8 ? 5 : 4; }
 constexpr int ks_depth(int s) { return s <= 3 ? 3 : 2; }
+// NT of a workgroup of rpw rows of W
+constexpr uint32_t ks_columns(uint32_t rpw) { return rpw <= 16 ? 1 : rpw <= 32 ? 2 : rpw <= 48 ? 3 : 5; }
 
 struct GemmArgs {
     const uint8_t *a;
@@ -598,17 +601,10 @@ struct GemmArgs {
 };
 
 template <int MT, int NT>
-void launch_ksplit(const GemmArgs &g, uint32_t rpw)
+void launch_ksplit(const GemmArgs &g, uint32_t rpw, bool once)
 {
     constexpr int NW = ks_waves(MT + NT), D = ks_depth(MT + NT);
     const uint32_t mt = (g.m + 16 * MT - 1) / (16 * MT), nt = (g.n + rpw - 1) / rpw;
-    // W past the caches (nontemporal) where it is read once and no cache would
-    // have kept it: 16 x 152064 x 5120 136 us against 151; 4 x 17408 x 5120, cold,
-    // 17.1 against 19.1.  A small weight that is in the 256 MB memory-side cache
-    // stays there otherwise (1 x 5120 x 5120: 6.7 us against 8.0), and with more
-    // rows the gain is small (37 x 5120 x 17408, cold: 27.6 against 28.6; cached:
-    // 26.6 against 24.1), so those pass it only when larger than that cache.
-    const bool once = mt == 1 && (uint64_t)g.n * g.k >= (MT == 1 ? 1u << 26 : 1u << 28);
     auto go = [&](auto k) {
         hipLaunchKernelGGL(k, dim3(mt * nt), dim3(64 * NW), 0, g.st, g.a, g.as, g.w, g.ws, g.out, g.m, g.n, g.k, mt,
                            rpw);
@@ -620,16 +616,14 @@ void launch_ksplit(const GemmArgs &g, uint32_t rpw)
 }
 
 template <int MT>
-void launch_ksplit_rows(const GemmArgs &g, uint32_t rpw)
+void launch_ksplit_rows(const GemmArgs &g, uint32_t rpw, bool once)
 {
-    if (rpw <= 16)
-        launch_ksplit<MT, 1>(g, rpw);
-    else if (rpw <= 32)
-        launch_ksplit<MT, 2>(g, rpw);
-    else if (rpw <= 48)
-        launch_ksplit<MT, 3>(g, rpw);
-    else
-        launch_ksplit<MT, 5>(g, rpw);
+    switch (ks_columns(rpw)) {
+    case 1: launch_ksplit<MT, 1>(g, rpw, once); break;
+    case 2: launch_ksplit<MT, 2>(g, rpw, once); break;
+    case 3: launch_ksplit<MT, 3>(g, rpw, once); break;
+    default: launch_ksplit<MT, 5>(g, rpw, once); break;
+    }
 }
 
 template <int MW, int NW, int TJ>
@@ -648,13 +642,17 @@ hipError_t launch_tiles(const GemmArgs &g, uint32_t mt, uint32_t nt, uint32_t fi
     return hipGetLastError();
 }
 
-} // namespace
+// Which kernel, with which tiles, serves a shape.
+struct Choice {
+    int kernel;                      // QP_BLOCKSCALE_*
+    uint32_t mt, rpw;                // ksplit: MT and rows of W per workgroup
+    bool once;                       // ksplit: W past the caches
+    uint32_t mtiles, ntiles;         // tiles: the grid of them,
+    uint32_t full;                   // 256 x 256: those before the quarters
+};
 
-hipError_t launch_fp8_gemm_blockscale(const uint8_t *a, const float *as, const uint8_t *w,
-                                      const float *ws, uint16_t *out, uint32_t m, uint32_t n,
-                                      uint32_t k, hipStream_t st)
+Choice choose(uint32_t m, uint32_t n, uint32_t k)
 {
-    const GemmArgs g = {a, as, w, ws, out, m, n, k, st};
     const uint32_t cus = cu_count() ? cu_count() : 256, nb = (k + 127) / 128;
 
     // Time estimates in tenths of a nanosecond, fitted to 36 shapes from 17 x 512
@@ -674,7 +672,7 @@ hipError_t launch_fp8_gemm_blockscale(const uint8_t *a, const float *as, const u
         const uint32_t mwg = (m + 16 * mt - 1) / (16 * mt), per = cus > mwg ? cus / mwg : 1;
         const uint32_t rounds_n = (uint32_t)((n + 80ull * per - 1) / (80ull * per));
         const uint32_t share = (uint32_t)((n + (uint64_t)rounds_n * per - 1) / ((uint64_t)rounds_n * per));
-        const uint32_t rows = (share + 3) / 4 * 4, nt = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 48 ? 3 : 5;
+        const uint32_t rows = (share + 3) / 4 * 4, nt = ks_columns(rows);
         const uint64_t wgs = (uint64_t)mwg * ((n + rows - 1) / rows);
         const uint64_t t = 23000 + (wgs + cus - 1) / cus *
                                        (8800 + 1180 * mt * nt +
@@ -700,22 +698,53 @@ hipError_t launch_fp8_gemm_blockscale(const uint8_t *a, const float *as, const u
     const uint64_t t_large = 58000 + (full + cus - 1) / cus * 16800ull * nb + (quarter ? t_small(4 * tail) : 0);
 
     if (t_ks <= t_small(small) && t_ks <= t_large) {
-        if (mtk == 1)
-            launch_ksplit_rows<1>(g, rpw);
-        else if (mtk == 2)
-            launch_ksplit_rows<2>(g, rpw);
-        else if (mtk == 3)
-            launch_ksplit_rows<3>(g, rpw);
+        // W past the caches (nontemporal) where it is read once and no cache would
+        // have kept it: 16 x 152064 x 5120 136 us against 151; 4 x 17408 x 5120, cold,
+        // 17.1 against 19.1.  A small weight that is in the 256 MB memory-side cache
+        // stays there otherwise (1 x 5120 x 5120: 6.7 us against 8.0), and with more
+        // rows the gain is small (37 x 5120 x 17408, cold: 27.6 against 28.6; cached:
+        // 26.6 against 24.1), so those pass it only when larger than that cache.
+        const bool once = m <= 16 * mtk && (uint64_t)n * k >= (mtk == 1 ? 1u << 26 : 1u << 28);
+        return {QP_BLOCKSCALE_KSPLIT, mtk, rpw, once, 0, 0, 0};
+    }
+    if (full == 0 || t_small(small) <= t_large)
+        return {QP_BLOCKSCALE_TILES_128, 0, 0, false, ms, ns, (uint32_t)small};
+    return {quarter ? QP_BLOCKSCALE_TILES_256_QUARTERS : QP_BLOCKSCALE_TILES_256, 0, 0, false, ml, nl, (uint32_t)full};
+}
+
+} // namespace
+
+int fp8_gemm_blockscale_kernel(uint32_t m, uint32_t n, uint32_t k)
+{
+    const Choice c = choose(m, n, k);
+    return c.kernel == QP_BLOCKSCALE_KSPLIT ? c.kernel + (int)(c.mt + 8 * ks_columns(c.rpw) + 64 * c.once) : c.kernel;
+}
+
+hipError_t launch_fp8_gemm_blockscale(const uint8_t *a, const float *as, const uint8_t *w,
+                                      const float *ws, uint16_t *out, uint32_t m, uint32_t n,
+                                      uint32_t k, hipStream_t st)
+{
+    const GemmArgs g = {a, as, w, ws, out, m, n, k, st};
+    const Choice c = choose(m, n, k);
+    if (c.kernel == QP_BLOCKSCALE_KSPLIT) {
+        if (c.mt == 1)
+            launch_ksplit_rows<1>(g, c.rpw, c.once);
+        else if (c.mt == 2)
+            launch_ksplit_rows<2>(g, c.rpw, c.once);
+        else if (c.mt == 3)
+            launch_ksplit_rows<3>(g, c.rpw, c.once);
         else
-            launch_ksplit_rows<4>(g, rpw);
+            launch_ksplit_rows<4>(g, c.rpw, c.once);
         count_launch();
         return hipGetLastError();
     }
-    if (full == 0 || t_small(small) <= t_large)
-        return launch_tiles<2, 2, 4>(g, ms, ns, 0, (uint32_t)small, false);
-    if (const hipError_t e = launch_tiles<4, 2, 8>(g, ml, nl, 0, (uint32_t)full, false))
+    if (c.kernel == QP_BLOCKSCALE_TILES_128)
+        return launch_tiles<2, 2, 4>(g, c.mtiles, c.ntiles, 0, c.full, false);
+    if (const hipError_t e = launch_tiles<4, 2, 8>(g, c.mtiles, c.ntiles, 0, c.full, false))
         return e;
-    return quarter ? launch_tiles<2, 2, 4>(g, ml, nl, (uint32_t)full, (uint32_t)tail, true) : hipSuccess;
+    if (c.kernel == QP_BLOCKSCALE_TILES_256)
+        return hipSuccess;
+    return launch_tiles<2, 2, 4>(g, c.mtiles, c.ntiles, c.full, c.mtiles * c.ntiles - c.full, true);
 }
 
 } // namespace qp

@@ -60,6 +60,8 @@ hipError_t launch_silu_mul_quant(const uint16_t *gate_up, int fmt, void *q, floa
 hipError_t launch_fp8_gemm_blockscale(const uint8_t *a, const float *as, const uint8_t *w,
                                       const float *ws, uint16_t *out, uint32_t m, uint32_t n,
                                       uint32_t k, hipStream_t st);
+// An enum qp_blockscale_kernel value (see its declaration).
+int fp8_gemm_blockscale_kernel(uint32_t m, uint32_t n, uint32_t k);
 // work: moe_fp8_workspace() bytes, 16-byte aligned.
 uint64_t moe_fp8_workspace(uint32_t T, uint32_t topk, uint32_t I);
 hipError_t launch_moe_fp8(const uint16_t *x, const float *logits, const uint8_t *w13,

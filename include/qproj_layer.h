@@ -95,6 +95,19 @@ int fp8_gemm_blockscale(const uint8_t *a, const float *a_scale, const uint8_t *w
                         const float *block_scale, uint16_t *out, uint32_t m,
                         uint32_t n, uint32_t k, void *stream);
 
+/* The kernel that fp8_gemm_blockscale runs for a shape on the current device
+ * (256 compute units where there is none): one of the values below, or
+ * QP_ERR_SHAPE.  QP_BLOCKSCALE_KSPLIT is a base, to which are added the rows
+ * of A in 16s and, times 8, the rows of W in 16s that a workgroup takes, and 64
+ * where W is read past the caches.  Informative: for tests and profiles. */
+enum qp_blockscale_kernel {
+    QP_BLOCKSCALE_TILES_128 = 1,          /* 128 x 128 tiles                       */
+    QP_BLOCKSCALE_TILES_256 = 2,          /* 256 x 256 tiles                       */
+    QP_BLOCKSCALE_TILES_256_QUARTERS = 3, /* the same, the last as 128 x 128 ones  */
+    QP_BLOCKSCALE_KSPLIT = 256            /* small tiles, K split over the waves   */
+};
+int fp8_gemm_blockscale_kernel(uint32_t m, uint32_t n, uint32_t k);
+
 /* ------------------------------------------------------------------------
  * A mixture-of-experts layer for the few tokens of a decode or verify step,
  * in two launches.
