@@ -458,6 +458,16 @@ __global__ __launch_bounds__(256) void k_quant_rowwise_fp8_long(
 hipError_t launch_quant_rowwise_fp8(const uint16_t *x, uint8_t *q, float *s,
                                     uint32_t rows, uint32_t k, hipStream_t st)
 {
+    // A launch holds fewer than 2^32 threads (one with more loses rows without
+    // an error), and a row takes 64 of them or more: rows of 16 values, which
+    // may number 2^26 and more, go in several launches.
+    constexpr uint32_t MOST = 1u << 25;
+    if (rows > MOST) {
+        if (const hipError_t e = launch_quant_rowwise_fp8(x, q, s, MOST, k, st))
+            return e;
+        const size_t at = (size_t)MOST * k;
+        return launch_quant_rowwise_fp8(x + at, q + at, s + MOST, rows - MOST, k, st);
+    }
     const uint32_t nch = k / 8;
     const dim3 gw((rows + 3) / 4), b(256);
 #define QP_ROW_WAVE(C)                                                                        \

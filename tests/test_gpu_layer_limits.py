@@ -45,3 +45,22 @@ def test_a_missing_scale_is_a_type_error(fmt):
         qp.rmsnorm_residual_quant(x, None, w, 1e-6, fmt, q, None)
     with pytest.raises(TypeError, match="scale"):
         qp.silu_mul_quant(_normal((2, 512), 5), fmt, q, None)
+
+
+def test_rowwise_quantizer_of_more_rows_than_one_launch_holds():
+    """quant_rowwise_fp8 gives a row a wave as well."""
+    rows, k, piece = (1 << 26) + 3, 16, 1 << 20
+    g = torch.Generator(device=DEV).manual_seed(6)
+    x = torch.empty((rows, k), dtype=torch.bfloat16, device=DEV)
+    for at in range(0, rows, 1 << 22):
+        x[at:at + (1 << 22)].normal_(generator=g)
+    q, s = torch.full((rows, k), 0x5A, dtype=torch.uint8, device=DEV), torch.full((rows,), float("nan"), device=DEV)
+    qp.quant_rowwise_fp8(x, q, s)
+    torch.cuda.synchronize()
+    for at in (0, (1 << 25) - piece // 2, (1 << 26) - piece // 2, rows - piece):
+        part = slice(at, min(at + piece, rows))
+        q1, s1 = torch.zeros_like(q[part]), torch.zeros_like(s[part])
+        qp.quant_rowwise_fp8(x[part], q1, s1)
+        torch.cuda.synchronize()
+        assert torch.equal(q1, q[part]) and torch.equal(s1, s[part])
+    assert bool(torch.isfinite(s).all())
