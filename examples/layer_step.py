@@ -11,7 +11,8 @@ Two layers on one residual stream:
            library and the router's product, up to 16 rows)
 
 Weights are random; each layer is checked against plain torch operations and
-timed.  Every buffer is allocated once and reused, as a serving program would.
+timed.  The layers' buffers are allocated once and reused, as a serving program
+would; only the router's product, which is torch's, takes a temporary.
 """
 from __future__ import annotations
 

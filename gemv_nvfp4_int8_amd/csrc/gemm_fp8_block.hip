@@ -48,9 +48,9 @@ namespace {
 // wave's row l for each; a block's four values per lane (its rows 16t + l%16)
 // come from three lane swaps.
 //
-// Measured: 8192 x 12288 x 5120: 453 us, 2.28 PFLOP/s; 4096 x 5120 x 17408: 333
-// us, 2.19; 600 x 4104 x 2368 (128 x 128 tiles): 14.8 us.  Bound by issue and
-// power: the MFMAs take 57% of the cycles and the vector ALU 48%, four of its
+// Measured: 8192 x 12288 x 5120: 445 to 490 us from box to box, 2.1 to 2.3
+// PFLOP/s; 4096 x 5120 x 17408: 327 to 340 us, 2.2; 600 x 4104 x 2368 (128 x 128
+// tiles): 15.0 us.  Bound by issue and power: the MFMAs take 57% of the cycles and the vector ALU 48%, four of its
 // 6.7 instructions per MFMA being the fold, at a shader clock of 1.77 GHz.
 // ---------------------------------------------------------------------------
 constexpr uint32_t FB_OOB = 0x80000000u;
@@ -401,8 +401,8 @@ __global__ __launch_bounds__(64 * MW * NW) void k_fp8_gemm_block_tiles(
 // them.  The waves take runs of four K blocks in turn (512 bytes of a row, some
 // of it in flight at once: 28.2 us against 29.0 with single blocks in turn, 28.9
 // with runs of eight; 37 x 5120 x 17408), or single ones where there is at most
-// one for each (75 x 4224 x 224: 6.1 against 7.4); each wave DMAs its blocks' panels into
-// its own ring of D slots and waits for nothing but its own loads, so there is
+// one for each (75 x 4224 x 224: 6.1 against 7.4 when that came in, 4.3 with the
+// choice of rows that followed); each wave DMAs its blocks' panels into its own ring of D slots and waits for nothing but its own loads, so there is
 // no barrier until the NW partial tiles are joined through LDS, in wave order.
 // (Fragments loaded straight to registers, 16 rows of 64 bytes to an
 // instruction, were half as fast: 8 rows of whole 128-byte lines are what the
@@ -413,8 +413,8 @@ __global__ __launch_bounds__(64 * MW * NW) void k_fp8_gemm_block_tiles(
 //
 // Bound by W's way from HBM and, behind that, the waves' own work on a block,
 // which overlap in part: 37 x 5120 x 17408 takes 28 us, with W in the caches
-// (the same instructions) 17; the bytes alone 14.5.  4 x 17408 x 5120: 16.5 us,
-// 5.4 TB/s; 16 x 152064 x 5120: 136 us, 5.8 TB/s.
+// (the same instructions) 17; the bytes alone 14.5.  4 x 17408 x 5120: 16.4 us,
+// 5.4 TB/s; 16 x 152064 x 5120: 129 to 136 us, 5.8 to 6.1 TB/s.
 // ---------------------------------------------------------------------------
 template <int MT, int NT, int NW, int D, bool ONCE>
 __global__ __launch_bounds__(64 * NW) void k_fp8_gemm_block_ksplit(
@@ -656,8 +656,12 @@ Choice choose(uint32_t m, uint32_t n, uint32_t k)
     const uint32_t cus = cu_count() ? cu_count() : 256, nb = (k + 127) / 128;
 
     // Time estimates in tenths of a nanosecond, fitted to 36 shapes from 17 x 512
-    // x 4096 to 6599 x 256 x 8448 with every kernel on each (one MI355X; the
-    // choice costs 1% against the best of them).  ksplit, per round of its
+    // x 4096 to 6599 x 256 x 8448 with every kernel on each (one MI355X).  The
+    // choice costs 1% against the best of them in the mean, at the worst 13 to
+    // 20% (989 x 296 x 16384).  They rank the kernels and are no forecast: there is
+    // no term for the bytes that a share takes from L2 and HBM, so that where those
+    // bound a call the estimate is low (37 x 17408 x 5120 16.8 for 22.9 us, 16 x
+    // 152064 x 5120 75 for 129, 7218 x 1641 x 384 8.6 for 13.9).  ksplit, per round of its
     // workgroups: a start and an end that grow with the tile, and per K block
     // 8.5 ns for 8 rows of A, 12.9 for 8 of W and 9.1 for a 16 x 16 tile.  It
     // takes 16 to 64 rows of A a workgroup, whatever suits the shape: 64 x 5120

@@ -31,9 +31,10 @@
 //    token's sum over its experts needs no atomics and has a fixed order.
 //
 // Measured (both launches, replayed from a graph): 16 tokens, 6 of 64 experts,
-// 5120 x 1408: 192 us, 5.7 TB/s of weights (124 us and 76 us; one read of them
-// at 6.2 TB/s: 177 us); 5 tokens, 2 of 8, 4096 x 8192: 109 us, 5.6 TB/s; 1
-// token, 8 of 128, 2048 x 768: 14.0 us (8.7 and 6.4), where each launch is
+// 5120 x 1408: 192 to 201 us by the experts chosen, 5.7 TB/s of weights (in a
+// kernel trace, which slows them, 122 and 78 us; one read of the weights at 6.2
+// TB/s: 177 us); 5 tokens, 2 of 8, 4096 x 8192: 109 us, 5.6 TB/s; 1 token, 8 of
+// 128, 2048 x 768: 14.1 us (traced 8.7 and 6.4), where each launch is
 // mostly its start, the choice of the first expert and one trip to HBM.
 #include "qp_device.hpp"
 #include "qp_launch.hpp"
