@@ -9,8 +9,10 @@ fallback.  If ``libqproj.so`` has not been built, the first call into the
 library raises ImportError (build it with ``__graft_entry__.build()`` or
 ``python -m gemv_nvfp4_int8_amd._build``).
 
-The operations and their rounding rules are documented in include/qproj.h and
-(the operators around the projections) include/qproj_layer.h.
+The operations and their rounding rules are documented in include/qproj.h,
+(the operators around the projections) include/qproj_layer.h and (rotary
+positions, paged cache, attention and log probabilities)
+include/qproj_decoder.h.
 """
 from __future__ import annotations
 
@@ -48,6 +50,22 @@ QP_BLOCKSCALE_TILES_256 = 2
 QP_BLOCKSCALE_TILES_256_QUARTERS = 3
 QP_BLOCKSCALE_KSPLIT = 256
 
+QP_KV_BF16 = 0
+QP_KV_FP8_ROW = 1
+
+QP_ROPE_HALF = 0
+QP_ROPE_INTERLEAVED = 1
+
+QP_ROPE_PLAIN = 0
+QP_ROPE_LINEAR = 1
+QP_ROPE_BASE = 2
+QP_ROPE_WAVELENGTH = 3
+QP_ROPE_RAMP = 4
+
+QP_LOGITS_BF16 = 0
+QP_LOGITS_F32 = 1
+QP_LOGPROBS_MAX_TOP = 32
+
 QP_TILES_BANDED = 0
 QP_TILES_MFAST = 1
 QP_TILES_NFAST = 2
@@ -73,6 +91,7 @@ def lib() -> ctypes.CDLL:
                 "fallback path")
         L = ctypes.CDLL(LIB_PATH)
         P, U, F, I = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_float, ctypes.c_int
+        D, Q = ctypes.c_double, ctypes.c_uint64
         PP = ctypes.POINTER(ctypes.c_void_p)
         sig = {
             "requant_w_nvfp4_int8": [P, P, F, P, P, U, U, P],
@@ -98,6 +117,10 @@ def lib() -> ctypes.CDLL:
             "fp8_gemm_blockscale": [P, P, P, P, P, U, U, U, P],
             "fp8_gemm_blockscale_kernel": [U, U, U],
             "moe_fp8_blockscale": [P, P, P, P, P, P, P, ctypes.c_uint64, P, U, U, U, U, U, I, P],
+            "rope_inv_freq": [P, U, D, I, D, D, D, U],
+            "qk_norm_rope_cache": [P, P, P, F, P, P, F, I, U, P, I, P, P, P, P, P, U, U, U, U, U, U, P],
+            "paged_attention": [P, I, P, P, P, P, P, P, P, F, U, P, Q, P, U, U, U, U, U, U, U, U, U, P],
+            "token_logprobs": [P, I, P, P, P, P, P, P, Q, U, U, U, P],
             "qproj_cache_create": [PP],
             "qproj_cache_destroy": [P],
             "qproj_cache_evict": [P, P],
@@ -119,6 +142,10 @@ def lib() -> ctypes.CDLL:
         L.qproj_noalloc_scratch_bytes.argtypes = []
         L.moe_fp8_blockscale_workspace.restype = ctypes.c_uint64
         L.moe_fp8_blockscale_workspace.argtypes = [U, U, U]
+        L.paged_attention_workspace.restype = ctypes.c_uint64
+        L.paged_attention_workspace.argtypes = [U, U, U, U, U, U]
+        L.token_logprobs_workspace.restype = ctypes.c_uint64
+        L.token_logprobs_workspace.argtypes = [U, U, U]
         L.qproj_abi_version.restype = ctypes.c_int
         L.qproj_abi_version.argtypes = []
         _lib = L
@@ -169,6 +196,27 @@ def _need(t: torch.Tensor, name: str, dtypes, shape):
         raise ValueError(f"{name}: must be contiguous")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+
+
+def _ptr_or_null(t):
+    return None if t is None else t.data_ptr()
+
+
+def _one_device(*tensors):
+    """The one device index of the tensors given (None is passed over)."""
+    devices = {t.get_device() for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError(f"tensors on several devices: {sorted(devices)}")
+    return devices.pop()
+
+
+def _on_device(device, *tensors):
+    """Every tensor given is on `device`, and that is the current device."""
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors on devices {device} and {t.get_device()}")
+    if torch._C._cuda_getDevice() != device:
+        raise ValueError(f"tensors on device {device}, which is not the current one")
 
 
 def _check(fn: str, status: int):
@@ -527,6 +575,127 @@ def moe_fp8_blockscale(x, router_logits, w13, s13, w2, s2, topk, renormalize, wo
         _stream(stream)))
 
 
+def rope_inv_freq(rot, base, scaling=QP_ROPE_PLAIN, factor=1.0, low=0.0, high=0.0, original=0):
+    """The rotary frequencies [rot/2] (F32, a host tensor) of base^(-2i/rot),
+    scaled (QP_ROPE_*) for contexts `factor` times the model's `original` one."""
+    out = torch.empty(max(int(rot) // 2, 0), dtype=torch.float32)
+    _check("rope_inv_freq", lib().rope_inv_freq(
+        _ptr(out), int(rot), float(base), int(scaling), float(factor), float(low), float(high),
+        int(original)))
+    return out
+
+
+class KVCache:
+    """A paged cache in the caller's tensors: k and v [pages, kv_heads,
+    page_size, d], BF16, or E4M3 with F32 scales [pages, kv_heads, page_size].
+    Checked once, here; the tensors stay the caller's and are kept referenced."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        self.pages, self.kv_heads, self.page_size, self.d = k.shape
+        self.fmt = QP_KV_BF16 if k.dtype in BF16 else QP_KV_FP8_ROW
+        for name, t, scale in (("k", k, k_scale), ("v", v, v_scale)):
+            _need(t, name, BF16 if self.fmt == QP_KV_BF16 else U8, k.shape)
+            if self.fmt == QP_KV_FP8_ROW:
+                _need(scale, name + "_scale", F32, k.shape[:3])
+            elif scale is not None:
+                raise ValueError(f"{name}_scale: a BF16 cache has none")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = _one_device(k, v, k_scale, v_scale)
+        self._args = (self.fmt, _ptr(k), _ptr(v), _ptr_or_null(k_scale), _ptr_or_null(v_scale))
+
+
+def qk_norm_rope_cache(qkv, q_norm, k_norm, eps, positions, inv_freq, rope_scale, layout, slots, cache,
+                       q_out, stream=None):
+    """Norms of queries and keys for each head (q_norm and k_norm None: none),
+    the first 2 * len(inv_freq) entries of each turned by position * inv_freq
+    (layout QP_ROPE_HALF or QP_ROPE_INTERLEAVED; inv_freq None: not turned),
+    the queries written to q_out [t, q_heads, d], keys and values to the
+    KVCache at their slots (page * page_size + offset; -1: to none)."""
+    t, q_heads, d = q_out.shape
+    kv = cache.kv_heads
+    if d != cache.d:
+        raise ValueError(f"q_out: head size {d}, the cache's is {cache.d}")
+    _need(qkv, "qkv", BF16, (t, (q_heads + 2 * kv) * d))
+    _need(q_out, "q_out", BF16, (t, q_heads, d))
+    _need(positions, "positions", I32, (t,))
+    _need(slots, "slots", I32, (t,))
+    half = 0
+    if inv_freq is not None:
+        half = inv_freq.numel()
+        _need(inv_freq, "inv_freq", F32, (half,))
+    if q_norm is not None:
+        _need(q_norm, "q_norm", BF16, (d,))
+    if k_norm is not None:
+        _need(k_norm, "k_norm", BF16, (d,))
+    _on_device(cache.device, qkv, q_out, positions, slots, inv_freq, q_norm, k_norm)
+    _check("qk_norm_rope_cache", lib().qk_norm_rope_cache(
+        _ptr(qkv), _ptr_or_null(q_norm), _ptr_or_null(k_norm), float(eps), _ptr(positions),
+        _ptr_or_null(inv_freq), float(rope_scale), int(layout), 2 * half, _ptr(slots), *cache._args,
+        _ptr(q_out), t, q_heads, kv, d, cache.pages, cache.page_size, _stream(stream)))
+
+
+def paged_attention_workspace(t, seqs, max_q, q_heads, kv_heads, d) -> int:
+    """Bytes of scratch paged_attention needs for t rows of seqs sequences with
+    at most max_q rows each."""
+    return int(lib().paged_attention_workspace(t, seqs, max_q, q_heads, kv_heads, d))
+
+
+def paged_attention(q, cache, page_table, q_start, kv_len, max_q, scale, window, workspace, out,
+                    stream=None):
+    """Attention of the rows q_start[s]..q_start[s+1]-1 of q [t, q_heads, d],
+    the last of sequence s's kv_len[s] positions, over that sequence's pages
+    page_table[s] of the KVCache; window 0: over all positions up to the
+    row's own, else over the last `window` of them."""
+    t, q_heads, d = q.shape
+    seqs, width = page_table.shape
+    if d != cache.d:
+        raise ValueError(f"q: head size {d}, the cache's is {cache.d}")
+    _need(q, "q", BF16, (t, q_heads, d))
+    _need(out, "out", BF16, (t, q_heads, d))
+    _need(page_table, "page_table", I32, (seqs, width))
+    _need(q_start, "q_start", I32, (seqs + 1,))
+    _need(kv_len, "kv_len", I32, (seqs,))
+    _need(workspace, "workspace", (torch.uint8,), (workspace.numel(),))
+    _on_device(cache.device, q, out, page_table, q_start, kv_len, workspace)
+    _check("paged_attention", lib().paged_attention(
+        _ptr(q), *cache._args, _ptr(page_table), _ptr(q_start), _ptr(kv_len), float(scale), int(window),
+        _ptr(workspace), workspace.numel(), _ptr(out), t, seqs, int(max_q), q_heads, cache.kv_heads, d,
+        cache.pages, cache.page_size, width, _stream(stream)))
+
+
+def token_logprobs_workspace(rows, vocab, top) -> int:
+    """Bytes of scratch token_logprobs needs."""
+    return int(lib().token_logprobs_workspace(rows, vocab, top))
+
+
+def token_logprobs(logits, targets, logprob, entropy, top_ids, top_logprobs, workspace, stream=None):
+    """Log probabilities of `targets` [rows] under logits [rows, vocab] (BF16 or
+    F32) into logprob [rows], the entropy into entropy [rows], the most probable
+    tokens and their log probabilities into top_ids and top_logprobs
+    [rows, top].  Targets with logprob, entropy, and the last two may be None."""
+    rows, vocab = logits.shape
+    f32 = isinstance(logits, torch.Tensor) and logits.dtype == torch.float32
+    _need(logits, "logits", F32 if f32 else BF16, (rows, vocab))
+    top = 0
+    if targets is not None:
+        _need(targets, "targets", I32, (rows,))
+    if logprob is not None:
+        _need(logprob, "logprob", F32, (rows,))
+    if entropy is not None:
+        _need(entropy, "entropy", F32, (rows,))
+    if top_ids is not None or top_logprobs is not None:
+        _need(top_ids, "top_ids", I32, (rows, top_ids.shape[-1] if isinstance(top_ids, torch.Tensor) else 0))
+        top = top_ids.shape[1]
+        _need(top_logprobs, "top_logprobs", F32, (rows, top))
+    _need(workspace, "workspace", (torch.uint8,), (workspace.numel(),))
+    _on_device(_one_device(logits), targets, logprob, entropy, top_ids, top_logprobs, workspace)
+    _check("token_logprobs", lib().token_logprobs(
+        _ptr(logits), QP_LOGITS_F32 if f32 else QP_LOGITS_BF16, _ptr_or_null(targets),
+        _ptr_or_null(logprob), _ptr_or_null(entropy), _ptr_or_null(top_ids) if top else None,
+        _ptr_or_null(top_logprobs) if top else None, _ptr(workspace), workspace.numel(), rows, vocab,
+        top, _stream(stream)))
+
+
 class DerivedWeights:
     """A derived-weight cache (the library's qp_cache): weights requantised on
     first use and kept, keyed by the source weight's device address
@@ -620,6 +789,9 @@ __all__ = [
     "fp8_gemm_rowscale", "fp8_rowwise_proj", "fp8_gemv_rowscale",
     "fp8_gemv_blockscale", "w4a16_gemv", "rmsnorm_residual_quant",
     "silu_mul_quant", "fp8_gemm_blockscale", "fp8_gemm_blockscale_kernel",
-    "moe_fp8_blockscale", "moe_fp8_blockscale_workspace", "DerivedWeights",
+    "moe_fp8_blockscale", "moe_fp8_blockscale_workspace", "rope_inv_freq",
+    "KVCache", "qk_norm_rope_cache", "paged_attention",
+    "paged_attention_workspace", "token_logprobs", "token_logprobs_workspace",
+    "DerivedWeights",
     "launch_count", "status_string", "abi_version", "lib", "QProjError",
 ]
