@@ -1,0 +1,138 @@
+// attn_common.hpp -- what the attention kernels share: how a call's work is cut
+// into equal shares, and where partial results go.
+//
+// A UNIT is a run of rows that read the same keys: up to `ROWS` of a sequence's
+// rows times its query heads of one kv head, flattened (row r of a unit is token
+// r / group, head r % group of the sequence's rows).  Its work is the TILES of
+// keys that any of its rows sees.  All units' tiles in one line are dealt to the
+// workgroups in equal, contiguous shares, so that sequences of different lengths
+// need no balancing and a single long one fills the chip.  A unit that lies
+// within one share is finished there; of one that does not, each share leaves its
+// running maximum, sum and unnormalised output in the workspace, and a second
+// launch joins them in the order of the keys (no atomics: the result does not
+// depend on timing).  A share continues at most one unit that began before it
+// (slot 2w) and begins at most one that ends after it (slot 2w + 1).
+#pragma once
+
+#include "qp_device.hpp"
+#include "decoder.hpp"
+
+namespace qp {
+namespace attn {
+
+constexpr float LOG2E = 1.4426950408889634f;
+
+// One entry per share: the unit that it began and did not finish.
+struct Begun {
+    int32_t last;        // the share that holds the unit's last tile; -1: no such unit
+    int32_t token;       // the row of q of the sequence's first row
+    int32_t row;         // the unit's first flattened row
+    int32_t rows;        // its rows
+    int32_t head;        // its kv head
+    int32_t pad[3];
+};
+
+// The workspace of `shares` shares of units of up to `rows` rows.
+struct Parts {
+    Begun *begun;        // [shares]
+    f32x2 *ml;           // [2 shares][rows]: maximum (of base-2 scores) and sum
+    float *o;            // [2 shares][rows][d]
+};
+
+inline uint64_t parts_bytes(uint64_t shares, uint64_t rows, uint64_t d)
+{
+    return shares * sizeof(Begun) + 2 * shares * rows * (8 + 4 * d);
+}
+
+inline Parts parts_at(void *work, uint64_t shares, uint64_t rows)
+{
+    uint8_t *p = (uint8_t *)work;
+    Parts r;
+    r.begun = (Begun *)p;
+    r.ml = (f32x2 *)(p + shares * sizeof(Begun));
+    r.o = (float *)(p + shares * sizeof(Begun) + 2 * shares * rows * 8);
+    return r;
+}
+
+// A value of a read-only array at an index that is the same in the whole wave.
+__device__ __forceinline__ int32_t uniform_load(const int32_t *p, size_t i)
+{
+    return ((const __attribute__((address_space(4))) int32_t *)p)[i];
+}
+
+// A value that is the same in the whole wave, in scalars.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint64_t uniform(uint64_t v)
+{
+    return (uint64_t)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v);
+}
+
+// A sequence as the host's arrays give it; n = 0 where its numbers do not fit.
+struct Seq {
+    int token, n, len;       // first row, rows, positions
+    int first;               // the first position that any row sees
+};
+
+__device__ __forceinline__ Seq read_seq(const AttnArgs &a, uint32_t s)
+{
+    Seq q;
+    const int lo = a.q_start[s], hi = a.q_start[s + 1], len = a.kv_len[s];
+    const bool ok = lo >= 0 && hi > lo && (uint32_t)hi <= a.t && (uint32_t)(hi - lo) <= a.max_q && len >= 0 &&
+                    (uint32_t)len <= a.width << a.cache.page_log2;
+    q.token = lo;
+    q.n = ok ? hi - lo : 0;
+    q.len = ok ? len : 0;
+    const int64_t back = (int64_t)q.len - q.n - (int64_t)a.window + 1;
+    q.first = a.window && back > 0 ? (int)back : 0;
+    return q;
+}
+
+// The same for a sequence number that is the same in the whole wave, in scalars.
+__device__ __forceinline__ Seq read_seq_uniform(const AttnArgs &a, uint32_t s)
+{
+    Seq q = read_seq(a, s);
+    q.token = __builtin_amdgcn_readfirstlane(q.token);
+    q.n = __builtin_amdgcn_readfirstlane(q.n);
+    q.len = __builtin_amdgcn_readfirstlane(q.len);
+    q.first = __builtin_amdgcn_readfirstlane(q.first);
+    return q;
+}
+
+// Bits of two BF16 values that are NaN or infinite, as 0xFFFF masks.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w)
+{
+    return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+}
+
+// Eight E4M3 codes as BF16 (exact: three bits of significand, exponents that fit).
+__device__ __forceinline__ u32x4 bf16_of_e4m3(u32x2 c)
+{
+    auto two = [](uint32_t w, bool hi) {
+        return hi ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true))
+                  : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+    };
+    return (u32x4){two(c[0], false), two(c[0], true), two(c[1], false), two(c[1], true)};
+}
+
+// The share that holds tile x of n tiles dealt to `shares` shares, share w
+// taking tiles w * n / shares .. (w + 1) * n / shares - 1.
+__device__ __forceinline__ uint32_t share_of(uint64_t x, uint64_t n, uint64_t shares)
+{
+    return (uint32_t)(((x + 1) * shares - 1) / n);
+}
+
+// Joins the parts of the units that were begun in one share and finished in
+// others (attn_decode.hip); `rows` of a part, of which `live` at most are used.
+hipError_t launch_attn_join(const AttnArgs &a, const Parts &p, uint32_t shares, uint32_t rows, uint32_t live,
+                            hipStream_t st);
+
+// Rows of a sequence times heads of a kv head up to DECODE_ROWS: attn_decode.hip;
+// more: attn_tiles.hip.
+constexpr uint32_t DECODE_ROWS = 16;
+uint64_t decode_work(uint32_t d);
+hipError_t launch_attn_decode(const AttnArgs &a, hipStream_t st);
+uint64_t tiles_work(uint32_t d);
+hipError_t launch_attn_tiles(const AttnArgs &a, hipStream_t st);
+
+} // namespace attn
+} // namespace qp

@@ -1,0 +1,636 @@
+// attn_decode.hip -- attention of few rows a sequence (decode, verify batches),
+// which reads the cache once and has little else to do.
+//
+// A wave takes 32 keys at a time and needs neither LDS nor barriers for them:
+//   S^T [key, row] = K Q^T   two 16x16x32 MFMAs (16 keys each) for every 32 of d;
+//                            K goes from memory to the operand's registers, 64
+//                            bytes of 16 rows a load
+//   P^T = exp2(S^T - m)      a lane holds 8 scores of ONE row, so maximum and sum
+//                            are its own; the maximum is shared with the row's
+//                            three other lanes only when it grows by more than 2^8
+//   O^T [d, row] += V^T P^T  P^T is already in the layout of the operand: key slot
+//                            (lane/16, i) stands for key 4 (lane/16) + i of the
+//                            first 16 (i < 4) or the second; V is loaded in whole
+//                            rows, 4 keys a load, and turned with byte permutes
+// so that a wave's only traffic is the cache itself: while one 32 keys are
+// worked on, the next are on their way (K is fetched again as soon as its
+// products are issued, V as soon as its own are).  The four waves of a workgroup
+// take every fourth 32 keys and join through LDS at a unit's end.
+#include "attn_common.hpp"
+#include "qp_launch.hpp"
+
+namespace qp {
+namespace attn {
+namespace {
+
+constexpr uint32_t WAVES = 4, WG = 64 * WAVES;
+constexpr uint32_t STEP = 32;              // keys of a wave's step
+constexpr uint32_t TILE = STEP * WAVES;    // keys of a workgroup's step, the unit of the shares
+
+__device__ __forceinline__ uint32_t tiles_of(const Seq &q)
+{
+    if (q.n == 0)
+        return 0;
+    const uint32_t from = q.first / TILE, to = (q.len + TILE - 1) / TILE;
+    return max(to - from, 1u);             // rows that see nothing are still written
+}
+
+template <int EPT>
+__device__ __forceinline__ void load_elements(const uint8_t *p, uint32_t *w)
+{
+    // EPT dwords
+    if constexpr (EPT == 1) {
+        w[0] = *(const uint32_t *)p;
+    } else if constexpr (EPT == 2) {
+        const u32x2 v = *(const u32x2 *)p;
+        w[0] = v[0];
+        w[1] = v[1];
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPT / 4; ++i) {
+            const u32x4 v = *(const u32x4 *)(p + 16 * i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[4 * i + j] = v[j];
+        }
+    }
+}
+
+// DP: d rounded up to 64, 128 or 256 (what lies past d is read from the head's
+// start, meets zeros of Q, and is not stored); NQ: 16s of rows.
+template <int DP, int NQ, bool FP8>
+__global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs a, Parts parts, uint32_t max_shares)
+{
+    constexpr int ROWS = 16 * NQ;
+    constexpr int KS = DP / 32;            // MFMAs over d
+    constexpr int ROWB = FP8 ? 1 : 2;      // bytes of an element
+    constexpr int EPL = DP / 16;           // elements of V of a lane and key
+    constexpr int VW = EPL * ROWB / 4;     // the same in dwords
+    constexpr int LD = DP + 4;             // LDS row, so that 16 rows spread over the banks
+    __shared__ float o_lds[WAVES][ROWS][LD];
+    __shared__ f32x2 ml_lds[WAVES][ROWS];
+    __shared__ uint32_t scan[WAVES];
+    __shared__ uint32_t found[2];
+
+    const uint32_t tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    const uint32_t col = lane % 16, quad = lane / 16;
+    const uint32_t d = a.cache.d, kv = a.cache.heads, group = a.q_heads / kv, pl = a.cache.page_log2;
+
+    // ---- the share: tiles of all sequences in one line, a sequence's heads one after the other
+    auto wave_scan = [&](uint32_t v) {                  // inclusive
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const uint32_t up = __shfl_up(v, off, 64);
+            v += lane >= (uint32_t)off ? up : 0;
+        }
+        return v;
+    };
+    uint32_t sum = 0, mine = 0;
+    for (uint32_t s = tid; s < a.seqs; s += WG) {
+        mine = tiles_of(read_seq(a, s));
+        sum += mine;
+    }
+    const uint32_t incl = wave_scan(sum);
+    if (lane == 63)
+        scan[wave] = incl;
+    __syncthreads();
+    uint64_t total = 0, ahead = 0;
+    for (uint32_t w = 0; w < WAVES; ++w) {
+        ahead += w < wave ? scan[w] : 0;
+        total += scan[w];
+    }
+    total = uniform(total * kv);
+    const uint64_t shares = min((uint64_t)max_shares, total);
+    const uint32_t w = blockIdx.x;
+    if (w >= shares) {
+        if (tid == 0)
+            parts.begun[w].last = -1;
+        return;
+    }
+    uint64_t x = uniform(w * total / shares);
+    const uint64_t share_end = uniform((w + 1) * total / shares);
+    // the sequence that holds tile x, and the first tile of it
+    uint32_t seq = 0;
+    uint64_t seq_tile = 0;
+    if (a.seqs <= WG) {
+        const uint64_t to = (ahead + incl) * kv, from = to - (uint64_t)mine * kv;
+        if (tid < a.seqs && x >= from && x < to) {
+            found[0] = tid;
+            found[1] = (uint32_t)(ahead + incl - mine);
+        }
+        __syncthreads();
+        seq = found[0];
+        seq_tile = (uint64_t)found[1] * kv;
+    } else {
+        uint64_t base = 0;
+        for (uint32_t s0 = 0; s0 < a.seqs; s0 += WG) {
+            __syncthreads();
+            const uint32_t t = s0 + tid < a.seqs ? tiles_of(read_seq(a, s0 + tid)) : 0;
+            const uint32_t in = wave_scan(t);
+            if (lane == 63)
+                scan[wave] = in;
+            if (tid == 0)
+                found[0] = ~0u;
+            __syncthreads();
+            uint64_t before = base;
+            for (uint32_t v = 0; v < WAVES; ++v) {
+                before += v < wave ? scan[v] : 0;
+                base += scan[v];
+            }
+            const uint64_t to = (before + in) * kv, from = to - (uint64_t)t * kv;
+            if (x >= from && x < to) {
+                found[0] = s0 + tid;
+                found[1] = (uint32_t)(before + in - t);
+            }
+            __syncthreads();
+            if (found[0] != ~0u)
+                break;
+        }
+        seq = found[0];
+        seq_tile = (uint64_t)found[1] * kv;
+    }
+    seq = min(uniform(seq), a.seqs - 1);
+    seq_tile = uniform(seq_tile);
+
+    bool began = false;
+    while (x < share_end) {
+        const Seq q = read_seq_uniform(a, seq);
+        const uint32_t tiles = tiles_of(q);
+        if (tiles == 0 || x >= seq_tile + (uint64_t)tiles * kv) {
+            seq_tile += (uint64_t)tiles * kv;
+            if (++seq == a.seqs)
+                break;                     // not reached unless the lengths change under the call
+            continue;
+        }
+        const uint32_t head = uniform((uint32_t)((x - seq_tile) / tiles));
+        const uint64_t unit = seq_tile + (uint64_t)head * tiles;
+        const uint32_t off = (uint32_t)(x - unit);
+        const uint32_t count = (uint32_t)min((uint64_t)(tiles - off), share_end - x);
+        const int rows = q.n * (int)group;
+
+        // ---- the unit's rows
+        bf16x8 qf[NQ][KS];
+        int pos[NQ];
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+            const uint32_t r = col + 16 * nq, tok = r / group;
+            pos[nq] = q.len - q.n + (int)tok;
+            const uint16_t *src = a.q + ((size_t)(q.token + tok) * a.q_heads + head * group + (r - tok * group)) * d;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                // what the lane's 16 bytes of K hold: 8 of every 32 of d, or (E4M3) 16 of every 64
+                const uint32_t e = FP8 ? 64 * (ks / 2) + 16 * quad + 8 * (ks % 2) : 32 * ks + 8 * quad;
+                u32x4 v = {0, 0, 0, 0};
+                if ((int)r < rows && e < d)
+                    v = *(const u32x4 *)(src + e);
+                qf[nq][ks] = __builtin_bit_cast(bf16x8, v);
+            }
+        }
+        const float scale = a.scale * LOG2E;
+        const uint32_t key_from = (q.first / TILE + off) * TILE, key_to = min(key_from + count * TILE, (uint32_t)q.len);
+        const int all_from = a.window ? q.len - (int)min(a.window, (uint32_t)q.len) : 0;   // from here every row sees ...
+        const int all_to = q.len - q.n + 1;                                                // ... up to here (exclusive)
+        const size_t page_bytes = ((size_t)d << pl) * ROWB, head_bytes = head * page_bytes;
+        const size_t table = (size_t)seq * a.width;
+        const uint32_t mask = (1u << pl) - 1;
+
+        float m[NQ], base[NQ], l[NQ];
+        f32x4 acc[NQ][EPL];
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+            m[nq] = -INFINITY;
+            base[nq] = l[nq] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j)
+                acc[nq][j] = (f32x4){0, 0, 0, 0};
+        }
+
+        u32x4 kr[2][FP8 ? KS / 2 : KS];
+        uint32_t vr[8][VW];
+        f32x4 ksc[2], vsc[2];
+        uint32_t page[2], hole = 0;        // of the step whose K is loaded
+        const uint32_t k_off = col * d * ROWB, v_off = 4 * quad * d * ROWB;
+        const uint32_t v_col = EPL * col < d ? EPL * col : 0;
+
+        auto pages = [&](uint32_t key) {
+            hole = 0;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t k = key + 16 * t;
+                // past the sequence's end nothing is looked up
+                page[t] = k < key_to ? (uint32_t)uniform_load(a.table, table + (k >> pl)) : ~0u;
+                if (page[t] >= a.cache.pages) {
+                    page[t] = 0;
+                    hole |= 1u << t;
+                }
+            }
+        };
+        auto load_k = [&](uint32_t key) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const size_t row = (key + 16 * t) & mask;
+                const uint8_t *p = (const uint8_t *)a.cache.k + (page[t] * (size_t)kv) * page_bytes + head_bytes + row * d * ROWB;
+#pragma unroll
+                for (int ks = 0; ks < (FP8 ? KS / 2 : KS); ++ks) {
+                    const uint32_t e = FP8 ? 64 * ks + 16 * quad : 32 * ks + 8 * quad;
+                    kr[t][ks] = *(const u32x4 *)(p + k_off + (e < d ? e * ROWB : 0));
+                }
+                if (FP8)
+                    ksc[t] = *(const f32x4 *)(a.cache.ks + ((page[t] * (size_t)kv + head) << pl) + row + 4 * quad);
+            }
+        };
+        auto load_v = [&](uint32_t key) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const size_t row = (key + 16 * t) & mask;
+                const uint8_t *p = (const uint8_t *)a.cache.v + (page[t] * (size_t)kv) * page_bytes + head_bytes + row * d * ROWB;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    load_elements<VW>(p + v_off + j * d * ROWB + v_col * ROWB, vr[4 * t + j]);
+                if (FP8)
+                    vsc[t] = *(const f32x4 *)(a.cache.vs + ((page[t] * (size_t)kv + head) << pl) + row + 4 * quad);
+            }
+        };
+
+        uint32_t key = key_from + STEP * wave;
+        if (key < key_to) {
+            pages(key);
+            load_k(key);
+            load_v(key);
+        }
+        for (; key < key_to; key += TILE) {
+            const uint32_t hole_now = hole;
+            // ---- scores
+            f32x4 s[NQ][2];
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    s[nq][t] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        u32x4 kw = FP8 ? bf16_of_e4m3((u32x2){kr[t][ks / 2][2 * (ks % 2)], kr[t][ks / 2][2 * (ks % 2) + 1]})
+                                       : kr[t][FP8 ? 0 : ks];
+                        s[nq][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kw), qf[nq][ks],
+                                                                           s[nq][t], 0, 0, 0);
+                    }
+                }
+            f32x4 sk[2], sv[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                sk[t] = FP8 ? ksc[t] * scale : (f32x4){scale, scale, scale, scale};
+                sv[t] = FP8 ? vsc[t] : (f32x4){1, 1, 1, 1};
+            }
+            const uint32_t next = key + TILE;
+            if (next < key_to) {
+                pages(next);
+                load_k(next);
+            }
+
+            // ---- probabilities; a step that some row sees only in part is masked
+            const bool whole = (int)key >= all_from && (int)(key + STEP) <= all_to && hole_now == 0;
+            uint32_t seen[NQ];             // bit 4t+i: the lane's row sees that key
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq) {
+                seen[nq] = 0xFF;
+                if (!whole) {
+                    seen[nq] = 0;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int k = (int)(key + 16 * t + 4 * quad) + i;
+                            const bool see = k <= pos[nq] && (!a.window || (uint32_t)(pos[nq] - k) < a.window) &&
+                                             !(hole_now >> t & 1);
+                            seen[nq] |= (uint32_t)see << (4 * t + i);
+                        }
+                }
+            }
+            bf16x8 pf[NQ];
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq) {
+                float top = -INFINITY, p[8];
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        p[4 * t + i] = s[nq][t][i] * sk[t][i];
+                        if (!whole)
+                            p[4 * t + i] = seen[nq] >> (4 * t + i) & 1 ? p[4 * t + i] : -INFINITY;
+                        top = __builtin_fmaxf(top, p[4 * t + i]);
+                    }
+                if (__any(top > m[nq] + 8.0f)) {
+                    // the row's four lanes agree on a new maximum; what was summed under the old one fades
+                    top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
+                    top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
+                    top = __builtin_fmaxf(top, m[nq]);
+                    const float to = top == -INFINITY ? 0.0f : top;
+                    const float fade = __builtin_amdgcn_exp2f(m[nq] - to);
+                    m[nq] = top;
+                    base[nq] = to;
+                    l[nq] *= fade;
+#pragma unroll
+                    for (int j = 0; j < EPL; ++j)
+                        acc[nq][j] *= fade;
+                }
+                float part = 0.0f;
+                u32x4 w4;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    p[i] = __builtin_amdgcn_exp2f(p[i] - base[nq]);
+                    part += p[i];
+                    if (FP8) {
+                        p[i] *= sv[i / 4][i % 4];
+                        if (!whole)
+                            p[i] = seen[nq] >> i & 1 ? p[i] : 0.0f;
+                    }
+                }
+                l[nq] += part;
+                // rounded to BF16, the operand's type (2^-9 of each on average over keys, as the output's own rounding)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w4[i] = pk_bf16(p[2 * i], p[2 * i + 1]);
+                pf[nq] = __builtin_bit_cast(bf16x8, w4);
+            }
+
+            // ---- V in BF16, keys that no row sees as zeros (0 times NaN is NaN)
+            uint32_t vb[8][EPL / 2];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int e = 0; e < VW; ++e) {
+                        vb[k][2 * e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[k][e], 1.0f, false));
+                        vb[k][2 * e + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[k][e], 1.0f, true));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < EPL / 2; ++e)
+                        vb[k][e] = vr[k][e];
+                }
+            }
+            uint32_t odd = 0;
+            if (!whole) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int at = (int)(key + 16 * (k / 4) + 4 * quad) + k % 4;
+                    const bool any = at >= q.first && at < q.len && !(hole_now >> (k / 4) & 1);
+#pragma unroll
+                    for (int e = 0; e < EPL / 2; ++e) {
+                        vb[k][e] = any ? vb[k][e] : 0u;
+                        odd |= not_finite(vb[k][e]);
+                    }
+                }
+            }
+            auto turned = [&](int j) {
+                // element j of the lane's 8 keys
+                constexpr uint32_t LO = 0x05040100u, HI = 0x07060302u;
+                u32x4 r;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    r[k] = __builtin_amdgcn_perm(vb[2 * k + 1][j / 2], vb[2 * k][j / 2], j % 2 ? HI : LO);
+                return r;
+            };
+            if (!whole && __any(odd != 0)) {
+                // NaN or an infinity that some rows see: it stays away from the
+                // others' sums, and makes NaN of those that see it
+#pragma unroll
+                for (int j = 0; j < EPL; ++j) {
+                    u32x4 vf = turned(j), bad;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t z = not_finite(vf[i]);
+                        bad[i] = z & 0x3F803F80u;
+                        vf[i] &= ~z;
+                    }
+#pragma unroll
+                    for (int nq = 0; nq < NQ; ++nq) {
+                        u32x4 ones;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            ones[i] = (seen[nq] >> (2 * i) & 1 ? 0x3F80u : 0u) | (seen[nq] >> (2 * i + 1) & 1 ? 0x3F800000u : 0u);
+                        const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, bad), __builtin_bit_cast(bf16x8, ones), (f32x4){0, 0, 0, 0}, 0, 0, 0);
+                        acc[nq][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, vf), pf[nq], acc[nq][j],
+                                                                             0, 0, 0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[nq][j][i] = hit[i] > 0.0f ? __builtin_nanf("") : acc[nq][j][i];
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < EPL; ++j) {
+                    const bf16x8 vf = __builtin_bit_cast(bf16x8, turned(j));
+#pragma unroll
+                    for (int nq = 0; nq < NQ; ++nq)
+                        acc[nq][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[nq], acc[nq][j], 0, 0, 0);
+                }
+            }
+            if (next < key_to)
+                load_v(next);
+        }
+
+        // ---- the four waves join; a lane holds d = EPL (4 quad + i) + j of row col
+        __syncthreads();                   // the last unit's sums have been read
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+            float sum = l[nq];
+            sum += __shfl_xor(sum, 16, 64);
+            sum += __shfl_xor(sum, 32, 64);
+            if (quad == 0)
+                ml_lds[wave][16 * nq + col] = (f32x2){m[nq], sum};
+        }
+        __syncthreads();
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+            float top = -INFINITY;
+            for (uint32_t v = 0; v < WAVES; ++v)
+                top = __builtin_fmaxf(top, ml_lds[v][16 * nq + col][0]);
+            const float f = __builtin_amdgcn_exp2f(m[nq] - (top == -INFINITY ? 0.0f : top));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float *dst = &o_lds[wave][16 * nq + col][EPL * (4 * quad + i)];
+#pragma unroll
+                for (int j = 0; j < EPL; j += 4)
+                    *(f32x4 *)(dst + j) = (f32x4){acc[nq][j][i] * f, acc[nq][j + 1][i] * f, acc[nq][j + 2][i] * f,
+                                                  acc[nq][j + 3][i] * f};
+            }
+        }
+        __syncthreads();
+        const bool finished = count == tiles;
+        const bool begins = off == 0;
+        const size_t slot = (2 * (size_t)w + begins) * ROWS;
+        for (uint32_t i = tid; i < ROWS * DP / 8; i += WG) {
+            const uint32_t r = i / (DP / 8), e = 8 * (i % (DP / 8));
+            if ((int)r >= rows || e >= d)
+                continue;
+            float top = -INFINITY, sum = 0.0f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            for (uint32_t u = 0; u < WAVES; ++u)
+                top = __builtin_fmaxf(top, ml_lds[u][r][0]);
+            const float to = top == -INFINITY ? 0.0f : top;
+            for (uint32_t u = 0; u < WAVES; ++u) {
+                sum += ml_lds[u][r][1] * __builtin_amdgcn_exp2f(ml_lds[u][r][0] - to);
+#pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    const f32x4 part = *(const f32x4 *)&o_lds[u][r][e + j];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[j + k] += part[k];
+                }
+            }
+            if (finished) {
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const uint32_t tok = r / group;
+                u32x4 y;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    y[j] = pk_bf16(v[2 * j] * inv, v[2 * j + 1] * inv);
+                *(u32x4 *)(a.out + ((size_t)(q.token + tok) * a.q_heads + head * group + (r - tok * group)) * d + e) = y;
+            } else {
+                float *dst = parts.o + (slot + r) * d + e;
+                *(f32x4 *)dst = (f32x4){v[0], v[1], v[2], v[3]};
+                *(f32x4 *)(dst + 4) = (f32x4){v[4], v[5], v[6], v[7]};
+                if (e == 0)
+                    parts.ml[slot + r] = (f32x2){top, sum};
+            }
+        }
+        if (begins && !finished) {
+            began = true;
+            if (tid == 0)
+                parts.begun[w] = {(int)share_of(unit + tiles - 1, total, shares), q.token, 0, rows, (int)head, {0, 0, 0}};
+        }
+        x += count;
+    }
+    if (!began && tid == 0)
+        parts.begun[w].last = -1;
+}
+
+// One workgroup per share and row: LP lanes take a part's row, 16 bytes each;
+// the groups of lanes take the parts in turn and join through LDS.
+template <int LP>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, Parts parts, uint32_t rows)
+{
+    constexpr uint32_t G = 256 / LP;
+    __shared__ float o_lds[G][4 * LP];
+    __shared__ f32x2 ml_lds[G];
+    const Begun b = parts.begun[blockIdx.x];
+    if (b.last < 0)
+        return;
+    const uint32_t d = a.cache.d, group = a.q_heads / a.cache.heads, g = threadIdx.x / LP, e = 4 * (threadIdx.x % LP);
+    const uint32_t from = blockIdx.x, count = b.last - from + 1;
+    for (uint32_t r = blockIdx.y; r < (uint32_t)b.rows; r += gridDim.y) {
+        float m = -INFINITY, l = 0.0f;
+        f32x4 acc = {0, 0, 0, 0};
+        constexpr int U = 4;
+        for (uint32_t p0 = g; p0 < count; p0 += U * G) {
+            f32x2 ml[U];
+            f32x4 o[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t p = p0 + u * G;
+                ml[u] = (f32x2){-INFINITY, 0.0f};
+                o[u] = (f32x4){0, 0, 0, 0};
+                if (p < count) {
+                    const size_t at = (2 * (size_t)(from + p) + (p == 0)) * rows + r;
+                    ml[u] = parts.ml[at];
+                    if (e < d)
+                        o[u] = *(const f32x4 *)(parts.o + at * d + e);
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                top = __builtin_fmaxf(top, ml[u][0]);
+            const float to = top == -INFINITY ? 0.0f : top;
+            float f = __builtin_amdgcn_exp2f(m - to);
+            l *= f;
+            acc *= f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                f = __builtin_amdgcn_exp2f(ml[u][0] - to);
+                l += ml[u][1] * f;
+                acc += o[u] * f;
+            }
+            m = top;
+        }
+        __syncthreads();
+        *(f32x4 *)&o_lds[g][e] = acc;
+        if (e == 0)
+            ml_lds[g] = (f32x2){m, l};
+        __syncthreads();
+        if (g == 0 && e < d) {
+            float top = -INFINITY;
+            for (uint32_t u = 0; u < G; ++u)
+                top = __builtin_fmaxf(top, ml_lds[u][0]);
+            const float to = top == -INFINITY ? 0.0f : top;
+            l = 0.0f;
+            acc = (f32x4){0, 0, 0, 0};
+            for (uint32_t u = 0; u < G; ++u) {
+                const float f = __builtin_amdgcn_exp2f(ml_lds[u][0] - to);
+                l += ml_lds[u][1] * f;
+                acc += *(const f32x4 *)&o_lds[u][e] * f;
+            }
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const uint32_t flat = b.row + r, tok = flat / group;
+            *(u32x2 *)(a.out + ((size_t)(b.token + tok) * a.q_heads + b.head * group + (flat - tok * group)) * d + e) =
+                (u32x2){pk_bf16(acc[0] * inv, acc[1] * inv), pk_bf16(acc[2] * inv, acc[3] * inv)};
+        }
+    }
+}
+
+template <int DP, int NQ>
+void launch(const AttnArgs &a, const Parts &p, uint32_t shares, hipStream_t st)
+{
+    if (a.cache.fp8)
+        k_attn_decode<DP, NQ, true><<<shares, WG, 0, st>>>(a, p, shares);
+    else
+        k_attn_decode<DP, NQ, false><<<shares, WG, 0, st>>>(a, p, shares);
+}
+
+} // namespace
+
+hipError_t launch_attn_join(const AttnArgs &a, const Parts &p, uint32_t shares, uint32_t rows, uint32_t live,
+                            hipStream_t st)
+{
+    const dim3 grid(shares, min(live, 32u));
+    if (a.cache.d <= 64)
+        k_attn_join<16><<<grid, 256, 0, st>>>(a, p, rows);
+    else if (a.cache.d <= 128)
+        k_attn_join<32><<<grid, 256, 0, st>>>(a, p, rows);
+    else
+        k_attn_join<64><<<grid, 256, 0, st>>>(a, p, rows);
+    count_launch();
+    return hipGetLastError();
+}
+
+static uint32_t max_shares()
+{
+    return 2 * (cu_count() ? cu_count() : 256);
+}
+
+uint64_t decode_work(uint32_t d)
+{
+    return parts_bytes(max_shares(), DECODE_ROWS, d);
+}
+
+hipError_t launch_attn_decode(const AttnArgs &a, hipStream_t st)
+{
+    // no more workgroups than the table has room for tiles
+    const uint64_t most = (uint64_t)a.seqs * a.cache.heads * ((((uint64_t)a.width << a.cache.page_log2) + TILE - 1) / TILE);
+    const uint32_t shares = (uint32_t)min((uint64_t)max_shares(), most);
+    const Parts p = parts_at(a.work, shares, DECODE_ROWS);
+    if (a.cache.d <= 64)
+        launch<64, 1>(a, p, shares, st);
+    else if (a.cache.d <= 128)
+        launch<128, 1>(a, p, shares, st);
+    else
+        launch<256, 1>(a, p, shares, st);
+    count_launch();
+    if (hipError_t e = hipGetLastError())
+        return e;
+    return launch_attn_join(a, p, shares, DECODE_ROWS, a.max_q * (a.q_heads / a.cache.heads), st);
+}
+
+} // namespace attn
+} // namespace qp
