@@ -104,6 +104,9 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w)
     return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
 
+// A scale of V, finite: 0 times it is 0 in the rows that do not see its key.
+__device__ __forceinline__ float finite_scale(float s) { return __builtin_amdgcn_fmed3f(s, 0.0f, 3.4e38f); }
+
 // Eight E4M3 codes as BF16 (exact: three bits of significand, exponents that fit).
 __device__ __forceinline__ u32x4 bf16_of_e4m3(u32x2 c)
 {

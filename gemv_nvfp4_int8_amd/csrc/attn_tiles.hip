@@ -2,8 +2,9 @@
 // prompts, large verify batches).
 //
 // A workgroup takes a unit of 32 rows a wave and goes through its keys 64 at a
-// time; K and V of the next 64 are on their way to registers while these are
-// worked on from LDS, two buffers in turn with one barrier.  A wave computes
+// time; K and V of the next 64 are on their way (straight to LDS, or through
+// registers where they have to be decoded) while these are worked on, two buffers
+// in turn with one barrier.  A wave computes
 //   S^T [key, row] = K Q^T   32x32x16 MFMAs, K from LDS, Q in registers
 //   P^T = exp2(S^T - m)      a lane holds 32 scores of ONE row: its maximum and sum
 //                            need one exchange with the lane 32 further, the
@@ -26,12 +27,23 @@ constexpr uint32_t KT = 64;                // keys of a tile
 
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) void lds_void;
+
+__device__ const u32x4 ZEROS[1] = {{0, 0, 0, 0}};
 
 // The XOR of row r's piece numbers.
 template <int DP>
 __device__ __forceinline__ uint32_t swizzle(uint32_t r)
 {
     return DP == 64 ? (r >> 1 & 1) << 2 | (r >> 2 & 3) : (r & 3) << 2 | (r >> 2 & 3);
+}
+
+// The same value, computed where it is used: what follows from it is not kept in
+// registers through the loop.
+__device__ __forceinline__ uint32_t here(uint32_t v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
 }
 
 // A block of a sequence's rows: which keys any of them sees.
@@ -65,10 +77,11 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
     constexpr uint32_t ITEMS = KT * CPR / WG;          // of a thread, of K and of V each
     constexpr uint32_t TILE_BYTES = KT * DP * 2;
     static_assert(ITEMS >= 1 && KT * CPR % WG == 0, "every thread loads as many pieces");
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][TILE_BYTES];      // buffer; K, V
+    // an array for each buffer: loads on their way to one do not hold up reads of the other
+    __shared__ __attribute__((aligned(16))) uint8_t k_lds0[TILE_BYTES], v_lds0[TILE_BYTES], k_lds1[TILE_BYTES], v_lds1[TILE_BYTES];
     __shared__ float scales[2][2][KT];     // of K, of V (E4M3)
-    __shared__ uint32_t holes[2][KT / 16], odd[2][NW];
-    __shared__ uint8_t odd_bits[2][KT][CH];      // which of a piece of V are NaN or infinite
+    __shared__ uint32_t holes[2][KT / 16], odd[NW];
+    __shared__ uint8_t odd_bits[KT][CH];         // which of a piece of V are NaN or infinite
     __shared__ uint32_t scan[NW], seq_n[WG], seq_len[WG], seq_end[WG];
     __shared__ uint32_t found[4];
 
@@ -159,7 +172,10 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
     bool began = false;
     // LDS addresses of a lane's fragments: K's piece 2 ks + half of row col, V's
     // pieces of rows 4 half + (lane % 16) / 4 (+ 8) that hold its group's 16 of d
-    const uint32_t k_row = col * DP * 2, k_swz = swizzle<DP>(col);
+    uint32_t k_addr[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+        k_addr[ks] = col * DP * 2 + ((2 * ks + half) ^ swizzle<DP>(col)) * 16;
     const uint32_t v_row = 4 * half + lane % 16 / 4, v_piece = 2 * (lane / 16 % 2) + lane % 4 / 2;
     uint32_t v_addr[2][DB];
 #pragma unroll
@@ -192,7 +208,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
         const uint32_t first_row = row0 + 32 * wave, my_row = first_row + col;
         const bool wave_live = 32 * wave < rows, row_live = 32 * wave + col < rows;
         const int old = q.len - q.n;
-        const int pos = old + (int)(my_row / group);
+        const int my_pos = old + (int)(my_row / group);
         const int pos_lo = old + (int)(first_row / group), pos_hi = old + (int)((min(first_row + 32, row0 + rows) - 1) / group);
         const size_t q_at = ((size_t)(q.token + my_row / group) * a.q_heads + head * group + my_row % group) * d;
         bf16x8 qf[KS];
@@ -204,6 +220,10 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
             qf[ks] = __builtin_bit_cast(bf16x8, v);
         }
         float m = -INFINITY, base = 0.0f, l = 0.0f;
+        uint32_t nans[CH / 8];             // bit 4 c + j: the row's d = 8 c + 4 half + j has met NaN or an infinity
+#pragma unroll
+        for (uint32_t i = 0; i < CH / 8; ++i)
+            nans[i] = 0;
         f32x16 acc[DB];
 #pragma unroll
         for (int db = 0; db < DB; ++db)
@@ -211,247 +231,260 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
 
         // ---- loads: a thread's pieces of the tile, its page numbers one tile ahead
         const uint32_t t_end = blk.first_tile + off + count;
-        const size_t table = (size_t)seq * a.width, plane = ((size_t)kv * d) << pl;
+        const int32_t *table = a.table + (size_t)seq * a.width;
+        const uint32_t page_elems = (kv * d) << pl, head_elems = (head * d) << pl;   // of one page: below 2^31
         const uint32_t mask = (1u << pl) - 1;
-        const uint32_t elem = FP8 ? 1 : 2;
-        u32x4 kr[ITEMS], vr[ITEMS];
+        u32x4 kr[FP8 ? ITEMS : 1], vr[FP8 ? ITEMS : 1];
         float ksr = 0.0f, vsr = 0.0f;
-        uint32_t ok = 0, hole = 0, page[ITEMS], spage = 0;
+        uint32_t hole = 0, page[ITEMS], spage = 0;
         auto look = [&](uint32_t tile) {
+            const uint32_t tid = here(threadIdx.x);
 #pragma unroll
             for (uint32_t i = 0; i < ITEMS; ++i) {
                 const uint32_t key = tile * KT + (tid + WG * i) / CPR;
-                page[i] = key < (uint32_t)blk.to ? (uint32_t)a.table[table + (key >> pl)] : ~0u;
+                page[i] = key < (uint32_t)blk.to ? (uint32_t)table[key >> pl] : ~0u;
             }
             if (FP8 && tid < KT) {
                 const uint32_t key = tile * KT + tid;
-                spage = key < (uint32_t)blk.to ? (uint32_t)a.table[table + (key >> pl)] : ~0u;
+                spage = key < (uint32_t)blk.to ? (uint32_t)table[key >> pl] : ~0u;
             }
         };
-        auto load = [&](uint32_t tile) {
-            ok = hole = 0;
+        auto load = [&](uint32_t tile, uint8_t *kd, uint8_t *vd) {
+            const uint32_t tid = here(threadIdx.x);
+            hole = 0;
 #pragma unroll
             for (uint32_t i = 0; i < ITEMS; ++i) {
-                const uint32_t it = tid + WG * i, key = tile * KT + it / CPR, c = it % CPR;
+                // piece c of LDS row r holds piece c ^ swizzle(r) of the head's row
+                const uint32_t it = tid + WG * i, r = it / CPR, key = tile * KT + r;
+                const uint32_t c = FP8 ? it % CPR : it % CPR ^ swizzle<DP>(r);
                 const bool page_ok = page[i] < a.cache.pages;
-                const bool fine = page_ok && (int)key >= blk.from && c * (FP8 ? 16 : 8) < d;
-                ok |= (uint32_t)fine << i;
                 hole |= (uint32_t)!page_ok << i;
-                const size_t at = fine ? ((page[i] * plane + (((size_t)head << pl) + (key & mask)) * d) * elem + c * 16) : 0;
-                kr[i] = *(const u32x4 *)((const uint8_t *)a.cache.k + at);
-                vr[i] = *(const u32x4 *)((const uint8_t *)a.cache.v + at);
+                // what no row sees, and what lies past d, is read as zeros
+                const bool fine = page_ok && (int)key >= blk.from && c * (FP8 ? 16 : 8) < d;
+                const uint64_t at = (uint64_t)page[i] * page_elems + (head_elems + (key & mask) * d + c * (FP8 ? 16 : 8));
+                const uint8_t *kp = fine ? (const uint8_t *)a.cache.k + (FP8 ? at : 2 * at) : (const uint8_t *)ZEROS;
+                const uint8_t *vp = fine ? (const uint8_t *)a.cache.v + (FP8 ? at : 2 * at) : (const uint8_t *)ZEROS;
+                if constexpr (FP8) {
+                    kr[i] = *(const u32x4 *)kp;
+                    vr[i] = *(const u32x4 *)vp;
+                } else {
+                    __builtin_amdgcn_global_load_lds(kp, (lds_void *)(kd + 16 * (64 * wave + WG * i)), 16, 0, 0);
+                    __builtin_amdgcn_global_load_lds(vp, (lds_void *)(vd + 16 * (64 * wave + WG * i)), 16, 0, 0);
+                }
             }
             if (FP8 && tid < KT) {
                 const uint32_t key = tile * KT + tid;
-                const size_t at = spage < a.cache.pages ? ((spage * (size_t)kv + head) << pl) + (key & mask) : 0;
+                const uint64_t at = spage < a.cache.pages ? ((spage * (uint64_t)kv + head) << pl) + (key & mask) : 0;
                 ksr = a.cache.ks[at];
                 vsr = a.cache.vs[at];
             }
         };
-        auto store = [&](uint32_t tile, uint32_t buf) {
-            uint32_t bad = 0;
-            const int k0 = tile * KT;
-            // a piece of V; where NaN and infinities have to be kept from some rows, zeros in their places and a note of them
-            auto put_v = [&](uint8_t *to, u32x4 v, uint8_t *note, bool edge) {
-                if (edge) {
-                    uint32_t bits = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t z = not_finite(v[i]);
-                        bits |= (z & 1) << (2 * i) | (z >> 31) << (2 * i + 1);
-                        v[i] &= ~z;
-                    }
-                    *note = bits;
-                    bad |= bits;
-                }
-                *(u32x4 *)to = v;
-            };
-            // some row of the block does not see some key of the tile
-            const bool edge = k0 + (int)KT - 1 > old + (int)(row0 / group) ||
-                              (a.window && k0 <= old + (int)((row0 + rows - 1) / group) - (int64_t)a.window);
+        auto store = [&](uint32_t buf, uint8_t *kd, uint8_t *vd) {
+            const uint32_t tid = here(threadIdx.x);
 #pragma unroll
             for (uint32_t i = 0; i < ITEMS; ++i) {
                 const uint32_t it = tid + WG * i, r = it / CPR, c = it % CPR;
-                if (!(ok >> i & 1))
-                    kr[i] = vr[i] = (u32x4){0, 0, 0, 0};
-                uint8_t *kd = lds[buf][0] + r * DP * 2, *vd = lds[buf][1] + r * DP * 2;
-                const uint32_t z = swizzle<DP>(r);
                 if constexpr (FP8) {
 #pragma unroll
                     for (uint32_t h = 0; h < 2; ++h) {
-                        const uint32_t p = ((2 * c + h) ^ z) * 16;
+                        const uint32_t p = r * DP * 2 + ((2 * c + h) ^ swizzle<DP>(r)) * 16;
                         *(u32x4 *)(kd + p) = bf16_of_e4m3((u32x2){kr[i][2 * h], kr[i][2 * h + 1]});
-                        put_v(vd + p, bf16_of_e4m3((u32x2){vr[i][2 * h], vr[i][2 * h + 1]}), &odd_bits[buf][r][2 * c + h], edge);
+                        *(u32x4 *)(vd + p) = bf16_of_e4m3((u32x2){vr[i][2 * h], vr[i][2 * h + 1]});
                     }
-                } else {
-                    *(u32x4 *)(kd + (c ^ z) * 16) = kr[i];
-                    put_v(vd + (c ^ z) * 16, vr[i], &odd_bits[buf][r][c], edge);
                 }
                 if (c == 0 && r % 16 == 0)
                     holes[buf][r / 16] = hole >> i & 1;
             }
             if (FP8 && tid < KT) {
                 scales[buf][0][tid] = ksr * scale;
-                scales[buf][1][tid] = vsr;
+                scales[buf][1][tid] = finite_scale(vsr);
             }
-            const bool any = __any(bad != 0);
-            if (lane == 0)
-                odd[buf][wave] = any;
+        };
+        // One tile; masked: some of the wave's rows do not see some of its keys.
+        auto step = [&](const uint8_t *kt, const uint8_t *vt, int k0, uint32_t buf, uint32_t gaps, bool masked) {
+            const int pos = (int)here(my_pos);
+            auto sees = [&](int k) { return k0 + k <= pos && (!a.window || (uint32_t)(pos - k0 - k) < a.window) && !(gaps >> (k / 16) & 1); };
+            // ---- scores; a lane's are of keys 32 kb + 8 (i / 4) + 4 half + i % 4.  K's
+            // fragments are read AHEAD products before they are used (the order is pinned:
+            // left alone, each read is put right before its product)
+            constexpr int AHEAD = 4;
+            f32x16 s[2] = {(f32x16)0.0f, (f32x16)0.0f};
+            bf16x8 kf[AHEAD];
+            auto k_frag = [&](int n) { return *(const bf16x8 *)(kt + n % 2 * 32 * DP * 2 + k_addr[n / 2]); };
+#pragma unroll
+            for (int n = 0; n < AHEAD; ++n)
+                kf[n] = k_frag(n);
+#pragma unroll
+            for (int n = 0; n < 2 * KS; ++n) {
+                __builtin_amdgcn_sched_barrier(0);
+                s[n % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[n % AHEAD], qf[n / 2], s[n % 2], 0, 0, 0);
+                if (n + AHEAD < 2 * KS)
+                    kf[n % AHEAD] = k_frag(n + AHEAD);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            const float unit_scale = FP8 ? 1.0f : scale;
+            if constexpr (FP8) {
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const f32x4 z = *(const f32x4 *)&scales[buf][0][32 * kb + 2 * i + 4 * half];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            s[kb][i + j] *= z[j];
+                    }
+            }
+            if (masked) {
+                const int at = 4 * (int)here(half);
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float x = sees(32 * kb + 8 * (i / 4) + i % 4 + at) ? s[kb][i] : -INFINITY;
+                        asm volatile("" : "+v"(x));     // computed in this branch alone
+                        s[kb][i] = x;
+                    }
+            }
+            // ---- probabilities
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                top = __builtin_fmaxf(__builtin_fmaxf(top, s[0][i]), s[1][i]);
+            top *= unit_scale;
+            if (__any(top > m + 8.0f)) {
+                top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
+                top = __builtin_fmaxf(top, m);
+                const float to = top == -INFINITY ? 0.0f : top;
+                const float fade = __builtin_amdgcn_exp2f(m - to);
+                m = top;
+                base = to;
+                l *= fade;
+#pragma unroll
+                for (int db = 0; db < DB; ++db)
+                    acc[db] *= fade;
+            }
+            // ---- V: 16 keys' probabilities, then their products with every 32 of d; under
+            // these the next 16 keys' probabilities and V's fragments
+            float part[4] = {0, 0, 0, 0};
+            auto probability = [&](int blk, int i) {
+                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[blk / 2][8 * (blk % 2) + i], unit_scale, -base));
+                part[i % 4] += p;
+                return FP8 ? p * scales[buf][1][16 * blk + 8 * (i / 4) + 4 * half + i % 4] : p;
+            };
+            auto v_frag = [&](int blk, int db) {
+                u32x4 v;
+#pragma unroll
+                for (int jj = 0; jj < 2; ++jj) {
+                    const uint8_t *p = vt + 16 * blk * DP * 2 + v_addr[jj][db];
+                    const u32x2 t = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
+                    v[2 * jj] = t[0];
+                    v[2 * jj + 1] = t[1];
+                }
+                return v;
+            };
+            u32x4 vf[DB], pf, pn;
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+                vf[db] = v_frag(0, db);
+            // rounded to BF16, the operand's type (2^-9 of each on average over keys, as the output's own rounding)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                pf[i] = pk_bf16(probability(0, 2 * i), probability(0, 2 * i + 1));
+#pragma unroll
+            for (int blk = 0; blk < 4; ++blk) {
+#pragma unroll
+                for (int db = 0; db < DB; ++db) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[db]),
+                                                                      __builtin_bit_cast(bf16x8, pf), acc[db], 0, 0, 0);
+                    if (blk == 3)
+                        continue;
+                    vf[db] = v_frag(blk + 1, db);
+#pragma unroll
+                    for (int i = 4 * db / DB; i < 4 * (db + 1) / DB; ++i)
+                        pn[i] = pk_bf16(probability(blk + 1, 2 * i), probability(blk + 1, 2 * i + 1));
+                }
+                pf = pn;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            l += (part[0] + part[1]) + (part[2] + part[3]);
+            if (masked) {
+                uint32_t any = 0;
+                for (uint32_t u = 0; u < NW; ++u)
+                    any |= odd[u];
+                if (uniform(any)) {
+                    // NaN and infinities, in whose places V has zeros, for the rows that see them
+#pragma unroll 1
+                    for (int k = 0; k < (int)KT; ++k)
+                        if (sees(k)) {
+#pragma unroll
+                            for (uint32_t c = 0; c < CH; ++c)
+                                nans[c / 8] |= (odd_bits[k][c] >> 4 * half & 15u) << (4 * (c % 8));
+                        }
+                }
+            }
         };
 
         uint32_t tile = blk.first_tile + off;
+        const int block_lo = old + (int)(row0 / group), block_hi = old + (int)((row0 + rows - 1) / group);
         look(tile);
-        load(tile);
+        __syncthreads();                   // the last unit's tiles have been read
+        load(tile, k_lds0, v_lds0);
+        store(0, k_lds0, v_lds0);
         if (tile + 1 < t_end)
             look(tile + 1);
-        __syncthreads();                   // the last unit's tiles have been read
-        store(tile, 0);
-        __syncthreads();
-        for (uint32_t buf = 0; tile < t_end; ++tile, buf ^= 1) {
+        // A tile from one buffer while the next comes to the other.
+        auto turn = [&](uint32_t buf, const uint8_t *kt, uint8_t *vt, uint8_t *k_next, uint8_t *v_next) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
             const bool more = tile + 1 < t_end;
             if (more) {
-                load(tile + 1);
+                load(tile + 1, k_next, v_next);
                 if (tile + 2 < t_end)
                     look(tile + 2);
             }
             const int k0 = tile * KT;
-            const uint32_t gaps = __builtin_amdgcn_readfirstlane(holes[buf][0] | holes[buf][1] << 1 | holes[buf][2] << 2 |
-                                                                 holes[buf][3] << 3);
-            const bool none = !wave_live || k0 > pos_hi || (a.window && k0 + (int)KT - 1 <= pos_lo - (int64_t)a.window);
-            if (!none) {
-                // ---- scores
-                f32x16 s[2];
-                const uint8_t *kt = lds[buf][0] + k_row, *vt = lds[buf][1];
+            const uint32_t gaps = uniform(holes[buf][0] | holes[buf][1] << 1 | holes[buf][2] << 2 | holes[buf][3] << 3);
+            if (k0 + (int)KT - 1 > block_lo || (a.window && k0 <= block_hi - (int64_t)a.window) || gaps) {
+                // some row of the block does not see some key, and 0 times NaN would be
+                // NaN: those of V go, and are noted for the rows that see them
+                uint32_t bad = 0;
+                for (uint32_t i = here(threadIdx.x); i < KT * CH; i += WG) {
+                    u32x4 v = *(const u32x4 *)(vt + 16 * i);
+                    uint32_t bits = 0;
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    s[kb] = (f32x16)0.0f;
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        const bf16x8 kf = *(const bf16x8 *)(kt + kb * 32 * DP * 2 + ((2 * ks + half) ^ k_swz) * 16);
-                        s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[ks], s[kb], 0, 0, 0);
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t z = not_finite(v[j]);
+                        bits |= (z & 1) << (2 * j) | (z >> 31) << (2 * j + 1);
+                        v[j] &= ~z;
                     }
+                    const uint32_t r = i / CH;
+                    odd_bits[r][i % CH ^ swizzle<DP>(r)] = bits;
+                    if (bits)
+                        *(u32x4 *)(vt + 16 * i) = v;
+                    bad |= bits;
                 }
-                const float unit_scale = FP8 ? 1.0f : scale;
-                if constexpr (FP8) {
-#pragma unroll
-                    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const f32x4 z = *(const f32x4 *)&scales[buf][0][32 * kb + 2 * i + 4 * half];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                s[kb][i + j] *= z[j];
-                        }
-                }
-                const bool whole = k0 + (int)KT - 1 <= pos_lo && (!a.window || k0 > pos_hi - (int64_t)a.window) && gaps == 0;
-                uint32_t seen = ~0u;       // bit 16 kb + i: the lane's row sees key 32 kb + 8 (i / 4) + 4 half + i % 4
-                if (!whole) {
-                    seen = 0;
-#pragma unroll
-                    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int k = 32 * kb + 8 * (i / 4) + 4 * (int)half + i % 4;
-                            const bool see = k0 + k <= pos && (!a.window || (uint32_t)(pos - k0 - k) < a.window) &&
-                                             !(gaps >> (2 * kb + i / 8) & 1);
-                            seen |= (uint32_t)see << (16 * kb + i);
-                            s[kb][i] = see ? s[kb][i] : -INFINITY;
-                        }
-                }
-                // ---- probabilities
-                float top = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    top = __builtin_fmaxf(top, __builtin_fmaxf(s[0][i], s[1][i]));
-                top *= unit_scale;
-                if (__any(top > m + 8.0f)) {
-                    top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-                    top = __builtin_fmaxf(top, m);
-                    const float to = top == -INFINITY ? 0.0f : top;
-                    const float fade = __builtin_amdgcn_exp2f(m - to);
-                    m = top;
-                    base = to;
-                    l *= fade;
-#pragma unroll
-                    for (int db = 0; db < DB; ++db)
-                        acc[db] *= fade;
-                }
-                float part[4] = {0, 0, 0, 0};
-                bf16x8 pf[2][2];
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                    for (int sb = 0; sb < 2; ++sb) {
-                        float p[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][8 * sb + i], unit_scale, -base));
-                            part[i % 4] += p[i];
-                        }
-                        if constexpr (FP8) {
-#pragma unroll
-                            for (int i = 0; i < 8; i += 4) {
-                                const f32x4 z = *(const f32x4 *)&scales[buf][1][32 * kb + 16 * sb + 2 * i + 4 * half];
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    p[i + j] *= z[j];
-                                    if (!whole)
-                                        p[i + j] = seen >> (16 * kb + 8 * sb + i + j) & 1 ? p[i + j] : 0.0f;
-                                }
-                            }
-                        }
-                        // rounded to BF16, the operand's type (2^-9 of each on average over keys, as the output's own rounding)
-                        u32x4 w4;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            w4[i] = pk_bf16(p[2 * i], p[2 * i + 1]);
-                        pf[kb][sb] = __builtin_bit_cast(bf16x8, w4);
-                    }
-                l += (part[0] + part[1]) + (part[2] + part[3]);
-
-                // ---- V
-                auto v_frag = [&](int kb, int sb, int db) {
-                    u32x4 v;
-#pragma unroll
-                    for (int jj = 0; jj < 2; ++jj) {
-                        const uint8_t *p = vt + (32 * kb + 16 * sb) * DP * 2 + v_addr[jj][db];
-                        const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-                        const u32x2 t2 = __builtin_bit_cast(u32x2, t);
-                        v[2 * jj] = t2[0];
-                        v[2 * jj + 1] = t2[1];
-                    }
-                    return v;
-                };
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                    for (int sb = 0; sb < 2; ++sb)
-#pragma unroll
-                        for (int db = 0; db < DB; ++db)
-                            acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                                __builtin_bit_cast(bf16x8, v_frag(kb, sb, db)), pf[kb][sb], acc[db], 0, 0, 0);
-                if (!whole) {
-                    uint32_t any = 0;
-                    for (uint32_t u = 0; u < NW; ++u)
-                        any |= odd[buf][u];
-                    if (uniform(any)) {
-                        // what stood in the places of the zeros, for the rows that see it
-                        for (int k = 0; k < (int)KT; ++k) {
-                            const bool see = k0 + k <= pos && (!a.window || (uint32_t)(pos - k0 - k) < a.window);
-                            for (uint32_t c = 0; c < CH && see; ++c)
-#pragma unroll
-                                for (int db = 0; db < DB; ++db)
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i)
-                                        if (c == 4u * db + i / 4 && odd_bits[buf][k][c] >> (4 * half + i % 4) & 1)
-                                            acc[db][i] = __builtin_nanf("");
-                        }
-                    }
-                }
+                const bool any = __any(bad != 0);
+                if (lane == 0)
+                    odd[wave] = any;
+                __syncthreads();
             }
+            const bool none = !wave_live || k0 > pos_hi || (a.window && k0 + (int)KT - 1 <= pos_lo - (int64_t)a.window);
+            const bool whole = k0 + (int)KT - 1 <= pos_lo && (!a.window || k0 > pos_hi - (int64_t)a.window) && gaps == 0;
+            const int way = uniform(none ? 0u : whole ? 1u : 2u);
+            if (way != 0)
+                step(kt, vt, k0, buf, gaps, way == 2);
             if (more)
-                store(tile + 1, buf ^ 1);
-            __syncthreads();
+                store(buf ^ 1, k_next, v_next);
+            ++tile;
+        };
+        while (true) {
+            turn(0, k_lds0, v_lds0, k_lds1, v_lds1);
+            if (tile >= t_end)
+                break;
+            turn(1, k_lds1, v_lds1, k_lds0, v_lds0);
+            if (tile >= t_end)
+                break;
         }
 
         // ---- the rows' results: a lane holds d = 32 db + 8 (i / 4) + 4 half + i % 4 of row col
@@ -469,7 +502,10 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
                     const uint32_t e = 32 * db + 2 * i + 4 * half;
                     if (e >= d)
                         continue;
-                    const f32x4 v = {acc[db][i], acc[db][i + 1], acc[db][i + 2], acc[db][i + 3]};
+                    f32x4 v = {acc[db][i], acc[db][i + 1], acc[db][i + 2], acc[db][i + 3]};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[j] = nans[db / 2] >> (16 * (db % 2) + i + j) & 1 ? __builtin_nanf("") : v[j];
                     if (finished)
                         *(u32x2 *)(a.out + q_at + e) = (u32x2){pk_bf16(v[0] * inv, v[1] * inv), pk_bf16(v[2] * inv, v[3] * inv)};
                     else

@@ -22,7 +22,8 @@ int check_cache(int fmt, const void *k, const void *v, const float *ks, const fl
         if (int e = check_ptrs({ks, vs}))
             return e;
     if (kv_heads == 0 || kv_heads > 65535 || d == 0 || d > 256 || d % 16 != 0 || pages == 0 || page_size < 16 ||
-        page_size > 4096 || (page_size & (page_size - 1)) != 0 || !fits(pages, page_size))
+        page_size > 4096 || (page_size & (page_size - 1)) != 0 || !fits(pages, page_size) ||
+        !fits(kv_heads, (uint64_t)page_size * d))
         return QP_ERR_SHAPE;
     return QP_OK;
 }
