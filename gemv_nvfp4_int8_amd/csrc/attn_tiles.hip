@@ -80,7 +80,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
     // an array for each buffer: loads on their way to one do not hold up reads of the other
     __shared__ __attribute__((aligned(16))) uint8_t k_lds0[TILE_BYTES], v_lds0[TILE_BYTES], k_lds1[TILE_BYTES], v_lds1[TILE_BYTES];
     __shared__ float scales[2][2][KT];     // of K, of V (E4M3)
-    __shared__ uint32_t holes[2][KT / 16], odd[NW];
+    __shared__ uint32_t odd[NW];
     __shared__ uint8_t odd_bits[KT][CH];         // which of a piece of V are NaN or infinite
     __shared__ uint32_t scan[NW], seq_n[WG], seq_len[WG], seq_end[WG];
     __shared__ uint32_t found[4];
@@ -229,55 +229,79 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
         for (int db = 0; db < DB; ++db)
             acc[db] = (f32x16)0.0f;
 
-        // ---- loads: a thread's pieces of the tile, its page numbers one tile ahead
+        // ---- loads.  A wave's 64 pieces lie in one 16 keys, so in one page: its
+        // address is scalar, the lane's part the same for every tile
         const uint32_t t_end = blk.first_tile + off + count;
         const int32_t *table = a.table + (size_t)seq * a.width;
         const uint32_t page_elems = (kv * d) << pl, head_elems = (head * d) << pl;   // of one page: below 2^31
         const uint32_t mask = (1u << pl) - 1;
+        constexpr uint32_t EB = FP8 ? 1 : 2;               // bytes of an element
         u32x4 kr[FP8 ? ITEMS : 1], vr[FP8 ? ITEMS : 1];
         float ksr = 0.0f, vsr = 0.0f;
-        uint32_t hole = 0, page[ITEMS], spage = 0;
+        // lane i: the page of the 16 keys 16 i behind the first tile's, or behind 16 tiles later and so on
+        uint32_t pages = 0, pages_next = 0;
         auto look = [&](uint32_t tile) {
-            const uint32_t tid = here(threadIdx.x);
-#pragma unroll
-            for (uint32_t i = 0; i < ITEMS; ++i) {
-                const uint32_t key = tile * KT + (tid + WG * i) / CPR;
-                page[i] = key < (uint32_t)blk.to ? (uint32_t)table[key >> pl] : ~0u;
-            }
-            if (FP8 && tid < KT) {
-                const uint32_t key = tile * KT + tid;
-                spage = key < (uint32_t)blk.to ? (uint32_t)table[key >> pl] : ~0u;
-            }
+            const uint32_t key = tile * KT + 16 * lane;
+            return key < (uint32_t)blk.to && tile < t_end ? (uint32_t)table[key >> pl] : ~0u;
         };
+        // Starts a tile's loads; returns its 16s of keys that are holes, as bits.
         auto load = [&](uint32_t tile, uint8_t *kd, uint8_t *vd) {
+            const uint32_t at = (tile - (blk.first_tile + off)) % 16;
+            if (at == 0) {
+                pages = pages_next;
+                pages_next = look(tile + 16);
+            }
+            uint32_t page[KT / 16], gaps = 0;
+#pragma unroll
+            for (uint32_t g = 0; g < KT / 16; ++g) {
+                page[g] = __builtin_amdgcn_readlane(pages, 4 * at + g);
+                gaps |= (uint32_t)(page[g] >= a.cache.pages) << g;
+            }
+            const int k0 = tile * KT;
+            const bool inside = k0 >= blk.from && k0 + (int)KT <= blk.to && gaps == 0;
             const uint32_t tid = here(threadIdx.x);
-            hole = 0;
 #pragma unroll
             for (uint32_t i = 0; i < ITEMS; ++i) {
-                // piece c of LDS row r holds piece c ^ swizzle(r) of the head's row
-                const uint32_t it = tid + WG * i, r = it / CPR, key = tile * KT + r;
-                const uint32_t c = FP8 ? it % CPR : it % CPR ^ swizzle<DP>(r);
-                const bool page_ok = page[i] < a.cache.pages;
-                hole |= (uint32_t)!page_ok << i;
-                // what no row sees, and what lies past d, is read as zeros
-                const bool fine = page_ok && (int)key >= blk.from && c * (FP8 ? 16 : 8) < d;
-                const uint64_t at = (uint64_t)page[i] * page_elems + (head_elems + (key & mask) * d + c * (FP8 ? 16 : 8));
-                const uint8_t *kp = fine ? (const uint8_t *)a.cache.k + (FP8 ? at : 2 * at) : (const uint8_t *)ZEROS;
-                const uint8_t *vp = fine ? (const uint8_t *)a.cache.v + (FP8 ? at : 2 * at) : (const uint8_t *)ZEROS;
-                if constexpr (FP8) {
-                    kr[i] = *(const u32x4 *)kp;
-                    vr[i] = *(const u32x4 *)vp;
+                // piece c of LDS row r holds piece c ^ swizzle(r) of the head's row; r % 16 and c are
+                // the same for all i, or (8 rows a wave) for every other tile row group
+                const uint32_t it = tid + WG * i, r = it / CPR;
+                uint32_t c = FP8 ? it % CPR : it % CPR ^ swizzle<DP>(r);
+                c = c * (FP8 ? 16 : 8) < d ? c : 0;        // past d: meets zeros of Q, or is not stored
+                const uint32_t g = uniform((64 * wave + WG * i) / CPR / 16);
+                const uint32_t pg = page[g];
+                const uint64_t base = ((uint64_t)pg * page_elems + (head_elems + ((k0 + 16 * g) & mask) * d)) * EB;
+                const uint32_t lane_at = (r % 16 * d + c * (FP8 ? 16 : 8)) * EB;
+                const uint8_t *kp = (const uint8_t *)a.cache.k + base, *vp = (const uint8_t *)a.cache.v + base;
+                if (inside) {
+                    if constexpr (FP8) {
+                        kr[i] = *(const u32x4 *)(kp + lane_at);
+                        vr[i] = *(const u32x4 *)(vp + lane_at);
+                    } else {
+                        __builtin_amdgcn_global_load_lds(kp + lane_at, (lds_void *)(kd + 16 * (64 * wave + WG * i)), 16, 0, 0);
+                        __builtin_amdgcn_global_load_lds(vp + lane_at, (lds_void *)(vd + 16 * (64 * wave + WG * i)), 16, 0, 0);
+                    }
                 } else {
-                    __builtin_amdgcn_global_load_lds(kp, (lds_void *)(kd + 16 * (64 * wave + WG * i)), 16, 0, 0);
-                    __builtin_amdgcn_global_load_lds(vp, (lds_void *)(vd + 16 * (64 * wave + WG * i)), 16, 0, 0);
+                    // what no row sees is read as zeros
+                    const int key = k0 + (int)r;
+                    const bool fine = key >= blk.from && key < blk.to && pg < a.cache.pages;
+                    const uint8_t *kz = fine ? kp + lane_at : (const uint8_t *)ZEROS, *vz = fine ? vp + lane_at : (const uint8_t *)ZEROS;
+                    if constexpr (FP8) {
+                        kr[i] = *(const u32x4 *)kz;
+                        vr[i] = *(const u32x4 *)vz;
+                    } else {
+                        __builtin_amdgcn_global_load_lds(kz, (lds_void *)(kd + 16 * (64 * wave + WG * i)), 16, 0, 0);
+                        __builtin_amdgcn_global_load_lds(vz, (lds_void *)(vd + 16 * (64 * wave + WG * i)), 16, 0, 0);
+                    }
                 }
             }
             if (FP8 && tid < KT) {
-                const uint32_t key = tile * KT + tid;
-                const uint64_t at = spage < a.cache.pages ? ((spage * (uint64_t)kv + head) << pl) + (key & mask) : 0;
-                ksr = a.cache.ks[at];
-                vsr = a.cache.vs[at];
+                // all of the first wave
+                const uint32_t pg = __shfl(pages, 4 * at + tid / 16, 64);
+                const uint64_t s = pg < a.cache.pages ? ((pg * (uint64_t)kv + head) << pl) + ((k0 + tid) & mask) : 0;
+                ksr = a.cache.ks[s];
+                vsr = a.cache.vs[s];
             }
+            return gaps;
         };
         auto store = [&](uint32_t buf, uint8_t *kd, uint8_t *vd) {
             const uint32_t tid = here(threadIdx.x);
@@ -292,8 +316,6 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
                         *(u32x4 *)(vd + p) = bf16_of_e4m3((u32x2){vr[i][2 * h], vr[i][2 * h + 1]});
                     }
                 }
-                if (c == 0 && r % 16 == 0)
-                    holes[buf][r / 16] = hole >> i & 1;
             }
             if (FP8 && tid < KT) {
                 scales[buf][0][tid] = ksr * scale;
@@ -427,24 +449,19 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
 
         uint32_t tile = blk.first_tile + off;
         const int block_lo = old + (int)(row0 / group), block_hi = old + (int)((row0 + rows - 1) / group);
-        look(tile);
+        pages_next = look(tile);
         __syncthreads();                   // the last unit's tiles have been read
-        load(tile, k_lds0, v_lds0);
+        uint32_t gaps_next = load(tile, k_lds0, v_lds0);
         store(0, k_lds0, v_lds0);
-        if (tile + 1 < t_end)
-            look(tile + 1);
         // A tile from one buffer while the next comes to the other.
         auto turn = [&](uint32_t buf, const uint8_t *kt, uint8_t *vt, uint8_t *k_next, uint8_t *v_next) {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             __syncthreads();
             const bool more = tile + 1 < t_end;
-            if (more) {
-                load(tile + 1, k_next, v_next);
-                if (tile + 2 < t_end)
-                    look(tile + 2);
-            }
+            const uint32_t gaps = gaps_next;
+            if (more)
+                gaps_next = load(tile + 1, k_next, v_next);
             const int k0 = tile * KT;
-            const uint32_t gaps = uniform(holes[buf][0] | holes[buf][1] << 1 | holes[buf][2] << 2 | holes[buf][3] << 3);
             if (k0 + (int)KT - 1 > block_lo || (a.window && k0 <= block_hi - (int64_t)a.window) || gaps) {
                 // some row of the block does not see some key, and 0 times NaN would be
                 // NaN: those of V go, and are noted for the rows that see them
