@@ -235,7 +235,17 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
         const int32_t *table = a.table + (size_t)seq * a.width;
         const uint32_t page_elems = (kv * d) << pl, head_elems = (head * d) << pl;   // of one page: below 2^31
         const uint32_t mask = (1u << pl) - 1;
-        constexpr uint32_t EB = FP8 ? 1 : 2;               // bytes of an element
+        // the lane's element of those 16 rows: piece c of LDS row r holds piece
+        // c ^ swizzle(r) of the head's row; what lies past d is read from its start and
+        // meets zeros of Q, or is not stored.  Row r % 16 is the same for every second
+        // piece of a thread at least.
+        uint32_t lane_at[2];
+#pragma unroll
+        for (uint32_t i = 0; i < 2; ++i) {
+            const uint32_t it = tid + WG * i, r = it / CPR;
+            const uint32_t e = FP8 ? it % CPR * 16 : (it % CPR ^ swizzle<DP>(r)) * 8;
+            lane_at[i] = r % 16 * d + (e < d ? e : 0);
+        }
         u32x4 kr[FP8 ? ITEMS : 1], vr[FP8 ? ITEMS : 1];
         float ksr = 0.0f, vsr = 0.0f;
         // lane i: the page of the 16 keys 16 i behind the first tile's, or behind 16 tiles later and so on
@@ -258,42 +268,46 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
                 gaps |= (uint32_t)(page[g] >= a.cache.pages) << g;
             }
             const int k0 = tile * KT;
+            // a page's row 16 g of the tile, in elements
+            auto row_of = [&](uint32_t pg, uint32_t g) {
+                return (uint64_t)pg * page_elems + (head_elems + ((k0 + 16 * g) & mask) * d);
+            };
             const bool inside = k0 >= blk.from && k0 + (int)KT <= blk.to && gaps == 0;
-            const uint32_t tid = here(threadIdx.x);
+            if constexpr (FP8) {
 #pragma unroll
-            for (uint32_t i = 0; i < ITEMS; ++i) {
-                // piece c of LDS row r holds piece c ^ swizzle(r) of the head's row; r % 16 and c are
-                // the same for all i, or (8 rows a wave) for every other tile row group
-                const uint32_t it = tid + WG * i, r = it / CPR;
-                uint32_t c = FP8 ? it % CPR : it % CPR ^ swizzle<DP>(r);
-                c = c * (FP8 ? 16 : 8) < d ? c : 0;        // past d: meets zeros of Q, or is not stored
-                const uint32_t g = uniform((64 * wave + WG * i) / CPR / 16);
-                const uint32_t pg = page[g];
-                const uint64_t base = ((uint64_t)pg * page_elems + (head_elems + ((k0 + 16 * g) & mask) * d)) * EB;
-                const uint32_t lane_at = (r % 16 * d + c * (FP8 ? 16 : 8)) * EB;
-                const uint8_t *kp = (const uint8_t *)a.cache.k + base, *vp = (const uint8_t *)a.cache.v + base;
-                if (inside) {
-                    if constexpr (FP8) {
-                        kr[i] = *(const u32x4 *)(kp + lane_at);
-                        vr[i] = *(const u32x4 *)(vp + lane_at);
-                    } else {
-                        __builtin_amdgcn_global_load_lds(kp + lane_at, (lds_void *)(kd + 16 * (64 * wave + WG * i)), 16, 0, 0);
-                        __builtin_amdgcn_global_load_lds(vp + lane_at, (lds_void *)(vd + 16 * (64 * wave + WG * i)), 16, 0, 0);
-                    }
-                } else {
+                for (uint32_t i = 0; i < ITEMS; ++i) {
+                    const uint32_t g = uniform((64 * wave + WG * i) / CPR / 16);
+                    const int key = k0 + (int)((here(threadIdx.x) + WG * i) / CPR);
+                    const uint64_t at = row_of(page[g], g) + lane_at[i % 2];
                     // what no row sees is read as zeros
-                    const int key = k0 + (int)r;
+                    const bool fine = inside || (key >= blk.from && key < blk.to && page[g] < a.cache.pages);
+                    kr[i] = *(const u32x4 *)(fine ? (const uint8_t *)a.cache.k + at : (const uint8_t *)ZEROS);
+                    vr[i] = *(const u32x4 *)(fine ? (const uint8_t *)a.cache.v + at : (const uint8_t *)ZEROS);
+                }
+            } else if (inside) {
+#pragma unroll
+                for (uint32_t i = 0; i < ITEMS; ++i) {
+                    const uint32_t g = uniform((64 * wave + WG * i) / CPR / 16);
+                    const uint64_t base = 2 * row_of(page[g], g);
+                    const uint32_t to = 16 * (64 * wave + WG * i);
+                    __builtin_amdgcn_global_load_lds((const uint8_t *)a.cache.k + base + 2 * lane_at[i % 2], (lds_void *)(kd + to), 16, 0, 0);
+                    __builtin_amdgcn_global_load_lds((const uint8_t *)a.cache.v + base + 2 * lane_at[i % 2], (lds_void *)(vd + to), 16, 0, 0);
+                }
+            } else {
+                // not unrolled, so that it is not made one with the loop above
+#pragma unroll 1
+                for (uint32_t i = 0; i < ITEMS; ++i) {
+                    const uint32_t g = uniform((64 * wave + WG * i) / CPR / 16), pg = __builtin_amdgcn_readlane(pages, 4 * at + g);
+                    const int key = k0 + (int)((here(threadIdx.x) + WG * i) / CPR);
+                    const uint64_t from = 2 * (row_of(pg, g) + here(ITEMS > 1 && CPR == 32 ? (i % 2 ? lane_at[1] : lane_at[0]) : lane_at[0]));
+                    const uint32_t to = 16 * (64 * wave + WG * i);
+                    // what no row sees is read as zeros
                     const bool fine = key >= blk.from && key < blk.to && pg < a.cache.pages;
-                    const uint8_t *kz = fine ? kp + lane_at : (const uint8_t *)ZEROS, *vz = fine ? vp + lane_at : (const uint8_t *)ZEROS;
-                    if constexpr (FP8) {
-                        kr[i] = *(const u32x4 *)kz;
-                        vr[i] = *(const u32x4 *)vz;
-                    } else {
-                        __builtin_amdgcn_global_load_lds(kz, (lds_void *)(kd + 16 * (64 * wave + WG * i)), 16, 0, 0);
-                        __builtin_amdgcn_global_load_lds(vz, (lds_void *)(vd + 16 * (64 * wave + WG * i)), 16, 0, 0);
-                    }
+                    __builtin_amdgcn_global_load_lds(fine ? (const uint8_t *)a.cache.k + from : (const uint8_t *)ZEROS, (lds_void *)(kd + to), 16, 0, 0);
+                    __builtin_amdgcn_global_load_lds(fine ? (const uint8_t *)a.cache.v + from : (const uint8_t *)ZEROS, (lds_void *)(vd + to), 16, 0, 0);
                 }
             }
+            const uint32_t tid = here(threadIdx.x);
             if (FP8 && tid < KT) {
                 // all of the first wave
                 const uint32_t pg = __shfl(pages, 4 * at + tid / 16, 64);
