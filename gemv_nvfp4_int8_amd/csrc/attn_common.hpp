@@ -67,6 +67,21 @@ __device__ __forceinline__ uint64_t uniform(uint64_t v)
     return (uint64_t)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v);
 }
 
+// The same value, computed where it is used: what follows from it is not kept in
+// registers through the loop, nor computed outside the branch it is in.
+__device__ __forceinline__ uint32_t here(uint32_t v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// `bytes` of device memory from an address that is the same in the whole wave:
+// what a lane reads behind them is 0, and not fetched.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t window_at(const void *base, uint64_t offset, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc((void *)uniform((uint64_t)base + offset), (short)0, (int)uniform(bytes), 0x00020000);
+}
+
 // A sequence as the host's arrays give it; n = 0 where its numbers do not fit.
 struct Seq {
     int token, n, len;       // first row, rows, positions
@@ -98,11 +113,11 @@ __device__ __forceinline__ Seq read_seq_uniform(const AttnArgs &a, uint32_t s)
     return q;
 }
 
-// Bits of two BF16 values that are NaN or infinite, as 0xFFFF masks.
-__device__ __forceinline__ uint32_t not_finite(uint32_t w)
-{
-    return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
-}
+// The top bits of those of two BF16 values that are NaN or infinite (one more in
+// the exponent's last place carries into the sign's).
+__device__ __forceinline__ uint32_t odd_tops(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+// The same as masks of 0xFFFF.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return (odd_tops(w) >> 15) * 0xFFFFu; }
 
 // A scale of V, finite: 0 times it is 0 in the rows that do not see its key.
 __device__ __forceinline__ float finite_scale(float s) { return __builtin_amdgcn_fmed3f(s, 0.0f, 3.4e38f); }
@@ -129,10 +144,10 @@ __device__ __forceinline__ uint32_t share_of(uint64_t x, uint64_t n, uint64_t sh
 hipError_t launch_attn_join(const AttnArgs &a, const Parts &p, uint32_t shares, uint32_t rows, uint32_t live,
                             hipStream_t st);
 
-// Rows of a sequence times heads of a kv head up to DECODE_ROWS: attn_decode.hip;
-// more: attn_tiles.hip.
-constexpr uint32_t DECODE_ROWS = 16;
-uint64_t decode_work(uint32_t d);
+// Rows of a sequence times heads of a kv head up to decode_rows(d):
+// attn_decode.hip; more: attn_tiles.hip.
+constexpr uint32_t decode_rows(uint32_t d) { return d <= 128 ? 64 : 32; }
+uint64_t decode_work(uint32_t rows, uint32_t d);
 hipError_t launch_attn_decode(const AttnArgs &a, hipStream_t st);
 uint64_t tiles_work(uint32_t d);
 hipError_t launch_attn_tiles(const AttnArgs &a, hipStream_t st);

@@ -35,20 +35,20 @@ __device__ __forceinline__ uint32_t tiles_of(const Seq &q)
     return max(to - from, 1u);             // rows that see nothing are still written
 }
 
-template <int EPT>
-__device__ __forceinline__ void load_elements(const uint8_t *p, uint32_t *w)
+// W dwords.
+template <int W>
+__device__ __forceinline__ void load_dwords(__amdgpu_buffer_rsrc_t p, uint32_t at, uint32_t *w)
 {
-    // EPT dwords
-    if constexpr (EPT == 1) {
-        w[0] = *(const uint32_t *)p;
-    } else if constexpr (EPT == 2) {
-        const u32x2 v = *(const u32x2 *)p;
+    if constexpr (W == 1) {
+        w[0] = __builtin_amdgcn_raw_buffer_load_b32(p, at, 0, 0);
+    } else if constexpr (W == 2) {
+        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(p, at, 0, 0));
         w[0] = v[0];
         w[1] = v[1];
     } else {
 #pragma unroll
-        for (int i = 0; i < EPT / 4; ++i) {
-            const u32x4 v = *(const u32x4 *)(p + 16 * i);
+        for (int i = 0; i < W / 4; ++i) {
+            const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(p, at + 16 * i, 0, 0));
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 w[4 * i + j] = v[j];
@@ -59,16 +59,18 @@ __device__ __forceinline__ void load_elements(const uint8_t *p, uint32_t *w)
 // DP: d rounded up to 64, 128 or 256 (what lies past d is read from the head's
 // start, meets zeros of Q, and is not stored); NQ: 16s of rows.
 template <int DP, int NQ, bool FP8>
-__global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs a, Parts parts, uint32_t max_shares)
+__global__ __launch_bounds__(WG, NQ == 1 && DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs a, Parts parts, uint32_t max_shares)
 {
     constexpr int ROWS = 16 * NQ;
     constexpr int KS = DP / 32;            // MFMAs over d
+    constexpr int KL = FP8 ? KS / 2 : KS;  // loads of K over d
     constexpr int ROWB = FP8 ? 1 : 2;      // bytes of an element
     constexpr int EPL = DP / 16;           // elements of V of a lane and key
     constexpr int VW = EPL * ROWB / 4;     // the same in dwords
     constexpr int LD = DP + 4;             // LDS row, so that 16 rows spread over the banks
     __shared__ float o_lds[WAVES][ROWS][LD];
     __shared__ f32x2 ml_lds[WAVES][ROWS];
+    __shared__ uint16_t odd_bits[WAVES][STEP][16];      // which of a lane's elements of V are NaN or infinite
     __shared__ uint32_t scan[WAVES];
     __shared__ uint32_t found[2];
 
@@ -190,12 +192,13 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
         const uint32_t key_from = (q.first / TILE + off) * TILE, key_to = min(key_from + count * TILE, (uint32_t)q.len);
         const int all_from = a.window ? q.len - (int)min(a.window, (uint32_t)q.len) : 0;   // from here every row sees ...
         const int all_to = q.len - q.n + 1;                                                // ... up to here (exclusive)
-        const size_t page_bytes = ((size_t)d << pl) * ROWB, head_bytes = head * page_bytes;
-        const size_t table = (size_t)seq * a.width;
+        const uint32_t page_elems = (kv * d) << pl, head_elems = (head * d) << pl;         // of one page: below 2^31
+        const int32_t *table = a.table + (size_t)seq * a.width;
         const uint32_t mask = (1u << pl) - 1;
 
         float m[NQ], base[NQ], l[NQ];
         f32x4 acc[NQ][EPL];
+        uint32_t nans[NQ][2];              // bit 16 (i % 2) + j of i / 2: the row's d = EPL (4 quad + i) + j has met NaN or an infinity
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) {
             m[nq] = -INFINITY;
@@ -203,122 +206,203 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
 #pragma unroll
             for (int j = 0; j < EPL; ++j)
                 acc[nq][j] = (f32x4){0, 0, 0, 0};
+            nans[nq][0] = nans[nq][1] = 0;
         }
 
-        u32x4 kr[2][FP8 ? KS / 2 : KS];
+        // a lane's places in 16 rows of K and of V, in bytes
+        uint32_t k_off[KL], v_off[4];
+#pragma unroll
+        for (int ks = 0; ks < KL; ++ks) {
+            const uint32_t e = FP8 ? 64 * ks + 16 * quad : 32 * ks + 8 * quad;
+            k_off[ks] = (col * d + (e < d ? e : 0)) * ROWB;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v_off[j] = ((4 * quad + j) * d + (EPL * col < d ? EPL * col : 0)) * ROWB;
+
+        u32x4 kr[2][KL];
         uint32_t vr[8][VW];
         f32x4 ksc[2], vsc[2];
-        uint32_t page[2], hole = 0;        // of the step whose K is loaded
-        const uint32_t k_off = col * d * ROWB, v_off = 4 * quad * d * ROWB;
-        const uint32_t v_col = EPL * col < d ? EPL * col : 0;
-
-        auto pages = [&](uint32_t key) {
+        // lane i: the page of 16 keys of the wave's step i / 2, of 32 steps
+        auto look = [&](uint32_t key) {
+            const uint32_t k = key + lane / 2 * TILE + lane % 2 * 16;
+            return k < key_to ? (uint32_t)table[k >> pl] : ~0u;
+        };
+        uint32_t pages = 0, pages_next = 0, step = 0, hole = 0;
+        uint64_t rows_at[2];               // where the step's 16 keys lie, in rows of the cache
+        const uint32_t row_bytes = d * ROWB;
+        // of the step at `key`; past the end, as of holes, nothing is loaded
+        auto places = [&](uint32_t key) {
+            if (step % 32 == 0) {
+                pages = pages_next;
+                pages_next = look(key + 32 * TILE);
+            }
             hole = 0;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const uint32_t k = key + 16 * t;
-                // past the sequence's end nothing is looked up
-                page[t] = k < key_to ? (uint32_t)uniform_load(a.table, table + (k >> pl)) : ~0u;
-                if (page[t] >= a.cache.pages) {
-                    page[t] = 0;
+                uint32_t page = __builtin_amdgcn_readlane(pages, 2 * (step % 32) + t);
+                if (page >= a.cache.pages) {
+                    page = 0;
                     hole |= 1u << t;
                 }
+                rows_at[t] = ((page * (uint64_t)kv + head) << pl) + ((key + 16 * t) & mask);
             }
+            ++step;
         };
-        auto load_k = [&](uint32_t key) {
+        auto load_k = [&]() {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const size_t row = (key + 16 * t) & mask;
-                const uint8_t *p = (const uint8_t *)a.cache.k + (page[t] * (size_t)kv) * page_bytes + head_bytes + row * d * ROWB;
+                const bool there = !(hole >> t & 1);
+                const __amdgpu_buffer_rsrc_t p = window_at(a.cache.k, rows_at[t] * row_bytes, there ? 16 * row_bytes : 0);
 #pragma unroll
-                for (int ks = 0; ks < (FP8 ? KS / 2 : KS); ++ks) {
-                    const uint32_t e = FP8 ? 64 * ks + 16 * quad : 32 * ks + 8 * quad;
-                    kr[t][ks] = *(const u32x4 *)(p + k_off + (e < d ? e * ROWB : 0));
-                }
+                for (int ks = 0; ks < KL; ++ks)
+                    kr[t][ks] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(p, k_off[ks], 0, 0));
                 if (FP8)
-                    ksc[t] = *(const f32x4 *)(a.cache.ks + ((page[t] * (size_t)kv + head) << pl) + row + 4 * quad);
+                    ksc[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                        window_at(a.cache.ks, 4 * rows_at[t], there ? 64 : 0), 16 * quad, 0, 0));
             }
         };
-        auto load_v = [&](uint32_t key) {
+        auto load_v = [&]() {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const size_t row = (key + 16 * t) & mask;
-                const uint8_t *p = (const uint8_t *)a.cache.v + (page[t] * (size_t)kv) * page_bytes + head_bytes + row * d * ROWB;
+                const bool there = !(hole >> t & 1);
+                const __amdgpu_buffer_rsrc_t p = window_at(a.cache.v, rows_at[t] * row_bytes, there ? 16 * row_bytes : 0);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    load_elements<VW>(p + v_off + j * d * ROWB + v_col * ROWB, vr[4 * t + j]);
+                    load_dwords<VW>(p, v_off[j], vr[4 * t + j]);
                 if (FP8)
-                    vsc[t] = *(const f32x4 *)(a.cache.vs + ((page[t] * (size_t)kv + head) << pl) + row + 4 * quad);
+                    vsc[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                        window_at(a.cache.vs, 4 * rows_at[t], there ? 64 : 0), 16 * quad, 0, 0));
             }
+        };
+        // elements 2 e and 2 e + 1 of the lane's 8 keys, in BF16
+        auto pair = [&](int e, uint32_t *x) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if constexpr (!FP8)
+                    x[k] = vr[k][e % VW];
+                else if (e % 2)
+                    x[k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[k][e / 2], 1.0f, true));
+                else
+                    x[k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[k][e / 2], 1.0f, false));
+            }
+        };
+        // element 2 e (odd: 2 e + 1) of the keys in the operand's order
+        auto turned = [&](const uint32_t *x, bool second) {
+            u32x4 r;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                r[k] = __builtin_amdgcn_perm(x[2 * k + 1], x[2 * k], second ? 0x07060302u : 0x05040100u);
+            return r;
         };
 
         uint32_t key = key_from + STEP * wave;
-        if (key < key_to) {
-            pages(key);
-            load_k(key);
-            load_v(key);
-        }
+        pages_next = look(key);
+        places(key);
+        load_k();
+        load_v();
+#pragma unroll 1
         for (; key < key_to; key += TILE) {
-            const uint32_t hole_now = hole;
+            const uint32_t hole_now = hole, next = key + TILE;
             // ---- scores
             f32x4 s[NQ][2];
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq)
+                s[nq][0] = s[nq][1] = (f32x4){0, 0, 0, 0};
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    s[nq][t] = (f32x4){0, 0, 0, 0};
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        u32x4 kw = FP8 ? bf16_of_e4m3((u32x2){kr[t][ks / 2][2 * (ks % 2)], kr[t][ks / 2][2 * (ks % 2) + 1]})
-                                       : kr[t][FP8 ? 0 : ks];
+                for (int ks = 0; ks < KS; ++ks) {
+                    u32x4 kw = kr[t][FP8 ? ks / 2 : ks];
+                    if constexpr (FP8)
+                        kw = bf16_of_e4m3((u32x2){kw[2 * (ks % 2)], kw[2 * (ks % 2) + 1]});
+#pragma unroll
+                    for (int nq = 0; nq < NQ; ++nq)
                         s[nq][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kw), qf[nq][ks],
                                                                            s[nq][t], 0, 0, 0);
+                }
+            float unit_scale = scale;
+            if constexpr (FP8) {
+                unit_scale = 1.0f;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const f32x4 z = ksc[t] * scale;
+#pragma unroll
+                    for (int nq = 0; nq < NQ; ++nq)
+                        s[nq][t] *= z;
+                }
+            }
+            // (always, so that the registers stay the same ones: past the end nothing is fetched)
+            places(next);
+            load_k();
+
+            // ---- a step that some row sees only in part
+            if ((int)key < all_from || (int)(key + STEP) > all_to || hole_now) {
+                const int first = (int)key + 4 * (int)here(quad);     // of the lane's keys first + 16 t + i
+                uint32_t odd = 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int at = first + 16 * (k / 4) + k % 4;
+                    const bool whole = !(hole_now >> (k / 4) & 1);
+#pragma unroll
+                    for (int nq = 0; nq < NQ; ++nq) {
+                        const bool sees = whole && at <= pos[nq] && (!a.window || (uint32_t)(pos[nq] - at) < a.window);
+                        float x = sees ? s[nq][k / 4][k % 4] : -INFINITY;
+                        asm volatile("" : "+v"(x));
+                        s[nq][k / 4][k % 4] = x;
+                    }
+                    // V's rows that no row of Q sees, as zeros (0 times NaN is NaN)
+                    const bool any = whole && at >= q.first && at < q.len;
+#pragma unroll
+                    for (int e = 0; e < VW; ++e) {
+                        uint32_t x = any ? vr[k][e] : 0u;
+                        asm volatile("" : "+v"(x));
+                        vr[k][e] = x;
+                        // E4M3's NaN codes are 0x7F and 0xFF: one more carries into their top bits
+                        odd |= FP8 ? ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u : odd_tops(x);
                     }
                 }
-            f32x4 sk[2], sv[2];
+                if (__any(odd != 0)) {
+                    // NaN or an infinity that some rows see: noted for them, and kept from the others as a zero
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                sk[t] = FP8 ? ksc[t] * scale : (f32x4){scale, scale, scale, scale};
-                sv[t] = FP8 ? vsc[t] : (f32x4){1, 1, 1, 1};
-            }
-            const uint32_t next = key + TILE;
-            if (next < key_to) {
-                pages(next);
-                load_k(next);
-            }
-
-            // ---- probabilities; a step that some row sees only in part is masked
-            const bool whole = (int)key >= all_from && (int)(key + STEP) <= all_to && hole_now == 0;
-            uint32_t seen[NQ];             // bit 4t+i: the lane's row sees that key
+                    for (int k = 0; k < 8; ++k) {
+                        uint32_t bits = 0;
 #pragma unroll
-            for (int nq = 0; nq < NQ; ++nq) {
-                seen[nq] = 0xFF;
-                if (!whole) {
-                    seen[nq] = 0;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int k = (int)(key + 16 * t + 4 * quad) + i;
-                            const bool see = k <= pos[nq] && (!a.window || (uint32_t)(pos[nq] - k) < a.window) &&
-                                             !(hole_now >> t & 1);
-                            seen[nq] |= (uint32_t)see << (4 * t + i);
+                        for (int e = 0; e < VW; ++e) {
+                            if constexpr (FP8) {
+                                const uint32_t z = ((vr[k][e] & 0x7F7F7F7Fu) + 0x01010101u) >> 7 & 0x01010101u;
+                                bits |= (z * 0x10204080u >> 28) << 4 * e;         // bytes 0..3 to bits 0..3
+                                vr[k][e] &= ~(z * 0xFFu);
+                            } else {
+                                const uint32_t z = not_finite(vr[k][e]);
+                                bits |= ((z & 1u) | z >> 30 & 2u) << 2 * e;
+                                vr[k][e] &= ~z;
+                            }
                         }
+                        odd_bits[wave][16 * (k / 4) + 4 * quad + k % 4][col] = (uint16_t)bits;
+                    }
+#pragma unroll 1
+                    for (int k = 0; k < (int)STEP; ++k) {
+                        const int at = (int)key + k;
+#pragma unroll
+                        for (int nq = 0; nq < NQ; ++nq)
+                            if (at <= pos[nq] && (!a.window || (uint32_t)(pos[nq] - at) < a.window) && !(hole_now >> (k / 16) & 1))
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    nans[nq][i / 2] |= (uint32_t)odd_bits[wave][k][4 * quad + i] << 16 * (i % 2);
+                    }
                 }
             }
+
+            // ---- probabilities
             bf16x8 pf[NQ];
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq) {
                 float top = -INFINITY, p[8];
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        p[4 * t + i] = s[nq][t][i] * sk[t][i];
-                        if (!whole)
-                            p[4 * t + i] = seen[nq] >> (4 * t + i) & 1 ? p[4 * t + i] : -INFINITY;
-                        top = __builtin_fmaxf(top, p[4 * t + i]);
-                    }
+                for (int i = 0; i < 4; ++i)
+                    top = __builtin_fmaxf(__builtin_fmaxf(top, s[nq][0][i]), s[nq][1][i]);
+                top *= unit_scale;
                 if (__any(top > m[nq] + 8.0f)) {
                     // the row's four lanes agree on a new maximum; what was summed under the old one fades
                     top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
@@ -337,13 +421,10 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
                 u32x4 w4;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    p[i] = __builtin_amdgcn_exp2f(p[i] - base[nq]);
+                    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nq][i / 4][i % 4], unit_scale, -base[nq]));
                     part += p[i];
-                    if (FP8) {
-                        p[i] *= sv[i / 4][i % 4];
-                        if (!whole)
-                            p[i] = seen[nq] >> i & 1 ? p[i] : 0.0f;
-                    }
+                    if (FP8)
+                        p[i] *= finite_scale(vsc[i / 4][i % 4]);
                 }
                 l[nq] += part;
                 // rounded to BF16, the operand's type (2^-9 of each on average over keys, as the output's own rounding)
@@ -353,82 +434,20 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
                 pf[nq] = __builtin_bit_cast(bf16x8, w4);
             }
 
-            // ---- V in BF16, keys that no row sees as zeros (0 times NaN is NaN)
-            uint32_t vb[8][EPL / 2];
+            // ---- V
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if constexpr (FP8) {
+            for (int e = 0; e < EPL / 2; ++e) {
+                uint32_t x[8];
+                pair(e, x);
 #pragma unroll
-                    for (int e = 0; e < VW; ++e) {
-                        vb[k][2 * e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[k][e], 1.0f, false));
-                        vb[k][2 * e + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[k][e], 1.0f, true));
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < EPL / 2; ++e)
-                        vb[k][e] = vr[k][e];
-                }
-            }
-            uint32_t odd = 0;
-            if (!whole) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int at = (int)(key + 16 * (k / 4) + 4 * quad) + k % 4;
-                    const bool any = at >= q.first && at < q.len && !(hole_now >> (k / 4) & 1);
-#pragma unroll
-                    for (int e = 0; e < EPL / 2; ++e) {
-                        vb[k][e] = any ? vb[k][e] : 0u;
-                        odd |= not_finite(vb[k][e]);
-                    }
-                }
-            }
-            auto turned = [&](int j) {
-                // element j of the lane's 8 keys
-                constexpr uint32_t LO = 0x05040100u, HI = 0x07060302u;
-                u32x4 r;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    r[k] = __builtin_amdgcn_perm(vb[2 * k + 1][j / 2], vb[2 * k][j / 2], j % 2 ? HI : LO);
-                return r;
-            };
-            if (!whole && __any(odd != 0)) {
-                // NaN or an infinity that some rows see: it stays away from the
-                // others' sums, and makes NaN of those that see it
-#pragma unroll
-                for (int j = 0; j < EPL; ++j) {
-                    u32x4 vf = turned(j), bad;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t z = not_finite(vf[i]);
-                        bad[i] = z & 0x3F803F80u;
-                        vf[i] &= ~z;
-                    }
-#pragma unroll
-                    for (int nq = 0; nq < NQ; ++nq) {
-                        u32x4 ones;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            ones[i] = (seen[nq] >> (2 * i) & 1 ? 0x3F80u : 0u) | (seen[nq] >> (2 * i + 1) & 1 ? 0x3F800000u : 0u);
-                        const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, bad), __builtin_bit_cast(bf16x8, ones), (f32x4){0, 0, 0, 0}, 0, 0, 0);
-                        acc[nq][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, vf), pf[nq], acc[nq][j],
-                                                                             0, 0, 0);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[nq][j][i] = hit[i] > 0.0f ? __builtin_nanf("") : acc[nq][j][i];
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < EPL; ++j) {
-                    const bf16x8 vf = __builtin_bit_cast(bf16x8, turned(j));
+                for (int h = 0; h < 2; ++h) {
+                    const bf16x8 vf = __builtin_bit_cast(bf16x8, turned(x, h));
 #pragma unroll
                     for (int nq = 0; nq < NQ; ++nq)
-                        acc[nq][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[nq], acc[nq][j], 0, 0, 0);
+                        acc[nq][2 * e + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[nq], acc[nq][2 * e + h], 0, 0, 0);
                 }
             }
-            if (next < key_to)
-                load_v(next);
+            load_v();
         }
 
         // ---- the four waves join; a lane holds d = EPL (4 quad + i) + j of row col
@@ -452,9 +471,8 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
             for (int i = 0; i < 4; ++i) {
                 float *dst = &o_lds[wave][16 * nq + col][EPL * (4 * quad + i)];
 #pragma unroll
-                for (int j = 0; j < EPL; j += 4)
-                    *(f32x4 *)(dst + j) = (f32x4){acc[nq][j][i] * f, acc[nq][j + 1][i] * f, acc[nq][j + 2][i] * f,
-                                                  acc[nq][j + 3][i] * f};
+                for (int j = 0; j < EPL; ++j)
+                    dst[j] = nans[nq][i / 2] >> (16 * (i % 2) + j) & 1 ? __builtin_nanf("") : acc[nq][j][i] * f;
             }
         }
         __syncthreads();
@@ -580,12 +598,23 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, Parts parts, uint
 }
 
 template <int DP, int NQ>
-void launch(const AttnArgs &a, const Parts &p, uint32_t shares, hipStream_t st)
+void launch_rows(const AttnArgs &a, const Parts &p, uint32_t shares, hipStream_t st)
 {
     if (a.cache.fp8)
         k_attn_decode<DP, NQ, true><<<shares, WG, 0, st>>>(a, p, shares);
     else
         k_attn_decode<DP, NQ, false><<<shares, WG, 0, st>>>(a, p, shares);
+}
+
+template <int DP>
+void launch(const AttnArgs &a, const Parts &p, uint32_t rows, uint32_t shares, hipStream_t st)
+{
+    if (rows <= 16)
+        launch_rows<DP, 1>(a, p, shares, st);
+    else if (rows <= 32 || DP == 256)
+        launch_rows<DP, 2>(a, p, shares, st);
+    else
+        launch_rows<DP == 256 ? 64 : DP, DP == 256 ? 1 : 4>(a, p, shares, st);
 }
 
 } // namespace
@@ -604,32 +633,37 @@ hipError_t launch_attn_join(const AttnArgs &a, const Parts &p, uint32_t shares, 
     return hipGetLastError();
 }
 
-static uint32_t max_shares()
+// Rows of a workgroup, in 16s that the kernel is built for.
+static uint32_t room(uint32_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+// As many workgroups as the chip holds at a time.
+static uint32_t max_shares(uint32_t rows, uint32_t d)
 {
-    return 2 * (cu_count() ? cu_count() : 256);
+    return (rows <= 16 && d <= 128 ? 2 : 1) * (cu_count() ? cu_count() : 256);
 }
 
-uint64_t decode_work(uint32_t d)
+uint64_t decode_work(uint32_t rows, uint32_t d)
 {
-    return parts_bytes(max_shares(), DECODE_ROWS, d);
+    return parts_bytes(max_shares(rows, d), room(rows), d);
 }
 
 hipError_t launch_attn_decode(const AttnArgs &a, hipStream_t st)
 {
+    const uint32_t rows = a.max_q * (a.q_heads / a.cache.heads), d = a.cache.d;
     // no more workgroups than the table has room for tiles
     const uint64_t most = (uint64_t)a.seqs * a.cache.heads * ((((uint64_t)a.width << a.cache.page_log2) + TILE - 1) / TILE);
-    const uint32_t shares = (uint32_t)min((uint64_t)max_shares(), most);
-    const Parts p = parts_at(a.work, shares, DECODE_ROWS);
-    if (a.cache.d <= 64)
-        launch<64, 1>(a, p, shares, st);
-    else if (a.cache.d <= 128)
-        launch<128, 1>(a, p, shares, st);
+    const uint32_t shares = (uint32_t)min((uint64_t)max_shares(rows, d), most);
+    const Parts p = parts_at(a.work, shares, room(rows));
+    if (d <= 64)
+        launch<64>(a, p, rows, shares, st);
+    else if (d <= 128)
+        launch<128>(a, p, rows, shares, st);
     else
-        launch<256, 1>(a, p, shares, st);
+        launch<256>(a, p, rows, shares, st);
     count_launch();
     if (hipError_t e = hipGetLastError())
         return e;
-    return launch_attn_join(a, p, shares, DECODE_ROWS, a.max_q * (a.q_heads / a.cache.heads), st);
+    return launch_attn_join(a, p, shares, room(rows), rows, st);
 }
 
 } // namespace attn

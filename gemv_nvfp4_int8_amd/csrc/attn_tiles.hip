@@ -29,21 +29,12 @@ typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) void lds_void;
 
-__device__ const u32x4 ZEROS[1] = {{0, 0, 0, 0}};
 
 // The XOR of row r's piece numbers.
 template <int DP>
 __device__ __forceinline__ uint32_t swizzle(uint32_t r)
 {
     return DP == 64 ? (r >> 1 & 1) << 2 | (r >> 2 & 3) : (r & 3) << 2 | (r >> 2 & 3);
-}
-
-// The same value, computed where it is used: what follows from it is not kept in
-// registers through the loop.
-__device__ __forceinline__ uint32_t here(uint32_t v)
-{
-    asm volatile("" : "+v"(v));
-    return v;
 }
 
 // A block of a sequence's rows: which keys any of them sees.
@@ -235,16 +226,17 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
         const int32_t *table = a.table + (size_t)seq * a.width;
         const uint32_t page_elems = (kv * d) << pl, head_elems = (head * d) << pl;   // of one page: below 2^31
         const uint32_t mask = (1u << pl) - 1;
-        // the lane's element of those 16 rows: piece c of LDS row r holds piece
+        // the lane's bytes of those 16 rows: piece c of LDS row r holds piece
         // c ^ swizzle(r) of the head's row; what lies past d is read from its start and
         // meets zeros of Q, or is not stored.  Row r % 16 is the same for every second
         // piece of a thread at least.
+        constexpr uint32_t EB = FP8 ? 1 : 2;               // bytes of an element
         uint32_t lane_at[2];
 #pragma unroll
         for (uint32_t i = 0; i < 2; ++i) {
             const uint32_t it = tid + WG * i, r = it / CPR;
             const uint32_t e = FP8 ? it % CPR * 16 : (it % CPR ^ swizzle<DP>(r)) * 8;
-            lane_at[i] = r % 16 * d + (e < d ? e : 0);
+            lane_at[i] = (r % 16 * d + (e < d ? e : 0)) * EB;
         }
         u32x4 kr[FP8 ? ITEMS : 1], vr[FP8 ? ITEMS : 1];
         float ksr = 0.0f, vsr = 0.0f;
@@ -268,43 +260,19 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
                 gaps |= (uint32_t)(page[g] >= a.cache.pages) << g;
             }
             const int k0 = tile * KT;
-            // a page's row 16 g of the tile, in elements
-            auto row_of = [&](uint32_t pg, uint32_t g) {
-                return (uint64_t)pg * page_elems + (head_elems + ((k0 + 16 * g) & mask) * d);
-            };
-            const bool inside = k0 >= blk.from && k0 + (int)KT <= blk.to && gaps == 0;
-            if constexpr (FP8) {
 #pragma unroll
-                for (uint32_t i = 0; i < ITEMS; ++i) {
-                    const uint32_t g = uniform((64 * wave + WG * i) / CPR / 16);
-                    const int key = k0 + (int)((here(threadIdx.x) + WG * i) / CPR);
-                    const uint64_t at = row_of(page[g], g) + lane_at[i % 2];
-                    // what no row sees is read as zeros
-                    const bool fine = inside || (key >= blk.from && key < blk.to && page[g] < a.cache.pages);
-                    kr[i] = *(const u32x4 *)(fine ? (const uint8_t *)a.cache.k + at : (const uint8_t *)ZEROS);
-                    vr[i] = *(const u32x4 *)(fine ? (const uint8_t *)a.cache.v + at : (const uint8_t *)ZEROS);
-                }
-            } else if (inside) {
-#pragma unroll
-                for (uint32_t i = 0; i < ITEMS; ++i) {
-                    const uint32_t g = uniform((64 * wave + WG * i) / CPR / 16);
-                    const uint64_t base = 2 * row_of(page[g], g);
+            for (uint32_t i = 0; i < ITEMS; ++i) {
+                const uint32_t g = uniform((64 * wave + WG * i) / CPR / 16);
+                const uint64_t row = (uint64_t)page[g] * page_elems + (head_elems + ((k0 + 16 * g) & mask) * d);
+                const uint32_t bytes = page[g] < a.cache.pages ? 16 * d * EB : 0;      // a hole is read as zeros
+                const __amdgpu_buffer_rsrc_t kp = window_at(a.cache.k, row * EB, bytes), vp = window_at(a.cache.v, row * EB, bytes);
+                if constexpr (FP8) {
+                    kr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(kp, lane_at[i % 2], 0, 0));
+                    vr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(vp, lane_at[i % 2], 0, 0));
+                } else {
                     const uint32_t to = 16 * (64 * wave + WG * i);
-                    __builtin_amdgcn_global_load_lds((const uint8_t *)a.cache.k + base + 2 * lane_at[i % 2], (lds_void *)(kd + to), 16, 0, 0);
-                    __builtin_amdgcn_global_load_lds((const uint8_t *)a.cache.v + base + 2 * lane_at[i % 2], (lds_void *)(vd + to), 16, 0, 0);
-                }
-            } else {
-                // not unrolled, so that it is not made one with the loop above
-#pragma unroll 1
-                for (uint32_t i = 0; i < ITEMS; ++i) {
-                    const uint32_t g = uniform((64 * wave + WG * i) / CPR / 16), pg = __builtin_amdgcn_readlane(pages, 4 * at + g);
-                    const int key = k0 + (int)((here(threadIdx.x) + WG * i) / CPR);
-                    const uint64_t from = 2 * (row_of(pg, g) + here(ITEMS > 1 && CPR == 32 ? (i % 2 ? lane_at[1] : lane_at[0]) : lane_at[0]));
-                    const uint32_t to = 16 * (64 * wave + WG * i);
-                    // what no row sees is read as zeros
-                    const bool fine = key >= blk.from && key < blk.to && pg < a.cache.pages;
-                    __builtin_amdgcn_global_load_lds(fine ? (const uint8_t *)a.cache.k + from : (const uint8_t *)ZEROS, (lds_void *)(kd + to), 16, 0, 0);
-                    __builtin_amdgcn_global_load_lds(fine ? (const uint8_t *)a.cache.v + from : (const uint8_t *)ZEROS, (lds_void *)(vd + to), 16, 0, 0);
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(kp, (lds_void *)(kd + to), 16, lane_at[i % 2], 0, 0, 0);
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(vp, (lds_void *)(vd + to), 16, lane_at[i % 2], 0, 0, 0);
                 }
             }
             const uint32_t tid = here(threadIdx.x);
