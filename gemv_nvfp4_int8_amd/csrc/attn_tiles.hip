@@ -240,31 +240,36 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
         }
         u32x4 kr[FP8 ? ITEMS : 1], vr[FP8 ? ITEMS : 1];
         float ksr = 0.0f, vsr = 0.0f;
-        // lane i: the page of the 16 keys 16 i behind the first tile's, or behind 16 tiles later and so on
-        uint32_t pages = 0, pages_next = 0;
+        // Where 16 tiles' 16s of keys lie, in elements: lane i's is of the keys 16 i
+        // behind the first tile's (or 16, 32, ... tiles later); and which of them are holes.
+        uint32_t at_lo = 0, at_hi = 0, page_next = 0;
+        uint64_t missing = 0, row_at = 0;                  // (the same in rows, for the scales)
         auto look = [&](uint32_t tile) {
             const uint32_t key = tile * KT + 16 * lane;
-            return key < (uint32_t)blk.to && tile < t_end ? (uint32_t)table[key >> pl] : ~0u;
+            page_next = key < (uint32_t)blk.to && tile < t_end ? (uint32_t)table[key >> pl] : ~0u;
         };
         // Starts a tile's loads; returns its 16s of keys that are holes, as bits.
         auto load = [&](uint32_t tile, uint8_t *kd, uint8_t *vd) {
-            const uint32_t at = (tile - (blk.first_tile + off)) % 16;
-            if (at == 0) {
-                pages = pages_next;
-                pages_next = look(tile + 16);
+            const uint32_t nth = (tile - (blk.first_tile + off)) % 16;
+            if (nth == 0) {
+                const bool hole = page_next >= a.cache.pages;
+                const uint64_t at = (uint64_t)(hole ? 0 : page_next) * page_elems + (head_elems + ((tile * KT + 16 * lane) & mask) * d);
+                missing = __ballot(hole);
+                at_lo = (uint32_t)at;
+                at_hi = (uint32_t)(at >> 32);
+                if (FP8)
+                    row_at = (((hole ? 0 : page_next) * (uint64_t)kv + head) << pl) + ((tile * KT + 16 * lane) & mask);
+                look(tile + 16);
             }
-            uint32_t page[KT / 16], gaps = 0;
-#pragma unroll
-            for (uint32_t g = 0; g < KT / 16; ++g) {
-                page[g] = __builtin_amdgcn_readlane(pages, 4 * at + g);
-                gaps |= (uint32_t)(page[g] >= a.cache.pages) << g;
-            }
-            const int k0 = tile * KT;
+            const uint32_t gaps = (uint32_t)(missing >> 4 * nth) & 15;
 #pragma unroll
             for (uint32_t i = 0; i < ITEMS; ++i) {
-                const uint32_t g = uniform((64 * wave + WG * i) / CPR / 16);
-                const uint64_t row = (uint64_t)page[g] * page_elems + (head_elems + ((k0 + 16 * g) & mask) * d);
-                const uint32_t bytes = page[g] < a.cache.pages ? 16 * d * EB : 0;      // a hole is read as zeros
+                // the 16 keys that this wave's pieces are of
+                constexpr uint32_t WAVE_ROWS = 64 / CPR;
+                const uint32_t g = i * (WG / CPR) / 16 + (WAVE_ROWS * NW > 16 ? wave * WAVE_ROWS / 16 : 0);
+                const uint64_t row = (uint64_t)(uint32_t)__builtin_amdgcn_readlane(at_hi, 4 * nth + g) << 32 |
+                                     (uint32_t)__builtin_amdgcn_readlane(at_lo, 4 * nth + g);
+                const uint32_t bytes = gaps >> g & 1 ? 0 : 16 * d * EB;                // a hole is read as zeros
                 const __amdgpu_buffer_rsrc_t kp = window_at(a.cache.k, row * EB, bytes), vp = window_at(a.cache.v, row * EB, bytes);
                 if constexpr (FP8) {
                     kr[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(kp, lane_at[i % 2], 0, 0));
@@ -275,13 +280,12 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
                     __builtin_amdgcn_raw_ptr_buffer_load_lds(vp, (lds_void *)(vd + to), 16, lane_at[i % 2], 0, 0, 0);
                 }
             }
-            const uint32_t tid = here(threadIdx.x);
             if (FP8 && tid < KT) {
-                // all of the first wave
-                const uint32_t pg = __shfl(pages, 4 * at + tid / 16, 64);
-                const uint64_t s = pg < a.cache.pages ? ((pg * (uint64_t)kv + head) << pl) + ((k0 + tid) & mask) : 0;
-                ksr = a.cache.ks[s];
-                vsr = a.cache.vs[s];
+                // the first wave: a scale of K and of V each, of the keys' rows of the cache
+                const uint64_t row = __shfl(row_at, 4 * nth + lane / 16, 64) + lane % 16;
+                const bool hole = gaps >> lane / 16 & 1;
+                ksr = hole ? 0.0f : a.cache.ks[row];
+                vsr = hole ? 0.0f : a.cache.vs[row];
             }
             return gaps;
         };
@@ -431,7 +435,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
 
         uint32_t tile = blk.first_tile + off;
         const int block_lo = old + (int)(row0 / group), block_hi = old + (int)((row0 + rows - 1) / group);
-        pages_next = look(tile);
+        look(tile);
         __syncthreads();                   // the last unit's tiles have been read
         uint32_t gaps_next = load(tile, k_lds0, v_lds0);
         store(0, k_lds0, v_lds0);
