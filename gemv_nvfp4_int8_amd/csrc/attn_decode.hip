@@ -524,32 +524,36 @@ __global__ __launch_bounds__(WG, NQ == 1 && DP <= 128 ? 2 : 1) void k_attn_decod
         parts.begun[w].last = -1;
 }
 
-// One workgroup per share and row: LP lanes take a part's row, 16 bytes each;
-// the groups of lanes take the parts in turn and join through LDS.
-template <int LP>
+// LP lanes take a row of a part, 16 bytes each, and a workgroup has G such groups.
+// BY_ROW: a group goes through all parts of a row of its own.  Otherwise (few rows
+// of many parts) the groups share a row's parts and join through LDS.
+template <int LP, bool BY_ROW>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, Parts parts, uint32_t rows)
 {
     constexpr uint32_t G = 256 / LP;
-    __shared__ float o_lds[G][4 * LP];
-    __shared__ f32x2 ml_lds[G];
+    __shared__ float o_lds[BY_ROW ? 1 : G][4 * LP];
+    __shared__ f32x2 ml_lds[BY_ROW ? 1 : G];
     const Begun b = parts.begun[blockIdx.x];
     if (b.last < 0)
         return;
     const uint32_t d = a.cache.d, group = a.q_heads / a.cache.heads, g = threadIdx.x / LP, e = 4 * (threadIdx.x % LP);
     const uint32_t from = blockIdx.x, count = b.last - from + 1;
-    for (uint32_t r = blockIdx.y; r < (uint32_t)b.rows; r += gridDim.y) {
+    const uint32_t per = BY_ROW ? G : 1;
+    for (uint32_t r0 = blockIdx.y * per; r0 < (uint32_t)b.rows; r0 += gridDim.y * per) {
+        const uint32_t r = r0 + (BY_ROW ? g : 0);
         float m = -INFINITY, l = 0.0f;
         f32x4 acc = {0, 0, 0, 0};
         constexpr int U = 4;
-        for (uint32_t p0 = g; p0 < count; p0 += U * G) {
+        const uint32_t step = BY_ROW ? 1 : G;
+        for (uint32_t p0 = BY_ROW ? 0 : g; p0 < count; p0 += U * step) {
             f32x2 ml[U];
             f32x4 o[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const uint32_t p = p0 + u * G;
+                const uint32_t p = p0 + u * step;
                 ml[u] = (f32x2){-INFINITY, 0.0f};
                 o[u] = (f32x4){0, 0, 0, 0};
-                if (p < count) {
+                if (p < count && r < (uint32_t)b.rows) {
                     const size_t at = (2 * (size_t)(from + p) + (p == 0)) * rows + r;
                     ml[u] = parts.ml[at];
                     if (e < d)
@@ -572,12 +576,14 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, Parts parts, uint
             }
             m = top;
         }
-        __syncthreads();
-        *(f32x4 *)&o_lds[g][e] = acc;
-        if (e == 0)
-            ml_lds[g] = (f32x2){m, l};
-        __syncthreads();
-        if (g == 0 && e < d) {
+        if constexpr (!BY_ROW) {
+            __syncthreads();
+            *(f32x4 *)&o_lds[g][e] = acc;
+            if (e == 0)
+                ml_lds[g] = (f32x2){m, l};
+            __syncthreads();
+            if (g != 0)
+                continue;
             float top = -INFINITY;
             for (uint32_t u = 0; u < G; ++u)
                 top = __builtin_fmaxf(top, ml_lds[u][0]);
@@ -589,12 +595,26 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, Parts parts, uint
                 l += ml_lds[u][1] * f;
                 acc += *(const f32x4 *)&o_lds[u][e] * f;
             }
+        }
+        if (e < d && r < (uint32_t)b.rows) {
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             const uint32_t flat = b.row + r, tok = flat / group;
             *(u32x2 *)(a.out + ((size_t)(b.token + tok) * a.q_heads + b.head * group + (flat - tok * group)) * d + e) =
                 (u32x2){pk_bf16(acc[0] * inv, acc[1] * inv), pk_bf16(acc[2] * inv, acc[3] * inv)};
         }
     }
+}
+
+template <int LP>
+void join(const AttnArgs &a, const Parts &p, uint32_t shares, uint32_t rows, uint32_t live, hipStream_t st)
+{
+    constexpr uint32_t G = 256 / LP;
+    // a unit has about shares / units parts
+    const uint64_t units = max((uint64_t)a.seqs * a.cache.heads, (uint64_t)a.t * a.q_heads / rows);
+    if (live >= G && shares <= 8 * units)
+        k_attn_join<LP, true><<<dim3(shares, (live + G - 1) / G), 256, 0, st>>>(a, p, rows);
+    else
+        k_attn_join<LP, false><<<dim3(shares, min(live, 32u)), 256, 0, st>>>(a, p, rows);
 }
 
 template <int DP, int NQ>
@@ -622,13 +642,12 @@ void launch(const AttnArgs &a, const Parts &p, uint32_t rows, uint32_t shares, h
 hipError_t launch_attn_join(const AttnArgs &a, const Parts &p, uint32_t shares, uint32_t rows, uint32_t live,
                             hipStream_t st)
 {
-    const dim3 grid(shares, min(live, 32u));
     if (a.cache.d <= 64)
-        k_attn_join<16><<<grid, 256, 0, st>>>(a, p, rows);
+        join<16>(a, p, shares, rows, live, st);
     else if (a.cache.d <= 128)
-        k_attn_join<32><<<grid, 256, 0, st>>>(a, p, rows);
+        join<32>(a, p, shares, rows, live, st);
     else
-        k_attn_join<64><<<grid, 256, 0, st>>>(a, p, rows);
+        join<64>(a, p, shares, rows, live, st);
     count_launch();
     return hipGetLastError();
 }

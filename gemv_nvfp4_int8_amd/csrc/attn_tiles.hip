@@ -539,35 +539,33 @@ void launch(const AttnArgs &a, const Parts &p, uint32_t shares, hipStream_t st)
         k_attn_tiles<DP, NW, false><<<shares, 64 * NW, 0, st>>>(a, p, shares);
 }
 
-constexpr uint32_t UNIT_ROWS = 128;
+// Rows of a unit: four waves', or (64 < d <= 128) eight waves'.
+constexpr uint32_t unit_rows(uint32_t d) { return d > 64 && d <= 128 ? 256 : 128; }
 
-uint32_t max_shares(uint32_t d)
-{
-    // as many workgroups as the chip holds at a time
-    return (d <= 128 ? 2 : 1) * (cu_count() ? cu_count() : 256);
-}
+// As many workgroups as the chip holds at a time.
+uint32_t max_shares(uint32_t d) { return (d <= 64 ? 2 : 1) * (cu_count() ? cu_count() : 256); }
 
 } // namespace
 
 uint64_t tiles_work(uint32_t d)
 {
-    return parts_bytes(max_shares(d), UNIT_ROWS, d);
+    return parts_bytes(max_shares(d), unit_rows(d), d);
 }
 
 hipError_t launch_attn_tiles(const AttnArgs &a, hipStream_t st)
 {
-    const uint32_t shares = max_shares(a.cache.d);
-    const Parts p = parts_at(a.work, shares, UNIT_ROWS);
+    const uint32_t shares = max_shares(a.cache.d), rows = unit_rows(a.cache.d);
+    const Parts p = parts_at(a.work, shares, rows);
     if (a.cache.d <= 64)
         launch<64, 4>(a, p, shares, st);
     else if (a.cache.d <= 128)
-        launch<128, 4>(a, p, shares, st);
+        launch<128, 8>(a, p, shares, st);
     else
         launch<256, 4>(a, p, shares, st);
     count_launch();
     if (hipError_t e = hipGetLastError())
         return e;
-    return launch_attn_join(a, p, shares, UNIT_ROWS, UNIT_ROWS, st);
+    return launch_attn_join(a, p, shares, rows, rows, st);
 }
 
 } // namespace attn

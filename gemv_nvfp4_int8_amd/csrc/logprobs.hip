@@ -6,11 +6,14 @@
 // e = 2^y with y = (x - m) log2(e), and the sum t of e y, which is what the
 // entropy needs: H = ln s - ln 2 * t / s.  The largest logits of the wave so far
 // lie in a register, the i-th in lane i, as 64-bit keys (value, then the lower
-// token): an element enters them only if it passes the last of the list, a
-// ballot counts its place and the rest moves up one lane.  Few elements pass: the
-// list begins with a bound below its end, found by halving among the lanes'
-// maxima.  The four waves of a workgroup join through LDS; few rows are split over
-// several workgroups, whose waves' results a second launch joins.
+// token).  The first piece's are found by a bound that as many lanes' maxima
+// reach as are wanted (halving over the bits of the maxima), the few elements
+// that reach it being put into LDS, where each counts the larger ones: its place.
+// From then on an element enters only if it passes the last of the list, a ballot
+// counts its place and the rest moves up one lane.  The four waves of a workgroup
+// join through LDS, where again all keys that pass a bound count the larger ones;
+// where a row a workgroup would fill the chip badly, rows are split, and a second
+// launch joins the parts.
 #include "qp_device.hpp"
 #include "qp_launch.hpp"
 #include "decoder.hpp"
@@ -22,7 +25,7 @@ constexpr uint32_t WAVES = 4, WG = 64 * WAVES;
 constexpr int NV = 4;                      // 16-byte loads of a lane and piece
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
-// A wave's results: sums, and (behind them) the list of `top` keys.
+// A part's results: sums, and (behind all parts' sums) the list of `top` keys.
 struct Sums {
     float m, s, t, pad;
 };
@@ -56,6 +59,52 @@ struct List {
     }
 };
 
+// Enters what passes the `top`-th of the list, `least`, from a key a lane.
+__device__ __forceinline__ void merge(List &best, uint64_t &least, uint64_t k, uint32_t top, uint32_t lane)
+{
+    for (uint64_t who = __ballot(k > least); who; who &= who - 1) {
+        const uint64_t c = List{k}.at(__builtin_ctzll(who));
+        if (c > least) {
+            best.insert(c, lane);
+            least = best.at(top - 1);
+        }
+    }
+}
+
+// A wave's room in LDS for keys that pass a bound, and for them in order.
+constexpr uint32_t ROOM = 256;
+struct Bench {
+    uint64_t in[ROOM], out[64];
+};
+
+// Puts the lanes' keys that reach `bound` behind the first n; returns the new n,
+// which may be more than there is room for (then not all are there).
+__device__ __forceinline__ uint32_t collect(Bench &bench, uint32_t n, bool pass, uint64_t key)
+{
+    const uint64_t who = __ballot(pass);
+    const uint32_t at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+    if (pass && at < ROOM)
+        bench.in[at] = key;
+    return n + __popcll(who);
+}
+
+// The list of n <= ROOM collected keys: each counts the larger ones.
+__device__ __forceinline__ List in_order(Bench &bench, uint32_t n, uint32_t lane)
+{
+    __builtin_amdgcn_wave_barrier();
+    for (uint32_t i0 = 0; i0 < n; i0 += 64) {
+        const uint64_t mine = i0 + lane < n ? bench.in[i0 + lane] : 0;
+        uint32_t place = 0;
+#pragma unroll 4
+        for (uint32_t i = 0; i < n; ++i)
+            place += bench.in[i] > mine;
+        if (mine && place < 64)
+            bench.out[place] = mine;
+    }
+    __builtin_amdgcn_wave_barrier();
+    return {lane < n ? bench.out[lane] : 0};
+}
+
 // Adds (m, s, t) of another part to this one: what was summed under the lower maximum fades.
 __device__ __forceinline__ void fade_to(float to, float m, float &s, float &t)
 {
@@ -74,10 +123,43 @@ __device__ __forceinline__ float sum_over_wave(float v)
     return v;
 }
 
-// One wave: joins `parts` waves' results and writes the row's outputs.
+// One wave: the list of `parts` lists of `top` keys each, in order.  Each list has
+// h = ceil(top / parts) keys not below its h-th, so together they have `top` not
+// below the lowest of these: that is the bound.
+__device__ __forceinline__ List join_lists(const uint64_t *keys, uint32_t parts, uint32_t top, Bench &bench, uint32_t lane)
+{
+    const uint32_t h = (top + parts - 1) / parts;
+    uint64_t bound = ~0ull;
+    for (uint32_t p = lane; p < parts; p += 64)
+        bound = min(bound, keys[p * top + h - 1]);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1)
+        bound = min(bound, (uint64_t)__shfl_xor(bound, off, WAVE));
+    constexpr int U = 8;                   // loads on their way together
+    uint32_t n = 0;
+    for (uint32_t i0 = 0; i0 < parts * top; i0 += 64 * U) {
+        uint64_t k[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            k[u] = i0 + 64 * u + lane < parts * top ? keys[i0 + 64 * u + lane] : 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            n = collect(bench, n, k[u] != 0 && k[u] >= bound, k[u]);
+    }
+    if (n <= ROOM)
+        return in_order(bench, n, lane);
+    // more than there is room for (many equal logits): one after the other
+    List best = {lane < top ? keys[lane] : 0};
+    uint64_t least = best.at(top - 1);
+    for (uint32_t i = top; i < parts * top; i += 64)
+        merge(best, least, i + lane < parts * top ? keys[i + lane] : 0, top, lane);
+    return best;
+}
+
+// One wave: joins `parts` results and writes the row's outputs.
 template <bool F32>
 __device__ __forceinline__ void finish(const LogprobArgs &a, uint32_t row, const Sums *sums, const uint64_t *keys,
-                                       uint32_t parts, uint32_t lane)
+                                       uint32_t parts, Bench &bench, uint32_t lane)
 {
     const uint32_t target = a.targets ? (uint32_t)a.targets[row] : 0;
     float x = 0.0f;
@@ -109,18 +191,7 @@ __device__ __forceinline__ void finish(const LogprobArgs &a, uint32_t row, const
     }
     if (a.top == 0)
         return;
-    List best = {lane < a.top ? keys[lane] : 0};
-    uint64_t least = best.at(a.top - 1);
-    for (uint32_t i0 = a.top; i0 < parts * a.top; i0 += 64) {
-        const uint64_t k = i0 + lane < parts * a.top ? keys[i0 + lane] : 0;
-        for (uint64_t who = __ballot(k > least); who; who &= who - 1) {
-            const uint64_t c = List{k}.at(__builtin_ctzll(who));
-            if (c > least) {
-                best.insert(c, lane);
-                least = best.at(a.top - 1);
-            }
-        }
-    }
+    const List best = join_lists(keys, parts, a.top, bench, lane);
     if (lane < a.top) {
         const uint32_t id = 0xFFFFFFFFu - (uint32_t)best.key;
         // a row with NaN may have fewer than `top` values that compare
@@ -138,6 +209,7 @@ __global__ __launch_bounds__(WG) void k_logprobs(LogprobArgs a, uint32_t parts)
     constexpr uint32_t PIECE = 64 * NV * V;
     __shared__ Sums sums[WAVES];
     __shared__ uint64_t keys[WAVES * 32];
+    __shared__ Bench bench[WITH_TOP ? WAVES : 1];
     const uint32_t row = blockIdx.x / parts, part = blockIdx.x % parts;
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t begin = row * a.vocab, end = begin + a.vocab;    // below 2^31
@@ -232,8 +304,8 @@ __global__ __launch_bounds__(WG) void k_logprobs(LogprobArgs a, uint32_t parts)
         // ---- the largest
         if (!WITH_TOP)
             continue;
-        bool touched = false;              // the list has elements of this piece, which may lie behind its others
         if (first) {
+            first = false;
             // the largest value with 16 zeros behind it that `top` lanes' maxima reach
             const uint32_t u = ordered(top);
             uint32_t bound = 0;
@@ -241,13 +313,30 @@ __global__ __launch_bounds__(WG) void k_logprobs(LogprobArgs a, uint32_t parts)
             for (int b = 31; b >= 16; --b)
                 if ((uint32_t)__popcll(__ballot(u >= (bound | 1u << b))) >= a.top)
                     bound |= 1u << b;
-            if (bound > ordered(-INFINITY)) {           // below lie the keys that are no numbers
-                least = ((uint64_t)bound << 32) - 1;
-                least_x = from_ordered(bound);
+            // below -inf lie the keys that are no numbers
+            const float bound_x = bound > ordered(-INFINITY) ? from_ordered(bound) : -INFINITY;
+            uint32_t n = 0;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                if (!__any(most[v] >= bound_x))
+                    continue;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const uint32_t id = pos + (64 * v + lane) * V + j - begin;
+                    n = collect(bench[wave], n, x[v][j] >= bound_x && id < a.vocab,
+                                (uint64_t)ordered(x[v][j]) << 32 | (0xFFFFFFFFu - id));
+                }
             }
-            first = false;
-            touched = true;
+            if (n <= ROOM) {
+                best = in_order(bench[wave], n, lane);
+                least = best.at(a.top - 1);
+                least_x = least ? from_ordered((uint32_t)(least >> 32)) : -INFINITY;
+                if (least)
+                    continue;
+                best.key = 0;              // fewer than `top`: all over, one after the other
+            }
         }
+        bool touched = least == 0;         // the list has elements of this piece, which may lie behind its others
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             if (!__any(most[v] > least_x || (touched && most[v] == least_x)))
@@ -279,40 +368,60 @@ __global__ __launch_bounds__(WG) void k_logprobs(LogprobArgs a, uint32_t parts)
     fade_to(all, m, s, t);
     s = sum_over_wave(s);
     t = sum_over_wave(t);
-    Sums *to_sums = sums;
-    uint64_t *to_keys = keys;
-    uint32_t at = wave;
-    if (parts > 1) {
-        to_sums = (Sums *)a.work;
-        to_keys = (uint64_t *)(to_sums + (size_t)a.rows * parts * WAVES);
-        at = blockIdx.x * WAVES + wave;
-    }
     if (lane == 0)
-        to_sums[at] = {all, s, t, 0.0f};
+        sums[wave] = {all, s, t, 0.0f};
     if (WITH_TOP && lane < a.top)
-        to_keys[(size_t)at * a.top + lane] = best.key;
-    if (parts > 1)
-        return;
+        keys[wave * a.top + lane] = best.key;
     __syncthreads();
-    if (wave == 0)
-        finish<F32>(a, row, sums, keys, WAVES, lane);
+    if (wave != 0)
+        return;
+    if (parts == 1) {
+        finish<F32>(a, row, sums, keys, WAVES, bench[0], lane);
+        return;
+    }
+    // the workgroup's sums and list, for the join
+    float top = all;
+    for (uint32_t u = 1; u < WAVES; ++u)
+        top = __builtin_fmaxf(top, sums[u].m);
+    fade_to(top, all, s, t);
+    for (uint32_t u = 1; u < WAVES; ++u) {
+        Sums p = sums[u];
+        fade_to(top, p.m, p.s, p.t);
+        s += p.s;
+        t += p.t;
+    }
+    Sums *to_sums = (Sums *)a.work;
+    uint64_t *to_keys = (uint64_t *)(to_sums + (size_t)a.rows * parts);
+    if (lane == 0)
+        to_sums[blockIdx.x] = {top, s, t, 0.0f};
+    if (WITH_TOP) {
+        best = join_lists(keys, WAVES, a.top, bench[0], lane);
+        if (lane < a.top)
+            to_keys[(size_t)blockIdx.x * a.top + lane] = best.key;
+    }
 }
 
 template <bool F32>
 __global__ __launch_bounds__(64) void k_logprobs_join(LogprobArgs a, uint32_t parts)
 {
+    __shared__ Bench bench;
     const Sums *sums = (const Sums *)a.work;
-    const uint64_t *keys = (const uint64_t *)(sums + (size_t)a.rows * parts * WAVES);
-    const size_t first = (size_t)blockIdx.x * parts * WAVES;
-    finish<F32>(a, blockIdx.x, sums + first, keys + first * a.top, parts * WAVES, threadIdx.x);
+    const uint64_t *keys = (const uint64_t *)(sums + (size_t)a.rows * parts);
+    const size_t first = (size_t)blockIdx.x * parts;
+    finish<F32>(a, blockIdx.x, sums + first, keys + first * a.top, parts, bench, threadIdx.x);
 }
 
-// Workgroups of a row: one, unless that leaves compute units without any; then as
-// many as give each wave one piece, or fill the chip twice.
+// Workgroups of a row: as few as keep the chip's last round of workgroups from
+// being a poor one (its rounds rounded up are then at most 1/8 more than they
+// are), each wave having a piece of its own.
 uint32_t parts_of(uint32_t rows, uint32_t vocab, bool f32)
 {
-    const uint32_t cus = cu_count() ? cu_count() : 256, piece = 64 * NV * (f32 ? 4 : 8) * WAVES;
-    return max(1u, min((vocab + piece - 1) / piece, 2 * cus / rows));
+    const uint64_t cus = cu_count() ? cu_count() : 256, piece = 64 * NV * (f32 ? 4 : 8) * WAVES;
+    const uint64_t most = (vocab + piece - 1) / piece, room = 7 * cus;
+    uint64_t parts = 1;
+    while (parts < most && 8 * room * ((rows * parts + room - 1) / room) > 9 * rows * parts)
+        ++parts;
+    return (uint32_t)parts;
 }
 
 template <bool F32>
@@ -340,7 +449,7 @@ void launch(const LogprobArgs &a, hipStream_t st)
 uint64_t token_logprobs_work(uint32_t rows, uint32_t vocab, uint32_t top)
 {
     const uint64_t parts = max(parts_of(rows, vocab, false), parts_of(rows, vocab, true));
-    return parts > 1 ? (uint64_t)rows * parts * WAVES * (sizeof(Sums) + 8 * top) : 16;
+    return parts > 1 ? (uint64_t)rows * parts * (sizeof(Sums) + 8 * top) : 16;
 }
 
 hipError_t launch_token_logprobs(const LogprobArgs &a, hipStream_t st)
