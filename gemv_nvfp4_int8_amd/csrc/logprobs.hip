@@ -1,19 +1,18 @@
 // logprobs.hip -- log probabilities of given tokens, entropy and the most
 // probable tokens of rows of logits, in one pass over them.
 //
-// A wave goes through its pieces of a row 64 x NV x 16 bytes at a time and needs
-// nobody else until its end.  Each lane keeps a running maximum m, the sum s of
-// e = 2^y with y = (x - m) log2(e), and the sum t of e y, which is what the
-// entropy needs: H = ln s - ln 2 * t / s.  The largest logits of the wave so far
-// lie in a register, the i-th in lane i, as 64-bit keys (value, then the lower
-// token).  The first piece's are found by a bound that as many lanes' maxima
-// reach as are wanted (halving over the bits of the maxima), the few elements
-// that reach it being put into LDS, where each counts the larger ones: its place.
-// From then on an element enters only if it passes the last of the list, a ballot
-// counts its place and the rest moves up one lane.  The four waves of a workgroup
-// join through LDS, where again all keys that pass a bound count the larger ones;
-// where a row a workgroup would fill the chip badly, rows are split, and a second
-// launch joins the parts.
+// Each lane keeps a running maximum m, the sum s of e = 2^y with y = (x - m)
+// log2(e), and the sum t of e y, which is what the entropy needs:
+// H = ln s - ln 2 * t / s.
+// The most probable tokens cost the pass nothing: its 256 lanes' maxima are there
+// at its end, and what the n-th largest of them is, at least n elements reach.
+// The lanes that reach it (n of them, but for ties) have their elements looked
+// through again, n / 256 of the row; those that reach the bound, little more than
+// n, go to LDS as 64-bit keys (value, then the lower token), where each counts the
+// larger ones: its place.  Where more reach it than there is room for (many equal
+// logits), all elements go through a list in a register, one lane a place.
+// Rows are a workgroup's each; those of a last round that would leave much of the
+// chip empty are split, and a second launch joins their parts.
 #include "qp_device.hpp"
 #include "qp_launch.hpp"
 #include "decoder.hpp"
@@ -23,6 +22,7 @@ namespace {
 
 constexpr uint32_t WAVES = 4, WG = 64 * WAVES;
 constexpr int NV = 4;                      // 16-byte loads of a lane and piece
+constexpr uint32_t RESIDENT = 8;           // workgroups that a compute unit holds at a time
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 // A part's results: sums, and (behind all parts' sums) the list of `top` keys.
@@ -71,38 +71,33 @@ __device__ __forceinline__ void merge(List &best, uint64_t &least, uint64_t k, u
     }
 }
 
-// A wave's room in LDS for keys that pass a bound, and for them in order.
-constexpr uint32_t ROOM = 256;
+// Room in LDS for keys that reach a bound, and for the largest in order.
+constexpr uint32_t ROOM = 512;
 struct Bench {
     uint64_t in[ROOM], out[64];
+    uint32_t n;                            // keys that reached it: more than ROOM are not all there
 };
 
-// Puts the lanes' keys that reach `bound` behind the first n; returns the new n,
-// which may be more than there is room for (then not all are there).
-__device__ __forceinline__ uint32_t collect(Bench &bench, uint32_t n, bool pass, uint64_t key)
+__device__ __forceinline__ void collect(Bench &bench, uint64_t key)
 {
-    const uint64_t who = __ballot(pass);
-    const uint32_t at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
-    if (pass && at < ROOM)
+    const uint32_t at = atomicAdd(&bench.n, 1u);        // (in any order: they are put in order by value)
+    if (at < ROOM)
         bench.in[at] = key;
-    return n + __popcll(who);
 }
 
-// The list of n <= ROOM collected keys: each counts the larger ones.
-__device__ __forceinline__ List in_order(Bench &bench, uint32_t n, uint32_t lane)
+// The `top` largest of the n <= ROOM collected keys to bench.out, by `threads`
+// threads: each key counts the larger ones.
+__device__ __forceinline__ void in_order(Bench &bench, uint32_t n, uint32_t top, uint32_t thread, uint32_t threads)
 {
-    __builtin_amdgcn_wave_barrier();
-    for (uint32_t i0 = 0; i0 < n; i0 += 64) {
-        const uint64_t mine = i0 + lane < n ? bench.in[i0 + lane] : 0;
+    for (uint32_t i0 = thread; i0 < n; i0 += threads) {
+        const uint64_t mine = bench.in[i0];
         uint32_t place = 0;
 #pragma unroll 4
         for (uint32_t i = 0; i < n; ++i)
             place += bench.in[i] > mine;
-        if (mine && place < 64)
+        if (place < top)
             bench.out[place] = mine;
     }
-    __builtin_amdgcn_wave_barrier();
-    return {lane < n ? bench.out[lane] : 0};
 }
 
 // Adds (m, s, t) of another part to this one: what was summed under the lower maximum fades.
@@ -135,8 +130,11 @@ __device__ __forceinline__ List join_lists(const uint64_t *keys, uint32_t parts,
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1)
         bound = min(bound, (uint64_t)__shfl_xor(bound, off, WAVE));
+    bench.n = 0;
+    if (lane < 64)
+        bench.out[lane] = 0;
+    __builtin_amdgcn_wave_barrier();
     constexpr int U = 8;                   // loads on their way together
-    uint32_t n = 0;
     for (uint32_t i0 = 0; i0 < parts * top; i0 += 64 * U) {
         uint64_t k[U];
 #pragma unroll
@@ -144,10 +142,16 @@ __device__ __forceinline__ List join_lists(const uint64_t *keys, uint32_t parts,
             k[u] = i0 + 64 * u + lane < parts * top ? keys[i0 + 64 * u + lane] : 0;
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            n = collect(bench, n, k[u] != 0 && k[u] >= bound, k[u]);
+            if (k[u] != 0 && k[u] >= bound)
+                collect(bench, k[u]);
     }
-    if (n <= ROOM)
-        return in_order(bench, n, lane);
+    __builtin_amdgcn_wave_barrier();
+    const uint32_t n = __builtin_amdgcn_readfirstlane(bench.n);
+    if (n <= ROOM) {
+        in_order(bench, n, top, lane, 64);
+        __builtin_amdgcn_wave_barrier();
+        return {bench.out[lane]};
+    }
     // more than there is room for (many equal logits): one after the other
     List best = {lane < top ? keys[lane] : 0};
     uint64_t least = best.at(top - 1);
@@ -156,10 +160,10 @@ __device__ __forceinline__ List join_lists(const uint64_t *keys, uint32_t parts,
     return best;
 }
 
-// One wave: joins `parts` results and writes the row's outputs.
+// One wave: joins `parts` sums and writes the row's outputs.
 template <bool F32>
-__device__ __forceinline__ void finish(const LogprobArgs &a, uint32_t row, const Sums *sums, const uint64_t *keys,
-                                       uint32_t parts, Bench &bench, uint32_t lane)
+__device__ __forceinline__ void finish(const LogprobArgs &a, uint32_t row, const Sums *sums, uint32_t parts, List best,
+                                       uint32_t lane)
 {
     const uint32_t target = a.targets ? (uint32_t)a.targets[row] : 0;
     float x = 0.0f;
@@ -191,7 +195,6 @@ __device__ __forceinline__ void finish(const LogprobArgs &a, uint32_t row, const
     }
     if (a.top == 0)
         return;
-    const List best = join_lists(keys, parts, a.top, bench, lane);
     if (lane < a.top) {
         const uint32_t id = 0xFFFFFFFFu - (uint32_t)best.key;
         // a row with NaN may have fewer than `top` values that compare
@@ -201,75 +204,200 @@ __device__ __forceinline__ void finish(const LogprobArgs &a, uint32_t row, const
     }
 }
 
-// WITH_TOP: the list is kept at all; WITH_T: the entropy's sum is.
-template <bool F32, bool WITH_TOP, bool WITH_T>
-__global__ __launch_bounds__(WG) void k_logprobs(LogprobArgs a, uint32_t parts)
+// 16 bytes of logits as values; the elements at and behind `end` and before
+// `begin` (they are not read) as -inf.
+template <bool F32>
+__device__ __forceinline__ u32x4 load16(const void *logits, uint32_t at, uint32_t begin, uint32_t end)
 {
-    constexpr int V = F32 ? 4 : 8;         // elements of 16 bytes
-    constexpr uint32_t PIECE = 64 * NV * V;
+    constexpr uint32_t V = F32 ? 4 : 8;
+    if (at >= begin && at + V <= end)
+        return *(const u32x4 *)((const uint8_t *)logits + (size_t)at * (F32 ? 4 : 2));
+    u32x4 raw;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (F32) {
+            raw[j] = at + j >= begin && at + j < end ? ((const uint32_t *)logits)[at + j] : 0xFF800000u;
+        } else {
+            const uint32_t g = at + 2 * j;
+            const uint32_t lo = g >= begin && g < end ? ((const uint16_t *)logits)[g] : 0xFF80u;
+            const uint32_t hi = g + 1 >= begin && g + 1 < end ? ((const uint16_t *)logits)[g + 1] : 0xFF80u;
+            raw[j] = hi << 16 | lo;
+        }
+    }
+    return raw;
+}
+template <bool F32>
+__device__ __forceinline__ void values(u32x4 raw, float *x)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (F32) {
+            x[j] = __uint_as_float(raw[j]);
+        } else {
+            x[2 * j] = bf16_lo(raw[j]);
+            x[2 * j + 1] = bf16_hi(raw[j]);
+        }
+    }
+}
+
+// What a workgroup has of a row: pieces of 64 x NV x 16 bytes, wave w's at
+// first + PIECE * w and every `stride` from there.
+template <bool F32>
+struct Part {
+    static constexpr uint32_t V = F32 ? 4 : 8;          // elements of 16 bytes
+    static constexpr uint32_t PIECE = 64 * NV * V;
+    uint32_t begin, end;                                // the row, below 2^31
+    uint32_t first, stride;
+};
+
+// The whole workgroup: the `top` largest elements of its part, in order, to
+// bench.out (0 behind them, where there are fewer).  m: the lane's maximum.
+template <bool F32>
+__device__ __forceinline__ void largest(const LogprobArgs &a, const Part<F32> &p, float m, float *lane_max, uint64_t *keys,
+                                        Bench &bench, uint32_t lane, uint32_t wave)
+{
+    constexpr uint32_t V = Part<F32>::V, PIECE = Part<F32>::PIECE;
+    const uint32_t tid = threadIdx.x;
+    lane_max[tid] = m;
+    if (tid < 64)
+        bench.out[tid] = 0;
+    if (tid == 0)
+        bench.n = 0;
+    __syncthreads();
+    // the largest value with 16 zeros behind it that `top` lanes' maxima reach
+    uint32_t u[WAVES], bound = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < WAVES; ++w)
+        u[w] = ordered(lane_max[64 * w + lane]);
+#pragma unroll 1
+    for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1) {
+        uint32_t n = 0;
+#pragma unroll
+        for (uint32_t w = 0; w < WAVES; ++w)
+            n += __popcll(__ballot(u[w] >= (bound | bit)));
+        if (n >= a.top)
+            bound |= bit;
+    }
+    // below -inf lie the keys that are no numbers.  With -inf the elements that are
+    // more are looked for, and then the first tokens that are not
+    const bool rest = bound <= ordered(-INFINITY);
+    const uint32_t reach = rest ? ordered(-INFINITY) + 1 : bound;
+    uint32_t lanes = 0, before = 0;        // lanes that reach it; those before this wave's
+    uint64_t who = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < WAVES; ++w) {
+        const uint64_t mask = __ballot(u[w] >= reach);
+        before += w < wave ? __popcll(mask) : 0;
+        lanes += __popcll(mask);
+        who = w == wave ? mask : who;
+    }
+    __syncthreads();                       // lane_max has been read; now it lists those lanes
+    if (who >> lane & 1)
+        ((uint32_t *)lane_max)[before + __popcll(who & ((1ull << lane) - 1))] = tid;
+    __syncthreads();
+    const uint32_t pieces = (p.end - p.first + p.stride - 1) / p.stride;    // of the first wave; p.first < p.end
+    for (uint32_t i = tid; i < lanes * pieces * NV; i += WG) {
+        const uint32_t t = ((const uint32_t *)lane_max)[i % lanes], v = i / lanes % NV, nth = i / lanes / NV;
+        const uint32_t at = p.first + PIECE * (t / 64) + nth * p.stride + (64 * v + t % 64) * V;
+        if (at >= p.end)
+            continue;
+        float x[V];
+        values<F32>(load16<F32>(a.logits, at, p.begin, p.end), x);
+#pragma unroll
+        for (uint32_t j = 0; j < V; ++j)
+            if (ordered(x[j]) >= reach && x[j] == x[j])
+                collect(bench, (uint64_t)ordered(x[j]) << 32 | (0xFFFFFFFFu - (at + j - p.begin)));
+    }
+    __syncthreads();
+    uint32_t n = bench.n;
+    bool all = n <= ROOM;
+    if (rest && all) {
+        // of the part's first top + n tokens, `top` are -inf
+        const uint32_t from = max(p.first, p.begin);
+        all = a.top + n <= PIECE - V;
+        __syncthreads();
+        for (uint32_t i = from + tid; all && i < min(from + a.top + n, p.end); i += WG) {
+            const float x = F32 ? ((const float *)a.logits)[i]
+                                : __uint_as_float((uint32_t)((const uint16_t *)a.logits)[i] << 16);
+            if (x == -INFINITY)
+                collect(bench, (uint64_t)ordered(x) << 32 | (0xFFFFFFFFu - (i - p.begin)));
+        }
+        __syncthreads();
+        n = bench.n;
+        all = all && n <= ROOM;
+    }
+    if (all) {
+        in_order(bench, n, a.top, tid, WG);
+        __syncthreads();
+        return;
+    }
+    // one after the other, a list a wave
+    List best = {0};
+    uint64_t least = 0;
+#pragma unroll 1
+    for (uint32_t at = p.first + PIECE * wave; at < p.end; at += p.stride)
+#pragma unroll 1
+        for (int v = 0; v < NV; ++v) {
+            const uint32_t f = at + (64 * v + lane) * V;
+            float x[V];
+            values<F32>(load16<F32>(a.logits, f, p.begin, p.end), x);
+#pragma unroll
+            for (uint32_t j = 0; j < V; ++j) {
+                const bool in = f + j >= p.begin && f + j < p.end && x[j] == x[j];
+                merge(best, least, in ? (uint64_t)ordered(x[j]) << 32 | (0xFFFFFFFFu - (f + j - p.begin)) : 0, a.top, lane);
+            }
+        }
+    if (lane < a.top)
+        keys[wave * a.top + lane] = best.key;
+    __syncthreads();
+    if (wave == 0) {
+        best = join_lists(keys, WAVES, a.top, bench, lane);
+        bench.out[lane] = lane < a.top ? best.key : 0;
+    }
+    __syncthreads();
+}
+
+// The first `whole` rows are a workgroup's each, the others `split` workgroups'.
+// WITH_T: the entropy's sum is kept.
+template <bool F32, bool WITH_T>
+__global__ __launch_bounds__(WG, RESIDENT) void k_logprobs(LogprobArgs a, uint32_t whole, uint32_t split)
+{
+    constexpr uint32_t V = Part<F32>::V, PIECE = Part<F32>::PIECE;
     __shared__ Sums sums[WAVES];
+    __shared__ float lane_max[WG];
     __shared__ uint64_t keys[WAVES * 32];
-    __shared__ Bench bench[WITH_TOP ? WAVES : 1];
-    const uint32_t row = blockIdx.x / parts, part = blockIdx.x % parts;
+    __shared__ Bench bench;
+    const bool alone = blockIdx.x < whole;
+    const uint32_t parts = alone ? 1 : split, nth = blockIdx.x - whole;
+    const uint32_t row = alone ? blockIdx.x : whole + nth / split, part = alone ? 0 : nth % split;
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const uint32_t begin = row * a.vocab, end = begin + a.vocab;    // below 2^31
-    const uint32_t stride = PIECE * WAVES * parts;
-    uint32_t pos = begin / V * V + PIECE * (part * WAVES + wave);
+    Part<F32> p;
+    p.begin = row * a.vocab;
+    p.end = p.begin + a.vocab;
+    p.first = p.begin / V * V + PIECE * WAVES * part;
+    p.stride = PIECE * WAVES * parts;
 
     u32x4 raw[NV];
-    auto load = [&](uint32_t p) {
+    auto load = [&](uint32_t at) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const uint32_t f = p + (64 * v + lane) * V;
-            if (f >= begin && f + V <= end) {
-                raw[v] = *(const u32x4 *)((const uint8_t *)a.logits + (size_t)f * (F32 ? 4 : 2));
-                continue;
-            }
-            // the row's ragged ends: only what belongs to it is read
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (F32) {
-                    raw[v][j] = f + j >= begin && f + j < end ? ((const uint32_t *)a.logits)[f + j] : 0xFF800000u;
-                } else {
-                    const uint32_t g = f + 2 * j;
-                    const uint32_t lo = g >= begin && g < end ? ((const uint16_t *)a.logits)[g] : 0xFF80u;
-                    const uint32_t hi = g + 1 >= begin && g + 1 < end ? ((const uint16_t *)a.logits)[g + 1] : 0xFF80u;
-                    raw[v][j] = hi << 16 | lo;
-                }
-            }
-        }
+        for (int v = 0; v < NV; ++v)
+            raw[v] = load16<F32>(a.logits, at + (64 * v + lane) * V, p.begin, p.end);
     };
-
     float m = -INFINITY, s = 0.0f, t = 0.0f;
-    List best = {0};
-    uint64_t least = 0;                    // what an element has to pass to enter the list
-    float least_x = -INFINITY;             // its value
-    bool first = true;
-    if (pos < end)
+    uint32_t pos = p.first + PIECE * wave;
+    if (pos < p.end)
         load(pos);
-    for (; pos < end; pos += stride) {
-        float x[NV][V], most[NV], top = -INFINITY;
+    for (; pos < p.end; pos += p.stride) {
+        float x[NV][V], top = -INFINITY;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
+            values<F32>(raw[v], x[v]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (F32) {
-                    x[v][j] = __uint_as_float(raw[v][j]);
-                } else {
-                    x[v][2 * j % V] = bf16_lo(raw[v][j]);
-                    x[v][(2 * j + 1) % V] = bf16_hi(raw[v][j]);
-                }
-            }
-            most[v] = x[v][0];
-#pragma unroll
-            for (int j = 1; j < V; ++j)
-                most[v] = __builtin_fmaxf(most[v], x[v][j]);
-            top = __builtin_fmaxf(top, most[v]);
+            for (uint32_t j = 0; j < V; ++j)
+                top = __builtin_fmaxf(top, x[v][j]);
         }
-        if (pos + stride < end)
-            load(pos + stride);
-
-        // ---- sums
+        if (pos + p.stride < p.end)
+            load(pos + p.stride);
         const float to = __builtin_fmaxf(m, top);
         fade_to(to, m, s, t);
         m = to;
@@ -280,7 +408,7 @@ __global__ __launch_bounds__(WG) void k_logprobs(LogprobArgs a, uint32_t parts)
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
+                for (uint32_t j = 0; j < V; ++j) {
                     const float y = WITH_T ? __builtin_fmaxf(__builtin_fmaf(x[v][j], LOG2E, by), -200.0f)
                                            : __builtin_fmaf(x[v][j], LOG2E, by);
                     const float e = __builtin_amdgcn_exp2f(y);
@@ -293,112 +421,48 @@ __global__ __launch_bounds__(WG) void k_logprobs(LogprobArgs a, uint32_t parts)
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
+                for (uint32_t j = 0; j < V; ++j) {
                     const float y = __builtin_fmaxf((x[v][j] - by) * LOG2E, -200.0f);
                     const float e = __builtin_amdgcn_exp2f(y);
                     s += e;
                     t = __builtin_fmaf(e, y, t);
                 }
         }
-
-        // ---- the largest
-        if (!WITH_TOP)
-            continue;
-        if (first) {
-            first = false;
-            // the largest value with 16 zeros behind it that `top` lanes' maxima reach
-            const uint32_t u = ordered(top);
-            uint32_t bound = 0;
-#pragma unroll
-            for (int b = 31; b >= 16; --b)
-                if ((uint32_t)__popcll(__ballot(u >= (bound | 1u << b))) >= a.top)
-                    bound |= 1u << b;
-            // below -inf lie the keys that are no numbers
-            const float bound_x = bound > ordered(-INFINITY) ? from_ordered(bound) : -INFINITY;
-            uint32_t n = 0;
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                if (!__any(most[v] >= bound_x))
-                    continue;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const uint32_t id = pos + (64 * v + lane) * V + j - begin;
-                    n = collect(bench[wave], n, x[v][j] >= bound_x && id < a.vocab,
-                                (uint64_t)ordered(x[v][j]) << 32 | (0xFFFFFFFFu - id));
-                }
-            }
-            if (n <= ROOM) {
-                best = in_order(bench[wave], n, lane);
-                least = best.at(a.top - 1);
-                least_x = least ? from_ordered((uint32_t)(least >> 32)) : -INFINITY;
-                if (least)
-                    continue;
-                best.key = 0;              // fewer than `top`: all over, one after the other
-            }
-        }
-        bool touched = least == 0;         // the list has elements of this piece, which may lie behind its others
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            if (!__any(most[v] > least_x || (touched && most[v] == least_x)))
-                continue;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const uint32_t id = pos + (64 * v + lane) * V + j - begin;
-                for (uint64_t who = __ballot((x[v][j] > least_x || (touched && x[v][j] == least_x)) && id < a.vocab); who;
-                     who &= who - 1) {
-                    const uint32_t l = __builtin_ctzll(who);
-                    const float c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x[v][j]), l));
-                    const uint64_t k = (uint64_t)ordered(c) << 32 |
-                                       (0xFFFFFFFFu - (uint32_t)__builtin_amdgcn_readlane(id, l));
-                    if (k > least) {
-                        best.insert(k, lane);
-                        touched = true;
-                        const uint64_t last = best.at(a.top - 1);
-                        if (last > least) {
-                            least = last;
-                            least_x = from_ordered((uint32_t)(last >> 32));
-                        }
-                    }
-                }
-            }
-        }
     }
 
-    const float all = wave_max(m);
-    fade_to(all, m, s, t);
+    const float most = wave_max(m);
+    if (a.top != 0)
+        largest<F32>(a, p, m, lane_max, keys, bench, lane, wave);
+    fade_to(most, m, s, t);
     s = sum_over_wave(s);
     t = sum_over_wave(t);
     if (lane == 0)
-        sums[wave] = {all, s, t, 0.0f};
-    if (WITH_TOP && lane < a.top)
-        keys[wave * a.top + lane] = best.key;
+        sums[wave] = {most, s, t, 0.0f};
     __syncthreads();
     if (wave != 0)
         return;
+    const List best = {a.top != 0 ? bench.out[lane] : 0};
     if (parts == 1) {
-        finish<F32>(a, row, sums, keys, WAVES, bench[0], lane);
+        finish<F32>(a, row, sums, WAVES, best, lane);
         return;
     }
     // the workgroup's sums and list, for the join
-    float top = all;
+    float top = most;
     for (uint32_t u = 1; u < WAVES; ++u)
         top = __builtin_fmaxf(top, sums[u].m);
-    fade_to(top, all, s, t);
+    fade_to(top, most, s, t);
     for (uint32_t u = 1; u < WAVES; ++u) {
-        Sums p = sums[u];
-        fade_to(top, p.m, p.s, p.t);
-        s += p.s;
-        t += p.t;
+        Sums q = sums[u];
+        fade_to(top, q.m, q.s, q.t);
+        s += q.s;
+        t += q.t;
     }
     Sums *to_sums = (Sums *)a.work;
-    uint64_t *to_keys = (uint64_t *)(to_sums + (size_t)a.rows * parts);
+    uint64_t *to_keys = (uint64_t *)(to_sums + (size_t)(gridDim.x - whole));
     if (lane == 0)
-        to_sums[blockIdx.x] = {top, s, t, 0.0f};
-    if (WITH_TOP) {
-        best = join_lists(keys, WAVES, a.top, bench[0], lane);
-        if (lane < a.top)
-            to_keys[(size_t)blockIdx.x * a.top + lane] = best.key;
-    }
+        to_sums[nth] = {top, s, t, 0.0f};
+    if (lane < a.top)
+        to_keys[(size_t)nth * a.top + lane] = best.key;
 }
 
 template <bool F32>
@@ -406,40 +470,40 @@ __global__ __launch_bounds__(64) void k_logprobs_join(LogprobArgs a, uint32_t pa
 {
     __shared__ Bench bench;
     const Sums *sums = (const Sums *)a.work;
-    const uint64_t *keys = (const uint64_t *)(sums + (size_t)a.rows * parts);
+    const uint64_t *keys = (const uint64_t *)(sums + (size_t)gridDim.x * parts);
     const size_t first = (size_t)blockIdx.x * parts;
-    finish<F32>(a, blockIdx.x, sums + first, keys + first * a.top, parts, bench, threadIdx.x);
+    List best = {0};
+    if (a.top != 0)
+        best = join_lists(keys + first * a.top, parts, a.top, bench, threadIdx.x);
+    finish<F32>(a, a.rows - gridDim.x + blockIdx.x, sums + first, parts, best, threadIdx.x);
 }
 
-// Workgroups of a row: as few as keep the chip's last round of workgroups from
-// being a poor one (its rounds rounded up are then at most 1/8 more than they
-// are), each wave having a piece of its own.
-uint32_t parts_of(uint32_t rows, uint32_t vocab, bool f32)
+// How rows are dealt: a workgroup each, as long as they fill the chip; the rows of
+// a last round that would leave much of it empty are split, at most until each wave
+// has one piece.
+struct Deal {
+    uint32_t whole, split;                 // rows that are not split; parts of the others
+    uint64_t parts(uint32_t rows) const { return (uint64_t)(rows - whole) * split; }
+};
+Deal deal(uint32_t rows, uint32_t vocab, bool f32)
 {
-    const uint64_t cus = cu_count() ? cu_count() : 256, piece = 64 * NV * (f32 ? 4 : 8) * WAVES;
-    const uint64_t most = (vocab + piece - 1) / piece, room = 7 * cus;
-    uint64_t parts = 1;
-    while (parts < most && 8 * room * ((rows * parts + room - 1) / room) > 9 * rows * parts)
-        ++parts;
-    return (uint32_t)parts;
+    const uint32_t room = RESIDENT * (cu_count() ? cu_count() : 256), piece = 64 * NV * (f32 ? 4 : 8) * WAVES;
+    const uint32_t last = rows % room, split = last ? min((vocab + piece - 1) / piece, room / last) : 1;
+    return split > 1 ? Deal{rows - last, split} : Deal{rows, 1};
 }
 
 template <bool F32>
 void launch(const LogprobArgs &a, hipStream_t st)
 {
-    const uint32_t parts = parts_of(a.rows, a.vocab, F32);
-    const dim3 grid(a.rows * parts);
-    if (a.top != 0 && a.entropy)
-        k_logprobs<F32, true, true><<<grid, WG, 0, st>>>(a, parts);
-    else if (a.top != 0)
-        k_logprobs<F32, true, false><<<grid, WG, 0, st>>>(a, parts);
-    else if (a.entropy)
-        k_logprobs<F32, false, true><<<grid, WG, 0, st>>>(a, parts);
+    const Deal d = deal(a.rows, a.vocab, F32);
+    const dim3 grid(d.whole + (uint32_t)d.parts(a.rows));
+    if (a.entropy)
+        k_logprobs<F32, true><<<grid, WG, 0, st>>>(a, d.whole, d.split);
     else
-        k_logprobs<F32, false, false><<<grid, WG, 0, st>>>(a, parts);
+        k_logprobs<F32, false><<<grid, WG, 0, st>>>(a, d.whole, d.split);
     count_launch();
-    if (parts > 1) {
-        k_logprobs_join<F32><<<a.rows, 64, 0, st>>>(a, parts);
+    if (d.whole < a.rows) {
+        k_logprobs_join<F32><<<a.rows - d.whole, 64, 0, st>>>(a, d.split);
         count_launch();
     }
 }
@@ -448,8 +512,8 @@ void launch(const LogprobArgs &a, hipStream_t st)
 
 uint64_t token_logprobs_work(uint32_t rows, uint32_t vocab, uint32_t top)
 {
-    const uint64_t parts = max(parts_of(rows, vocab, false), parts_of(rows, vocab, true));
-    return parts > 1 ? (uint64_t)rows * parts * (sizeof(Sums) + 8 * top) : 16;
+    const uint64_t parts = max(deal(rows, vocab, false).parts(rows), deal(rows, vocab, true).parts(rows));
+    return max(parts * (sizeof(Sums) + 8 * top), (uint64_t)16);
 }
 
 hipError_t launch_token_logprobs(const LogprobArgs &a, hipStream_t st)
