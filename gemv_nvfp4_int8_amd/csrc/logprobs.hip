@@ -73,8 +73,9 @@ __device__ __forceinline__ void merge(List &best, uint64_t &least, uint64_t k, u
 
 // Room in LDS for keys that reach a bound, and for the largest in order.
 constexpr uint32_t ROOM = 512;
+constexpr uint32_t BATCH = 16;
 struct Bench {
-    uint64_t in[ROOM], out[64];
+    uint64_t in[ROOM + BATCH], out[64];
     uint32_t n;                            // keys that reached it: more than ROOM are not all there
 };
 
@@ -86,15 +87,27 @@ __device__ __forceinline__ void collect(Bench &bench, uint64_t key)
 }
 
 // The `top` largest of the n <= ROOM collected keys to bench.out, by `threads`
-// threads: each key counts the larger ones.
+// threads (at least BATCH): each key counts the larger ones, BATCH at a time.
 __device__ __forceinline__ void in_order(Bench &bench, uint32_t n, uint32_t top, uint32_t thread, uint32_t threads)
 {
+    if (thread < BATCH)
+        bench.in[n + thread] = 0;          // no key
+    if (threads == 64)
+        __builtin_amdgcn_wave_barrier();
+    else
+        __syncthreads();
     for (uint32_t i0 = thread; i0 < n; i0 += threads) {
         const uint64_t mine = bench.in[i0];
         uint32_t place = 0;
-#pragma unroll 4
-        for (uint32_t i = 0; i < n; ++i)
-            place += bench.in[i] > mine;
+        for (uint32_t i = 0; i < n; i += BATCH) {
+            uint64_t k[BATCH];
+#pragma unroll
+            for (uint32_t j = 0; j < BATCH; ++j)
+                k[j] = bench.in[i + j];
+#pragma unroll
+            for (uint32_t j = 0; j < BATCH; ++j)
+                place += k[j] > mine;
+        }
         if (place < top)
             bench.out[place] = mine;
     }
@@ -118,28 +131,32 @@ __device__ __forceinline__ float sum_over_wave(float v)
     return v;
 }
 
-// One wave: the list of `parts` lists of `top` keys each, in order.  Each list has
-// h = ceil(top / parts) keys not below its h-th, so together they have `top` not
-// below the lowest of these: that is the bound.
+// One wave: the list of `parts` lists of `top` keys each, in order.  With
+// h = ceil(top / lists), a value that the h-th keys of ceil(top / h) lists reach is
+// reached by `top` keys: the largest such is the bound.
 __device__ __forceinline__ List join_lists(const uint64_t *keys, uint32_t parts, uint32_t top, Bench &bench, uint32_t lane)
 {
-    const uint32_t h = (top + parts - 1) / parts;
-    uint64_t bound = ~0ull;
-    for (uint32_t p = lane; p < parts; p += 64)
-        bound = min(bound, keys[p * top + h - 1]);
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-        bound = min(bound, (uint64_t)__shfl_xor(bound, off, WAVE));
-    bench.n = 0;
-    if (lane < 64)
-        bench.out[lane] = 0;
-    __builtin_amdgcn_wave_barrier();
+    const uint32_t lists = min(parts, 64u), h = (top + lists - 1) / lists, need = (top + h - 1) / h, total = parts * top;
     constexpr int U = 8;                   // loads on their way together
-    for (uint32_t i0 = 0; i0 < parts * top; i0 += 64 * U) {
-        uint64_t k[U];
+    uint64_t k[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            k[u] = i0 + 64 * u + lane < parts * top ? keys[i0 + 64 * u + lane] : 0;
+    for (int u = 0; u < U; ++u)
+        k[u] = 64 * u + lane < total ? keys[64 * u + lane] : 0;
+    const uint32_t value = lane < lists ? (uint32_t)(keys[lane * top + h - 1] >> 32) : 0;
+    bench.n = 0;
+    bench.out[lane] = 0;
+    uint32_t bits = 0;
+    for (uint32_t bit = 1u << 31; bit; bit >>= 1)
+        if ((uint32_t)__popcll(__ballot(value >= (bits | bit))) >= need)
+            bits |= bit;
+    const uint64_t bound = (uint64_t)bits << 32;
+    __builtin_amdgcn_wave_barrier();
+    for (uint32_t i0 = 0; i0 < total; i0 += 64 * U) {
+        if (i0 != 0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                k[u] = i0 + 64 * u + lane < total ? keys[i0 + 64 * u + lane] : 0;
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (k[u] != 0 && k[u] >= bound)
@@ -160,17 +177,29 @@ __device__ __forceinline__ List join_lists(const uint64_t *keys, uint32_t parts,
     return best;
 }
 
+// A row's target: whether it is a token, and its logit.
+struct Target {
+    bool there;
+    float x;
+};
+template <bool F32>
+__device__ __forceinline__ Target target_of(const LogprobArgs &a, uint32_t row)
+{
+    Target r = {false, 0.0f};
+    if (a.targets) {
+        const uint32_t id = (uint32_t)a.targets[row];
+        r.there = id < a.vocab;
+        const size_t e = (size_t)row * a.vocab + (r.there ? id : 0);
+        r.x = F32 ? ((const float *)a.logits)[e] : __uint_as_float((uint32_t)((const uint16_t *)a.logits)[e] << 16);
+    }
+    return r;
+}
+
 // One wave: joins `parts` sums and writes the row's outputs.
 template <bool F32>
 __device__ __forceinline__ void finish(const LogprobArgs &a, uint32_t row, const Sums *sums, uint32_t parts, List best,
-                                       uint32_t lane)
+                                       Target given, uint32_t lane)
 {
-    const uint32_t target = a.targets ? (uint32_t)a.targets[row] : 0;
-    float x = 0.0f;
-    if (a.targets && target < a.vocab) {
-        const size_t e = (size_t)row * a.vocab + target;
-        x = F32 ? ((const float *)a.logits)[e] : __uint_as_float((uint32_t)((const uint16_t *)a.logits)[e] << 16);
-    }
     float m = -INFINITY, s = 0.0f, t = 0.0f;
     for (uint32_t i = lane; i < parts; i += 64) {
         Sums p = sums[i];
@@ -189,7 +218,7 @@ __device__ __forceinline__ void finish(const LogprobArgs &a, uint32_t row, const
     const float norm = s == 0.0f ? 0.0f : logf(s);
     if (lane == 0) {
         if (a.targets)
-            a.logprob[row] = target < a.vocab ? x - base - norm : 0.0f;
+            a.logprob[row] = given.there ? given.x - base - norm : 0.0f;
         if (a.entropy)
             a.entropy[row] = s == 0.0f ? 0.0f : norm - LN2 * (t / s);
     }
@@ -383,6 +412,9 @@ __global__ __launch_bounds__(WG, RESIDENT) void k_logprobs(LogprobArgs a, uint32
         for (int v = 0; v < NV; ++v)
             raw[v] = load16<F32>(a.logits, at + (64 * v + lane) * V, p.begin, p.end);
     };
+    Target given = {false, 0.0f};
+    if (parts == 1 && wave == 0)
+        given = target_of<F32>(a, row);
     float m = -INFINITY, s = 0.0f, t = 0.0f;
     uint32_t pos = p.first + PIECE * wave;
     if (pos < p.end)
@@ -443,7 +475,7 @@ __global__ __launch_bounds__(WG, RESIDENT) void k_logprobs(LogprobArgs a, uint32
         return;
     const List best = {a.top != 0 ? bench.out[lane] : 0};
     if (parts == 1) {
-        finish<F32>(a, row, sums, WAVES, best, lane);
+        finish<F32>(a, row, sums, WAVES, best, given, lane);
         return;
     }
     // the workgroup's sums and list, for the join
@@ -472,10 +504,12 @@ __global__ __launch_bounds__(64) void k_logprobs_join(LogprobArgs a, uint32_t pa
     const Sums *sums = (const Sums *)a.work;
     const uint64_t *keys = (const uint64_t *)(sums + (size_t)gridDim.x * parts);
     const size_t first = (size_t)blockIdx.x * parts;
+    const uint32_t row = a.rows - gridDim.x + blockIdx.x;
+    const Target given = target_of<F32>(a, row);
     List best = {0};
     if (a.top != 0)
         best = join_lists(keys + first * a.top, parts, a.top, bench, threadIdx.x);
-    finish<F32>(a, a.rows - gridDim.x + blockIdx.x, sums + first, parts, best, threadIdx.x);
+    finish<F32>(a, row, sums + first, parts, best, given, threadIdx.x);
 }
 
 // How rows are dealt: a workgroup each, as long as they fill the chip; the rows of
