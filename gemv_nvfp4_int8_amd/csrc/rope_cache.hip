@@ -3,12 +3,13 @@
 //
 // A head is taken by G lanes (8, 16 or 32: the next power of two of d/8), 16
 // bytes each, so that its sum of squares and its largest magnitude are a few
-// cross-lane steps and no value is read twice from memory.  A lane's partners
-// of the half layout lie rot/2 further on or back, in another lane's 16 bytes:
-// they are loaded once more (from L1) rather than passed between lanes, because
-// rot/2 need not be a multiple of 8.  Cosines and sines are the same for all
-// heads of a token: one thread a pair computes them into LDS while the heads'
-// loads are on their way.
+// cross-lane steps.  A lane's partners of the half layout lie rot/2 further on or
+// back, in another lane's 16 bytes, and are loaded once more (from L1).  Cosines
+// and sines are the same for all heads of a token: one thread a pair computes them
+// into LDS while the heads' loads are on their way; what is not turned has the
+// angle 0 there, so that all lanes do the same.
+#include <type_traits>
+
 #include "qp_device.hpp"
 #include "qp_launch.hpp"
 #include "decoder.hpp"
@@ -18,22 +19,26 @@ namespace {
 
 constexpr uint32_t WG = 256;
 constexpr uint32_t MAX_TOKENS = 8;         // of a workgroup
+constexpr uint32_t MAX_HALF = 128;
 
-template <int G>
-__device__ __forceinline__ float group_sum(float v)
-{
-#pragma unroll
-    for (int off = G / 2; off >= 1; off >>= 1)
-        v += __shfl_xor(v, off, WAVE);
-    return v;
-}
+// How pairs lie: 8 partners in one lane's 16 bytes (rot/2 a multiple of 8), in the
+// same lane, or anywhere.
+enum Layout { HALF, PAIRS, HALF_ANY };
 
-template <int G>
-__device__ __forceinline__ float group_max(float v)
+// All lanes of G: op over their values, within 16 lanes by data-parallel moves.
+template <int G, typename Op>
+__device__ __forceinline__ float over_group(float v, Op op)
 {
-#pragma unroll
-    for (int off = G / 2; off >= 1; off >>= 1)
-        v = __builtin_fmaxf(v, __shfl_xor(v, off, WAVE));
+    auto moved = [](float x, auto ctrl) {
+        return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, false));
+    };
+    v = op(v, moved(v, std::integral_constant<int, 0xB1>()));           // lane ^ 1
+    v = op(v, moved(v, std::integral_constant<int, 0x4E>()));           // lane ^ 2
+    v = op(v, moved(v, std::integral_constant<int, 0x141>()));          // 7 - lane, of 8
+    if (G >= 16)
+        v = op(v, moved(v, std::integral_constant<int, 0x140>()));      // 15 - lane, of 16
+    if (G >= 32)
+        v = op(v, __shfl_xor(v, 16, WAVE));
     return v;
 }
 
@@ -51,120 +56,156 @@ __device__ __forceinline__ u32x4 pack(const float *x)
     return (u32x4){pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3]), pk_bf16(x[4], x[5]), pk_bf16(x[6], x[7])};
 }
 
-// One head's 16 bytes of one lane, and what the rotation needs beside them.
-struct Piece {
-    u32x4 own, partner;
-};
-
-// tokens * heads items are dealt to the workgroup's groups of G lanes, U at a
-// time so that a lane has that many loads in flight.
-template <bool FP8, int G, int U>
+// A workgroup has one token, whose heads its groups of G lanes take in turn, U at a
+// time so that a lane has their loads in flight together; or (fewer heads than
+// groups) `tokens` of them, a head a group.
+template <bool FP8, int G, Layout L>
 __global__ __launch_bounds__(WG) void k_qk_norm_rope(RopeArgs a, uint32_t tokens, uint32_t heads)
 {
-    __shared__ f32x2 turn[MAX_TOKENS * 128];
+    constexpr uint32_t NG = WG / G;
+    constexpr int U = 3;
+    // a token's cosines and sines, then eight times those of the angle 0
+    __shared__ __attribute__((aligned(16))) f32x2 turn[MAX_TOKENS][MAX_HALF + 8];
     const uint32_t d = a.cache.d, kv = a.cache.heads, half = a.rot / 2;
     const uint32_t t0 = blockIdx.x * tokens, nt = min(tokens, a.t - t0);
-    const uint32_t items = nt * heads, group = threadIdx.x / G, c0 = 8 * (threadIdx.x % G);
+    const uint32_t group = threadIdx.x / G, c0 = 8 * (threadIdx.x % G);
     const bool live = c0 < d;
-    const bool chunked = half % 8 == 0 && !a.interleaved;
-    constexpr uint32_t NG = WG / G;
+    const uint32_t nth = tokens == 1 ? 0 : group / heads, tok = t0 + nth;
+    const uint32_t h0 = tokens == 1 ? group : group - nth * heads;
+    // where the lane's angles are, and its partners
+    const bool turned = live && c0 < a.rot;
+    const uint32_t angle = L == PAIRS ? c0 / 2 : !turned ? MAX_HALF : c0 < half ? c0 : c0 - half;
+    const uint32_t other = c0 < half ? c0 + half : c0 - half;
 
-    Piece p[U];
-    auto load = [&](uint32_t first) {
+    u32x4 own[U], partner[U];
+    auto load = [&](uint32_t h) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const uint32_t i = first + u * NG;
-            p[u].own = p[u].partner = (u32x4){0, 0, 0, 0};
-            if (i >= items || !live)
+            own[u] = partner[u] = (u32x4){0, 0, 0, 0};
+            const uint32_t head = h + u * NG;
+            if (head >= heads || nth >= nt || !live)
                 continue;
-            const uint16_t *x = a.qkv + ((size_t)t0 * heads + i) * d;
-            p[u].own = *(const u32x4 *)(x + c0);
-            if (chunked && c0 < a.rot && i % heads < heads - kv)
-                p[u].partner = *(const u32x4 *)(x + (c0 < half ? c0 + half : c0 - half));
+            const uint16_t *x = a.qkv + ((size_t)tok * heads + head) * d;
+            own[u] = *(const u32x4 *)(x + c0);
+            if (L == HALF && turned && head < heads - kv)
+                partner[u] = *(const u32x4 *)(x + other);
         }
     };
-    load(group);
-    for (uint32_t i = threadIdx.x; i < nt * half; i += WG) {
-        // the angle in turns, in 64 bits: the whole turns of far positions drop
-        // out before anything is rounded to 32
-        const double turns = (double)a.pos[t0 + i / half] * (double)a.inv_freq[i % half] * 0.15915494309189533577;
-        float s, c;
-        sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-        turn[i] = (f32x2){c * a.rope_scale, s * a.rope_scale};
+    load(h0);
+    for (uint32_t i = threadIdx.x; i < nt * (MAX_HALF + 8); i += WG) {
+        const uint32_t n = i / (MAX_HALF + 8), j = i % (MAX_HALF + 8);
+        f32x2 cs = {1.0f, 0.0f};
+        if (j < half) {
+            // the angle in turns, in 64 bits: the whole turns of far positions drop
+            // out before anything is rounded to 32
+            const double turns = (double)a.pos[t0 + n] * (double)a.inv_freq[j] * 0.15915494309189533577;
+            float s, c;
+            sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+            cs = (f32x2){c * a.rope_scale, s * a.rope_scale};
+        }
+        turn[n][j] = cs;
     }
+    int32_t slot = -1;
+    if (nth < nt)
+        slot = a.slots[tok];
     __syncthreads();
+    if (nth >= nt)
+        return;
 
-    for (uint32_t first = group; first < items; first += U * NG) {
-        if (first != group)
-            load(first);
+    float c[8], s[8];                      // of the lane's eight entries (PAIRS: of its four pairs)
+    if (L != HALF_ANY) {
+#pragma unroll
+        for (int j = 0; j < (L == PAIRS ? 4 : 8); j += 2) {
+            const f32x4 v = *(const f32x4 *)&turn[nth][angle + j];
+            c[j] = v[0];
+            s[j] = v[1];
+            c[j + 1] = v[2];
+            s[j + 1] = v[3];
+        }
+        if (L == HALF && c0 < half) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s[j] = -s[j];
+        }
+    }
+    const bool kept = (uint32_t)slot < a.cache.pages << a.cache.page_log2;       // a slot below 0 wraps far past it
+    const float of_d = 1.0f / (float)d;
+    for (uint32_t h = h0; h < heads; h += U * NG) {
+        if (h != h0)
+            load(h);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const uint32_t i = first + u * NG;
-            if (i >= items)
+            const uint32_t head = h + u * NG;
+            if (head >= heads)
                 break;                                  // whole groups leave together
-            const uint32_t tok = i / heads, h = i - tok * heads;
+            const bool value = head >= heads - kv;
             float x[8];
-            unpack(p[u].own, x);
-            if (h < heads - kv) {
-                const uint16_t *w = h < a.q_heads ? a.qw : a.kw;
-                float rstd = 1.0f;
+            unpack(own[u], x);
+            if (!value) {
+                const uint16_t *w = head < a.q_heads ? a.qw : a.kw;
+                float rstd = 1.0f, y[8];
                 if (w) {
                     float ss = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         ss = __builtin_fmaf(x[j], x[j], ss);
-                    rstd = __builtin_amdgcn_rsqf(group_sum<G>(ss) / (float)d + a.eps);
-                    if (live) {
-                        float g[8];
-                        unpack(*(const u32x4 *)(w + c0), g);
+                    ss = over_group<G>(ss, [](float p, float q) { return p + q; });
+                    rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, of_d, a.eps));
+                    u32x4 g = {0, 0, 0, 0};
+                    if (live)
+                        g = *(const u32x4 *)(w + c0);
+                    unpack(g, y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        x[j] = x[j] * rstd * y[j];
+                }
+                if constexpr (L == PAIRS) {
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        const float lo = x[j], hi = x[j + 1];
+                        x[j] = __builtin_fmaf(lo, c[j / 2], -(hi * s[j / 2]));
+                        x[j + 1] = __builtin_fmaf(hi, c[j / 2], lo * s[j / 2]);
+                    }
+                } else if constexpr (L == HALF) {
+                    unpack(partner[u], y);
+                    if (w) {
+                        u32x4 g = {0, 0, 0, 0};
+                        if (turned)
+                            g = *(const u32x4 *)(w + other);
+                        float z[8];
+                        unpack(g, z);
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            x[j] = x[j] * rstd * g[j];
+                            y[j] = y[j] * rstd * z[j];
                     }
-                }
-                if (live && c0 < a.rot) {
-                    const f32x2 *cs = turn + tok * half;
-                    if (a.interleaved) {
 #pragma unroll
-                        for (int j = 0; j < 8; j += 2)
-                            if (c0 + j < a.rot) {
-                                const f32x2 t = cs[(c0 + j) / 2];
-                                const float lo = x[j], hi = x[j + 1];
-                                x[j] = __builtin_fmaf(lo, t[0], -(hi * t[1]));
-                                x[j + 1] = __builtin_fmaf(hi, t[0], lo * t[1]);
-                            }
-                    } else {
-                        float y[8];
-                        unpack(p[u].partner, y);
-                        const uint16_t *raw = a.qkv + ((size_t)t0 * heads + i) * d;
+                    for (int j = 0; j < 8; ++j)
+                        x[j] = __builtin_fmaf(x[j], c[j], y[j] * s[j]);
+                } else if (turned) {
+                    const uint16_t *raw = a.qkv + ((size_t)tok * heads + head) * d;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint32_t e = c0 + j;
-                            if (e >= a.rot)
-                                continue;
-                            const uint32_t o = e < half ? e + half : e - half;
-                            if (!chunked)
-                                y[j] = __uint_as_float((uint32_t)raw[o] << 16);
-                            if (w)
-                                y[j] = y[j] * rstd * __uint_as_float((uint32_t)w[o] << 16);
-                            const f32x2 t = cs[e < half ? e : e - half];
-                            x[j] = __builtin_fmaf(x[j], t[0], (e < half ? -y[j] : y[j]) * t[1]);
-                        }
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t e = c0 + j;
+                        if (e >= a.rot)
+                            continue;
+                        const uint32_t o = e < half ? e + half : e - half;
+                        const f32x2 t = turn[nth][e < half ? e : e - half];
+                        float z = __uint_as_float((uint32_t)raw[o] << 16);
+                        if (w)
+                            z = z * rstd * __uint_as_float((uint32_t)w[o] << 16);
+                        x[j] = __builtin_fmaf(x[j], t[0], (e < half ? -z : z) * t[1]);
                     }
                 }
             }
-            if (h < a.q_heads) {
+            if (head < a.q_heads) {
                 if (live)
-                    *(u32x4 *)(a.q_out + ((size_t)(t0 + tok) * a.q_heads + h) * d + c0) = pack(x);
+                    *(u32x4 *)(a.q_out + ((size_t)tok * a.q_heads + head) * d + c0) = pack(x);
                 continue;
             }
-            const int32_t slot = a.slots[t0 + tok];
-            const bool kept = (uint32_t)slot < a.cache.pages << a.cache.page_log2;   // a slot below 0 wraps far past it
-            const bool key = h < heads - kv;
-            const uint32_t head = h - a.q_heads - (key ? 0 : kv);
-            const size_t at = (((size_t)(slot >> a.cache.page_log2) * kv + head) << a.cache.page_log2) +
-                              (slot & ((1 << a.cache.page_log2) - 1));
-            void *cache = key ? a.cache.k : a.cache.v;
+            const uint32_t kv_head = head - a.q_heads - (value ? kv : 0);
+            const size_t at = (((size_t)((uint32_t)slot >> a.cache.page_log2) * kv + kv_head) << a.cache.page_log2) +
+                              ((uint32_t)slot & ((1u << a.cache.page_log2) - 1));
+            void *cache = value ? a.cache.v : a.cache.k;
             if (!FP8) {
                 if (live && kept)
                     *(u32x4 *)((uint16_t *)cache + at * d + c0) = pack(x);
@@ -174,7 +215,7 @@ __global__ __launch_bounds__(WG) void k_qk_norm_rope(RopeArgs a, uint32_t tokens
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 top = __builtin_fmaxf(top, __builtin_fabsf(live ? x[j] : 0.0f));
-            const float scale = div_by_const<448>(group_max<G>(top));
+            const float scale = div_by_const<448>(over_group<G>(top, [](float p, float q) { return __builtin_fmaxf(p, q); }));
             float q[8];
             div_all<8>(ScaleDiv(scale), x, q);
             u32x2 codes = {cvt_e4m3x4(q[0], q[1], q[2], q[3]), cvt_e4m3x4(q[4], q[5], q[6], q[7])};
@@ -183,23 +224,33 @@ __global__ __launch_bounds__(WG) void k_qk_norm_rope(RopeArgs a, uint32_t tokens
             if (live && kept) {
                 *(u32x2 *)((uint8_t *)cache + at * d + c0) = codes;
                 if (c0 == 0)
-                    (key ? a.cache.ks : a.cache.vs)[at] = scale;
+                    (value ? a.cache.vs : a.cache.ks)[at] = scale;
             }
         }
     }
 }
 
-template <int G>
-void launch(const RopeArgs &a, hipStream_t st)
+template <int G, Layout L>
+void launch_layout(const RopeArgs &a, hipStream_t st)
 {
     const uint32_t heads = a.q_heads + 2 * a.cache.heads;
-    // tokens of a workgroup: one, or as many as give every group of lanes an item
     const uint32_t tokens = max(1u, min(MAX_TOKENS, WG / G / heads));
     const dim3 grid((a.t + tokens - 1) / tokens);
     if (a.cache.fp8)
-        k_qk_norm_rope<true, G, 2><<<grid, WG, 0, st>>>(a, tokens, heads);
+        k_qk_norm_rope<true, G, L><<<grid, WG, 0, st>>>(a, tokens, heads);
     else
-        k_qk_norm_rope<false, G, 2><<<grid, WG, 0, st>>>(a, tokens, heads);
+        k_qk_norm_rope<false, G, L><<<grid, WG, 0, st>>>(a, tokens, heads);
+}
+
+template <int G>
+void launch(const RopeArgs &a, hipStream_t st)
+{
+    if (a.interleaved)
+        launch_layout<G, PAIRS>(a, st);
+    else if (a.rot % 16 == 0)
+        launch_layout<G, HALF>(a, st);
+    else
+        launch_layout<G, HALF_ANY>(a, st);
 }
 
 } // namespace
