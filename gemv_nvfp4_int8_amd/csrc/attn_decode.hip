@@ -57,9 +57,10 @@ __device__ __forceinline__ void load_dwords(__amdgpu_buffer_rsrc_t p, uint32_t a
 }
 
 // DP: d rounded up to 64, 128 or 256 (what lies past d is read from the head's
-// start, meets zeros of Q, and is not stored); NQ: 16s of rows.
+// start, meets zeros of Q, and is not stored); NQ: 16s of rows; blocks: of so many
+// rows a sequence and head may have.
 template <int DP, int NQ, bool FP8>
-__global__ __launch_bounds__(WG, NQ == 1 && DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs a, Parts parts, uint32_t max_shares)
+__global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs a, Parts parts, uint32_t max_shares, uint32_t blocks)
 {
     constexpr int ROWS = 16 * NQ;
     constexpr int KS = DP / 32;            // MFMAs over d
@@ -77,8 +78,10 @@ __global__ __launch_bounds__(WG, NQ == 1 && DP <= 128 ? 2 : 1) void k_attn_decod
     const uint32_t tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const uint32_t col = lane % 16, quad = lane / 16;
     const uint32_t d = a.cache.d, kv = a.cache.heads, group = a.q_heads / kv, pl = a.cache.page_log2;
+    const uint32_t units = kv * blocks;    // of a sequence
 
-    // ---- the share: tiles of all sequences in one line, a sequence's heads one after the other
+    // ---- the share: tiles of all sequences in one line, a sequence's heads one after
+    // the other, and the blocks of a head so that they find its keys in a cache
     auto wave_scan = [&](uint32_t v) {                  // inclusive
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
@@ -101,7 +104,7 @@ __global__ __launch_bounds__(WG, NQ == 1 && DP <= 128 ? 2 : 1) void k_attn_decod
         ahead += w < wave ? scan[w] : 0;
         total += scan[w];
     }
-    total = uniform(total * kv);
+    total = uniform(total * units);
     const uint64_t shares = min((uint64_t)max_shares, total);
     const uint32_t w = blockIdx.x;
     if (w >= shares) {
@@ -115,14 +118,14 @@ __global__ __launch_bounds__(WG, NQ == 1 && DP <= 128 ? 2 : 1) void k_attn_decod
     uint32_t seq = 0;
     uint64_t seq_tile = 0;
     if (a.seqs <= WG) {
-        const uint64_t to = (ahead + incl) * kv, from = to - (uint64_t)mine * kv;
+        const uint64_t to = (ahead + incl) * units, from = to - (uint64_t)mine * units;
         if (tid < a.seqs && x >= from && x < to) {
             found[0] = tid;
             found[1] = (uint32_t)(ahead + incl - mine);
         }
         __syncthreads();
         seq = found[0];
-        seq_tile = (uint64_t)found[1] * kv;
+        seq_tile = (uint64_t)found[1] * units;
     } else {
         uint64_t base = 0;
         for (uint32_t s0 = 0; s0 < a.seqs; s0 += WG) {
@@ -139,7 +142,7 @@ __global__ __launch_bounds__(WG, NQ == 1 && DP <= 128 ? 2 : 1) void k_attn_decod
                 before += v < wave ? scan[v] : 0;
                 base += scan[v];
             }
-            const uint64_t to = (before + in) * kv, from = to - (uint64_t)t * kv;
+            const uint64_t to = (before + in) * units, from = to - (uint64_t)t * units;
             if (x >= from && x < to) {
                 found[0] = s0 + tid;
                 found[1] = (uint32_t)(before + in - t);
@@ -149,7 +152,7 @@ __global__ __launch_bounds__(WG, NQ == 1 && DP <= 128 ? 2 : 1) void k_attn_decod
                 break;
         }
         seq = found[0];
-        seq_tile = (uint64_t)found[1] * kv;
+        seq_tile = (uint64_t)found[1] * units;
     }
     seq = min(uniform(seq), a.seqs - 1);
     seq_tile = uniform(seq_tile);
@@ -158,24 +161,29 @@ __global__ __launch_bounds__(WG, NQ == 1 && DP <= 128 ? 2 : 1) void k_attn_decod
     while (x < share_end) {
         const Seq q = read_seq_uniform(a, seq);
         const uint32_t tiles = tiles_of(q);
-        if (tiles == 0 || x >= seq_tile + (uint64_t)tiles * kv) {
-            seq_tile += (uint64_t)tiles * kv;
+        if (tiles == 0 || x >= seq_tile + (uint64_t)tiles * units) {
+            seq_tile += (uint64_t)tiles * units;
             if (++seq == a.seqs)
                 break;                     // not reached unless the lengths change under the call
             continue;
         }
-        const uint32_t head = uniform((uint32_t)((x - seq_tile) / tiles));
-        const uint64_t unit = seq_tile + (uint64_t)head * tiles;
+        const uint32_t nth = uniform((uint32_t)((x - seq_tile) / tiles)), head = nth / blocks;
+        const uint64_t unit = seq_tile + (uint64_t)nth * tiles;
         const uint32_t off = (uint32_t)(x - unit);
         const uint32_t count = (uint32_t)min((uint64_t)(tiles - off), share_end - x);
-        const int rows = q.n * (int)group;
+        const uint32_t row0 = (nth - head * blocks) * ROWS;
+        if (row0 >= (uint32_t)q.n * group) {            // this sequence has fewer blocks
+            x += count;
+            continue;
+        }
+        const int rows = min((int)(q.n * group - row0), ROWS);
 
         // ---- the unit's rows
         bf16x8 qf[NQ][KS];
         int pos[NQ];
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) {
-            const uint32_t r = col + 16 * nq, tok = r / group;
+            const uint32_t r = row0 + col + 16 * nq, tok = r / group;
             pos[nq] = q.len - q.n + (int)tok;
             const uint16_t *src = a.q + ((size_t)(q.token + tok) * a.q_heads + head * group + (r - tok * group)) * d;
 #pragma unroll
@@ -183,15 +191,16 @@ __global__ __launch_bounds__(WG, NQ == 1 && DP <= 128 ? 2 : 1) void k_attn_decod
                 // what the lane's 16 bytes of K hold: 8 of every 32 of d, or (E4M3) 16 of every 64
                 const uint32_t e = FP8 ? 64 * (ks / 2) + 16 * quad + 8 * (ks % 2) : 32 * ks + 8 * quad;
                 u32x4 v = {0, 0, 0, 0};
-                if ((int)r < rows && e < d)
+                if ((int)(col + 16 * nq) < rows && e < d)
                     v = *(const u32x4 *)(src + e);
                 qf[nq][ks] = __builtin_bit_cast(bf16x8, v);
             }
         }
         const float scale = a.scale * LOG2E;
         const uint32_t key_from = (q.first / TILE + off) * TILE, key_to = min(key_from + count * TILE, (uint32_t)q.len);
-        const int all_from = a.window ? q.len - (int)min(a.window, (uint32_t)q.len) : 0;   // from here every row sees ...
-        const int all_to = q.len - q.n + 1;                                                // ... up to here (exclusive)
+        const int last_pos = q.len - q.n + (int)((row0 + rows - 1) / group);
+        const int all_from = a.window ? last_pos + 1 - (int64_t)a.window : 0;              // from here every row sees ...
+        const int all_to = q.len - q.n + (int)(row0 / group) + 1;                          // ... up to here (exclusive)
         const uint32_t page_elems = (kv * d) << pl, head_elems = (head * d) << pl;         // of one page: below 2^31
         const int32_t *table = a.table + (size_t)seq * a.width;
         const uint32_t mask = (1u << pl) - 1;
@@ -499,12 +508,12 @@ __global__ __launch_bounds__(WG, NQ == 1 && DP <= 128 ? 2 : 1) void k_attn_decod
             }
             if (finished) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                const uint32_t tok = r / group;
+                const uint32_t flat = row0 + r, tok = flat / group;
                 u32x4 y;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     y[j] = pk_bf16(v[2 * j] * inv, v[2 * j + 1] * inv);
-                *(u32x4 *)(a.out + ((size_t)(q.token + tok) * a.q_heads + head * group + (r - tok * group)) * d + e) = y;
+                *(u32x4 *)(a.out + ((size_t)(q.token + tok) * a.q_heads + head * group + (flat - tok * group)) * d + e) = y;
             } else {
                 float *dst = parts.o + (slot + r) * d + e;
                 *(f32x4 *)dst = (f32x4){v[0], v[1], v[2], v[3]};
@@ -516,7 +525,7 @@ __global__ __launch_bounds__(WG, NQ == 1 && DP <= 128 ? 2 : 1) void k_attn_decod
         if (begins && !finished) {
             began = true;
             if (tid == 0)
-                parts.begun[w] = {(int)share_of(unit + tiles - 1, total, shares), q.token, 0, rows, (int)head, {0, 0, 0}};
+                parts.begun[w] = {(int)share_of(unit + tiles - 1, total, shares), q.token, (int)row0, rows, (int)head, {0, 0, 0}};
         }
         x += count;
     }
@@ -618,23 +627,25 @@ void join(const AttnArgs &a, const Parts &p, uint32_t shares, uint32_t rows, uin
 }
 
 template <int DP, int NQ>
-void launch_rows(const AttnArgs &a, const Parts &p, uint32_t shares, hipStream_t st)
+void launch_rows(const AttnArgs &a, const Parts &p, uint32_t shares, uint32_t blocks, hipStream_t st)
 {
     if (a.cache.fp8)
-        k_attn_decode<DP, NQ, true><<<shares, WG, 0, st>>>(a, p, shares);
+        k_attn_decode<DP, NQ, true><<<shares, WG, 0, st>>>(a, p, shares, blocks);
     else
-        k_attn_decode<DP, NQ, false><<<shares, WG, 0, st>>>(a, p, shares);
+        k_attn_decode<DP, NQ, false><<<shares, WG, 0, st>>>(a, p, shares, blocks);
 }
+
+// Rows of a block: 16, or (more, and as long as they leave two waves a SIMD) 32.
+uint32_t room(uint32_t rows, uint32_t d) { return rows <= 16 || d > 128 ? 16 : 32; }
 
 template <int DP>
 void launch(const AttnArgs &a, const Parts &p, uint32_t rows, uint32_t shares, hipStream_t st)
 {
-    if (rows <= 16)
-        launch_rows<DP, 1>(a, p, shares, st);
-    else if (rows <= 32 || DP == 256)
-        launch_rows<DP, 2>(a, p, shares, st);
+    const uint32_t each = room(rows, DP), blocks = (rows + each - 1) / each;
+    if (each == 16)
+        launch_rows<DP, 1>(a, p, shares, blocks, st);
     else
-        launch_rows<DP == 256 ? 64 : DP, DP == 256 ? 1 : 4>(a, p, shares, st);
+        launch_rows<DP == 256 ? 64 : DP, DP == 256 ? 1 : 2>(a, p, shares, blocks, st);
 }
 
 } // namespace
@@ -652,27 +663,25 @@ hipError_t launch_attn_join(const AttnArgs &a, const Parts &p, uint32_t shares, 
     return hipGetLastError();
 }
 
-// Rows of a workgroup, in 16s that the kernel is built for.
-static uint32_t room(uint32_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
-
 // As many workgroups as the chip holds at a time.
-static uint32_t max_shares(uint32_t rows, uint32_t d)
+static uint32_t max_shares(uint32_t d)
 {
-    return (rows <= 16 && d <= 128 ? 2 : 1) * (cu_count() ? cu_count() : 256);
+    return (d <= 128 ? 2 : 1) * (cu_count() ? cu_count() : 256);
 }
 
 uint64_t decode_work(uint32_t rows, uint32_t d)
 {
-    return parts_bytes(max_shares(rows, d), room(rows), d);
+    return parts_bytes(max_shares(d), room(rows, d), d);
 }
 
 hipError_t launch_attn_decode(const AttnArgs &a, hipStream_t st)
 {
-    const uint32_t rows = a.max_q * (a.q_heads / a.cache.heads), d = a.cache.d;
+    const uint32_t rows = a.max_q * (a.q_heads / a.cache.heads), d = a.cache.d, each = room(rows, d);
     // no more workgroups than the table has room for tiles
-    const uint64_t most = (uint64_t)a.seqs * a.cache.heads * ((((uint64_t)a.width << a.cache.page_log2) + TILE - 1) / TILE);
-    const uint32_t shares = (uint32_t)min((uint64_t)max_shares(rows, d), most);
-    const Parts p = parts_at(a.work, shares, room(rows));
+    const uint64_t most = (uint64_t)a.seqs * a.cache.heads * ((rows + each - 1) / each) *
+                          ((((uint64_t)a.width << a.cache.page_log2) + TILE - 1) / TILE);
+    const uint32_t shares = (uint32_t)min((uint64_t)max_shares(d), most);
+    const Parts p = parts_at(a.work, shares, each);
     if (d <= 64)
         launch<64>(a, p, rows, shares, st);
     else if (d <= 128)
@@ -682,7 +691,7 @@ hipError_t launch_attn_decode(const AttnArgs &a, hipStream_t st)
     count_launch();
     if (hipError_t e = hipGetLastError())
         return e;
-    return launch_attn_join(a, p, shares, room(rows), rows, st);
+    return launch_attn_join(a, p, shares, each, min(rows, each), st);
 }
 
 } // namespace attn
