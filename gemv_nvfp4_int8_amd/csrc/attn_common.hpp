@@ -146,7 +146,7 @@ hipError_t launch_attn_join(const AttnArgs &a, const Parts &p, uint32_t shares, 
 
 // Rows of a sequence times heads of a kv head up to decode_rows(d):
 // attn_decode.hip; more: attn_tiles.hip.
-constexpr uint32_t decode_rows(uint32_t d) { return d <= 128 ? 64 : 32; }
+constexpr uint32_t decode_rows(uint32_t d) { return d <= 128 ? 128 : 64; }
 uint64_t decode_work(uint32_t rows, uint32_t d);
 hipError_t launch_attn_decode(const AttnArgs &a, hipStream_t st);
 uint64_t tiles_work(uint32_t d);

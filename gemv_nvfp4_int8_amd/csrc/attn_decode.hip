@@ -57,8 +57,10 @@ __device__ __forceinline__ void load_dwords(__amdgpu_buffer_rsrc_t p, uint32_t a
 }
 
 // DP: d rounded up to 64, 128 or 256 (what lies past d is read from the head's
-// start, meets zeros of Q, and is not stored); NQ: 16s of rows; blocks: of so many
-// rows a sequence and head may have.
+// start, meets zeros of Q, and is not stored); NQ: 16s of rows of a wave; blocks (1, 2
+// or 4): of so many rows a workgroup has, whose waves then go through the same keys
+// at the same time, so that a block finds them in the L1 where another has loaded
+// them.
 template <int DP, int NQ, bool FP8>
 __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs a, Parts parts, uint32_t max_shares, uint32_t blocks)
 {
@@ -78,10 +80,9 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
     const uint32_t tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const uint32_t col = lane % 16, quad = lane / 16;
     const uint32_t d = a.cache.d, kv = a.cache.heads, group = a.q_heads / kv, pl = a.cache.page_log2;
-    const uint32_t units = kv * blocks;    // of a sequence
+    const uint32_t hop = STEP * (WAVES / blocks);      // from a wave's step to its next
 
-    // ---- the share: tiles of all sequences in one line, a sequence's heads one after
-    // the other, and the blocks of a head so that they find its keys in a cache
+    // ---- the share: tiles of all sequences in one line, a sequence's heads one after the other
     auto wave_scan = [&](uint32_t v) {                  // inclusive
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
@@ -104,7 +105,7 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
         ahead += w < wave ? scan[w] : 0;
         total += scan[w];
     }
-    total = uniform(total * units);
+    total = uniform(total * kv);
     const uint64_t shares = min((uint64_t)max_shares, total);
     const uint32_t w = blockIdx.x;
     if (w >= shares) {
@@ -118,14 +119,14 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
     uint32_t seq = 0;
     uint64_t seq_tile = 0;
     if (a.seqs <= WG) {
-        const uint64_t to = (ahead + incl) * units, from = to - (uint64_t)mine * units;
+        const uint64_t to = (ahead + incl) * kv, from = to - (uint64_t)mine * kv;
         if (tid < a.seqs && x >= from && x < to) {
             found[0] = tid;
             found[1] = (uint32_t)(ahead + incl - mine);
         }
         __syncthreads();
         seq = found[0];
-        seq_tile = (uint64_t)found[1] * units;
+        seq_tile = (uint64_t)found[1] * kv;
     } else {
         uint64_t base = 0;
         for (uint32_t s0 = 0; s0 < a.seqs; s0 += WG) {
@@ -142,7 +143,7 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
                 before += v < wave ? scan[v] : 0;
                 base += scan[v];
             }
-            const uint64_t to = (before + in) * units, from = to - (uint64_t)t * units;
+            const uint64_t to = (before + in) * kv, from = to - (uint64_t)t * kv;
             if (x >= from && x < to) {
                 found[0] = s0 + tid;
                 found[1] = (uint32_t)(before + in - t);
@@ -152,7 +153,7 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
                 break;
         }
         seq = found[0];
-        seq_tile = (uint64_t)found[1] * units;
+        seq_tile = (uint64_t)found[1] * kv;
     }
     seq = min(uniform(seq), a.seqs - 1);
     seq_tile = uniform(seq_tile);
@@ -161,22 +162,19 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
     while (x < share_end) {
         const Seq q = read_seq_uniform(a, seq);
         const uint32_t tiles = tiles_of(q);
-        if (tiles == 0 || x >= seq_tile + (uint64_t)tiles * units) {
-            seq_tile += (uint64_t)tiles * units;
+        if (tiles == 0 || x >= seq_tile + (uint64_t)tiles * kv) {
+            seq_tile += (uint64_t)tiles * kv;
             if (++seq == a.seqs)
                 break;                     // not reached unless the lengths change under the call
             continue;
         }
-        const uint32_t nth = uniform((uint32_t)((x - seq_tile) / tiles)), head = nth / blocks;
-        const uint64_t unit = seq_tile + (uint64_t)nth * tiles;
+        const uint32_t head = uniform((uint32_t)((x - seq_tile) / tiles));
+        const uint64_t unit = seq_tile + (uint64_t)head * tiles;
         const uint32_t off = (uint32_t)(x - unit);
         const uint32_t count = (uint32_t)min((uint64_t)(tiles - off), share_end - x);
-        const uint32_t row0 = (nth - head * blocks) * ROWS;
-        if (row0 >= (uint32_t)q.n * group) {            // this sequence has fewer blocks
-            x += count;
-            continue;
-        }
-        const int rows = min((int)(q.n * group - row0), ROWS);
+        // waves w, w + blocks, ... have the rows of block w % blocks
+        const uint32_t row0 = wave % blocks * ROWS, all_rows = q.n * group;
+        const int rows = (int)min(all_rows - min(row0, all_rows), (uint32_t)ROWS);
 
         // ---- the unit's rows
         bf16x8 qf[NQ][KS];
@@ -198,7 +196,7 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
         }
         const float scale = a.scale * LOG2E;
         const uint32_t key_from = (q.first / TILE + off) * TILE, key_to = min(key_from + count * TILE, (uint32_t)q.len);
-        const int last_pos = q.len - q.n + (int)((row0 + rows - 1) / group);
+        const int last_pos = q.len - q.n + (int)((row0 + max(rows, 1) - 1) / group);
         const int all_from = a.window ? last_pos + 1 - (int64_t)a.window : 0;              // from here every row sees ...
         const int all_to = q.len - q.n + (int)(row0 / group) + 1;                          // ... up to here (exclusive)
         const uint32_t page_elems = (kv * d) << pl, head_elems = (head * d) << pl;         // of one page: below 2^31
@@ -232,87 +230,102 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
         u32x4 kr[2][KL];
         uint32_t vr[8][VW];
         f32x4 ksc[2], vsc[2];
-        // lane i: the page of 16 keys of the wave's step i / 2, of 32 steps
-        auto look = [&](uint32_t key) {
-            const uint32_t k = key + lane / 2 * TILE + lane % 2 * 16;
-            return k < key_to ? (uint32_t)table[k >> pl] : ~0u;
-        };
-        uint32_t pages = 0, pages_next = 0, step = 0, hole = 0;
-        uint64_t rows_at[2];               // where the step's 16 keys lie, in rows of the cache
+        // Where the keys of 32 of the wave's steps lie: lane i's are 16 of step i / 2.  In
+        // bytes of K (and of V), for E4M3 also of the scales; and which are holes.
+        uint32_t step = 0, hole = 0, page_next = 0, at_lo = 0, at_hi = 0, scale_lo = 0, scale_hi = 0;
+        uint64_t missing = 0;
         const uint32_t row_bytes = d * ROWB;
-        // of the step at `key`; past the end, as of holes, nothing is loaded
+        auto look = [&](uint32_t key) {
+            const uint32_t k = key + lane / 2 * hop + lane % 2 * 16;
+            page_next = k < key_to ? (uint32_t)table[k >> pl] : ~0u;
+        };
+        // the places of the step at `key`, and their loads; past the end, as of holes,
+        // nothing is fetched
         auto places = [&](uint32_t key) {
             if (step % 32 == 0) {
-                pages = pages_next;
-                pages_next = look(key + 32 * TILE);
+                const bool none = page_next >= a.cache.pages;
+                missing = __ballot(none);
+                const uint64_t row = (((none ? 0 : page_next) * (uint64_t)kv + head) << pl) +
+                                     ((key + lane / 2 * hop + lane % 2 * 16) & mask);
+                at_lo = (uint32_t)(row * row_bytes);
+                at_hi = (uint32_t)(row * row_bytes >> 32);
+                scale_lo = (uint32_t)(4 * row);
+                scale_hi = (uint32_t)(4 * row >> 32);
+                look(key + 32 * hop);
             }
-            hole = 0;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                uint32_t page = __builtin_amdgcn_readlane(pages, 2 * (step % 32) + t);
-                if (page >= a.cache.pages) {
-                    page = 0;
-                    hole |= 1u << t;
-                }
-                rows_at[t] = ((page * (uint64_t)kv + head) << pl) + ((key + 16 * t) & mask);
-            }
+            hole = (uint32_t)(missing >> 2 * (step % 32)) & 3;
             ++step;
+        };
+        auto from_lane = [&](uint32_t hi, uint32_t lo, int t) {
+            const uint32_t i = 2 * ((step - 1) % 32) + t;
+            return (uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, i) << 32 | (uint32_t)__builtin_amdgcn_readlane(lo, i);
         };
         auto load_k = [&]() {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const bool there = !(hole >> t & 1);
-                const __amdgpu_buffer_rsrc_t p = window_at(a.cache.k, rows_at[t] * row_bytes, there ? 16 * row_bytes : 0);
+                const __amdgpu_buffer_rsrc_t p = window_at(a.cache.k, from_lane(at_hi, at_lo, t), hole >> t & 1 ? 0 : 16 * row_bytes);
 #pragma unroll
                 for (int ks = 0; ks < KL; ++ks)
                     kr[t][ks] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(p, k_off[ks], 0, 0));
                 if (FP8)
                     ksc[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                        window_at(a.cache.ks, 4 * rows_at[t], there ? 64 : 0), 16 * quad, 0, 0));
+                        window_at(a.cache.ks, from_lane(scale_hi, scale_lo, t), hole >> t & 1 ? 0 : 64), 16 * quad, 0, 0));
             }
         };
         auto load_v = [&]() {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const bool there = !(hole >> t & 1);
-                const __amdgpu_buffer_rsrc_t p = window_at(a.cache.v, rows_at[t] * row_bytes, there ? 16 * row_bytes : 0);
+                const __amdgpu_buffer_rsrc_t p = window_at(a.cache.v, from_lane(at_hi, at_lo, t), hole >> t & 1 ? 0 : 16 * row_bytes);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     load_dwords<VW>(p, v_off[j], vr[4 * t + j]);
                 if (FP8)
                     vsc[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                        window_at(a.cache.vs, 4 * rows_at[t], there ? 64 : 0), 16 * quad, 0, 0));
+                        window_at(a.cache.vs, from_lane(scale_hi, scale_lo, t), hole >> t & 1 ? 0 : 64), 16 * quad, 0, 0));
             }
         };
-        // elements 2 e and 2 e + 1 of the lane's 8 keys, in BF16
-        auto pair = [&](int e, uint32_t *x) {
+        // V's fragments of the lane's elements 2 e and 2 e + 1 (E4M3: 4 e .. 4 e + 3): bytes
+        // of 8 keys put together
+        constexpr int FRAGS = FP8 ? 4 : 2;
+        auto fragments = [&](int e, bf16x8 *f) {
+            auto mix = [](uint32_t hi, uint32_t lo, uint32_t how) { return __builtin_amdgcn_perm(hi, lo, how); };
+            constexpr uint32_t FIRST = 0x05040100u, LAST = 0x07060302u;            // halves of two words
+            if constexpr (!FP8) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if constexpr (!FP8)
-                    x[k] = vr[k][e % VW];
-                else if (e % 2)
-                    x[k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[k][e / 2], 1.0f, true));
-                else
-                    x[k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[k][e / 2], 1.0f, false));
+                for (int h = 0; h < 2; ++h) {
+                    u32x4 r;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        r[k] = mix(vr[2 * k + 1][e], vr[2 * k][e], h ? LAST : FIRST);
+                    f[h] = __builtin_bit_cast(bf16x8, r);
+                }
+            } else {
+                uint32_t x[4][2];          // element, 4 keys
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const uint32_t v0 = vr[4 * t][e], v1 = vr[4 * t + 1][e], v2 = vr[4 * t + 2][e], v3 = vr[4 * t + 3][e];
+                    const uint32_t a0 = mix(v1, v0, 0x05010400u), a1 = mix(v1, v0, 0x07030602u);
+                    const uint32_t b0 = mix(v3, v2, 0x05010400u), b1 = mix(v3, v2, 0x07030602u);
+                    x[0][t] = mix(b0, a0, FIRST);
+                    x[1][t] = mix(b0, a0, LAST);
+                    x[2][t] = mix(b1, a1, FIRST);
+                    x[3][t] = mix(b1, a1, LAST);
+                }
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    f[h] = __builtin_bit_cast(bf16x8, bf16_of_e4m3((u32x2){x[h][0], x[h][1]}));
             }
-        };
-        // element 2 e (odd: 2 e + 1) of the keys in the operand's order
-        auto turned = [&](const uint32_t *x, bool second) {
-            u32x4 r;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                r[k] = __builtin_amdgcn_perm(x[2 * k + 1], x[2 * k], second ? 0x07060302u : 0x05040100u);
-            return r;
         };
 
-        uint32_t key = key_from + STEP * wave;
-        pages_next = look(key);
+        // (a wave whose block has no rows goes past the keys at once)
+        uint32_t key = rows > 0 ? key_from + STEP * (wave / blocks) : key_to;
+        look(key);
         places(key);
         load_k();
         load_v();
 #pragma unroll 1
-        for (; key < key_to; key += TILE) {
-            const uint32_t hole_now = hole, next = key + TILE;
+        for (; key < key_to; key += hop) {
+            const uint32_t hole_now = hole, next = key + hop;
             // ---- scores
             f32x4 s[NQ][2];
 #pragma unroll
@@ -445,16 +458,14 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
 
             // ---- V
 #pragma unroll
-            for (int e = 0; e < EPL / 2; ++e) {
-                uint32_t x[8];
-                pair(e, x);
+            for (int e = 0; e < EPL / FRAGS; ++e) {
+                bf16x8 f[FRAGS];
+                fragments(e, f);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const bf16x8 vf = __builtin_bit_cast(bf16x8, turned(x, h));
+                for (int h = 0; h < FRAGS; ++h)
 #pragma unroll
                     for (int nq = 0; nq < NQ; ++nq)
-                        acc[nq][2 * e + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[nq], acc[nq][2 * e + h], 0, 0, 0);
-                }
+                        acc[nq][FRAGS * e + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[h], pf[nq], acc[nq][FRAGS * e + h], 0, 0, 0);
             }
             load_v();
         }
@@ -473,7 +484,7 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) {
             float top = -INFINITY;
-            for (uint32_t v = 0; v < WAVES; ++v)
+            for (uint32_t v = wave % blocks; v < WAVES; v += blocks)
                 top = __builtin_fmaxf(top, ml_lds[v][16 * nq + col][0]);
             const float f = __builtin_amdgcn_exp2f(m[nq] - (top == -INFINITY ? 0.0f : top));
 #pragma unroll
@@ -487,20 +498,20 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
         __syncthreads();
         const bool finished = count == tiles;
         const bool begins = off == 0;
-        const size_t slot = (2 * (size_t)w + begins) * ROWS;
-        for (uint32_t i = tid; i < ROWS * DP / 8; i += WG) {
-            const uint32_t r = i / (DP / 8), e = 8 * (i % (DP / 8));
-            if ((int)r >= rows || e >= d)
+        const size_t slot = (2 * (size_t)w + begins) * ROWS * blocks;
+        for (uint32_t i = tid; i < ROWS * blocks * (DP / 8); i += WG) {
+            const uint32_t r = i / (DP / 8), e = 8 * (i % (DP / 8)), block = r / ROWS, rb = r % ROWS;
+            if (r >= all_rows || e >= d)
                 continue;
             float top = -INFINITY, sum = 0.0f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            for (uint32_t u = 0; u < WAVES; ++u)
-                top = __builtin_fmaxf(top, ml_lds[u][r][0]);
+            for (uint32_t u = block; u < WAVES; u += blocks)
+                top = __builtin_fmaxf(top, ml_lds[u][rb][0]);
             const float to = top == -INFINITY ? 0.0f : top;
-            for (uint32_t u = 0; u < WAVES; ++u) {
-                sum += ml_lds[u][r][1] * __builtin_amdgcn_exp2f(ml_lds[u][r][0] - to);
+            for (uint32_t u = block; u < WAVES; u += blocks) {
+                sum += ml_lds[u][rb][1] * __builtin_amdgcn_exp2f(ml_lds[u][rb][0] - to);
 #pragma unroll
                 for (int j = 0; j < 8; j += 4) {
-                    const f32x4 part = *(const f32x4 *)&o_lds[u][r][e + j];
+                    const f32x4 part = *(const f32x4 *)&o_lds[u][rb][e + j];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         v[j + k] += part[k];
@@ -508,12 +519,12 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
             }
             if (finished) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                const uint32_t flat = row0 + r, tok = flat / group;
+                const uint32_t tok = r / group;
                 u32x4 y;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     y[j] = pk_bf16(v[2 * j] * inv, v[2 * j + 1] * inv);
-                *(u32x4 *)(a.out + ((size_t)(q.token + tok) * a.q_heads + head * group + (flat - tok * group)) * d + e) = y;
+                *(u32x4 *)(a.out + ((size_t)(q.token + tok) * a.q_heads + head * group + (r - tok * group)) * d + e) = y;
             } else {
                 float *dst = parts.o + (slot + r) * d + e;
                 *(f32x4 *)dst = (f32x4){v[0], v[1], v[2], v[3]};
@@ -525,7 +536,7 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
         if (begins && !finished) {
             began = true;
             if (tid == 0)
-                parts.begun[w] = {(int)share_of(unit + tiles - 1, total, shares), q.token, (int)row0, rows, (int)head, {0, 0, 0}};
+                parts.begun[w] = {(int)share_of(unit + tiles - 1, total, shares), q.token, 0, (int)all_rows, (int)head, {0, 0, 0}};
         }
         x += count;
     }
@@ -638,14 +649,19 @@ void launch_rows(const AttnArgs &a, const Parts &p, uint32_t shares, uint32_t bl
 // Rows of a block: 16, or (more, and as long as they leave two waves a SIMD) 32.
 uint32_t room(uint32_t rows, uint32_t d) { return rows <= 16 || d > 128 ? 16 : 32; }
 
+uint32_t blocks_of(uint32_t rows, uint32_t d)
+{
+    const uint32_t n = (rows + room(rows, d) - 1) / room(rows, d);
+    return n <= 2 ? n : 4;
+}
+
 template <int DP>
 void launch(const AttnArgs &a, const Parts &p, uint32_t rows, uint32_t shares, hipStream_t st)
 {
-    const uint32_t each = room(rows, DP), blocks = (rows + each - 1) / each;
-    if (each == 16)
-        launch_rows<DP, 1>(a, p, shares, blocks, st);
+    if (room(rows, DP) == 16)
+        launch_rows<DP, 1>(a, p, shares, blocks_of(rows, DP), st);
     else
-        launch_rows<DP == 256 ? 64 : DP, DP == 256 ? 1 : 2>(a, p, shares, blocks, st);
+        launch_rows<DP == 256 ? 64 : DP, DP == 256 ? 1 : 2>(a, p, shares, blocks_of(rows, DP), st);
 }
 
 } // namespace
@@ -671,15 +687,14 @@ static uint32_t max_shares(uint32_t d)
 
 uint64_t decode_work(uint32_t rows, uint32_t d)
 {
-    return parts_bytes(max_shares(d), room(rows, d), d);
+    return parts_bytes(max_shares(d), room(rows, d) * blocks_of(rows, d), d);
 }
 
 hipError_t launch_attn_decode(const AttnArgs &a, hipStream_t st)
 {
-    const uint32_t rows = a.max_q * (a.q_heads / a.cache.heads), d = a.cache.d, each = room(rows, d);
+    const uint32_t rows = a.max_q * (a.q_heads / a.cache.heads), d = a.cache.d, each = room(rows, d) * blocks_of(rows, d);
     // no more workgroups than the table has room for tiles
-    const uint64_t most = (uint64_t)a.seqs * a.cache.heads * ((rows + each - 1) / each) *
-                          ((((uint64_t)a.width << a.cache.page_log2) + TILE - 1) / TILE);
+    const uint64_t most = (uint64_t)a.seqs * a.cache.heads * ((((uint64_t)a.width << a.cache.page_log2) + TILE - 1) / TILE);
     const uint32_t shares = (uint32_t)min((uint64_t)max_shares(d), most);
     const Parts p = parts_at(a.work, shares, each);
     if (d <= 64)
@@ -691,7 +706,7 @@ hipError_t launch_attn_decode(const AttnArgs &a, hipStream_t st)
     count_launch();
     if (hipError_t e = hipGetLastError())
         return e;
-    return launch_attn_join(a, p, shares, each, min(rows, each), st);
+    return launch_attn_join(a, p, shares, each, rows, st);
 }
 
 } // namespace attn
