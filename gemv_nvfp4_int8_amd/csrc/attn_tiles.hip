@@ -309,9 +309,8 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
             }
         };
         // One tile; masked: some of the wave's rows do not see some of its keys.
-        auto step = [&](const uint8_t *kt, const uint8_t *vt, int k0, uint32_t buf, uint32_t gaps, bool masked) {
-            const int pos = (int)here(my_pos);
-            auto sees = [&](int k) { return k0 + k <= pos && (!a.window || (uint32_t)(pos - k0 - k) < a.window) && !(gaps >> (k / 16) & 1); };
+        auto step = [&](const uint8_t *kt, const uint8_t *vt, int k0, uint32_t buf, uint32_t gaps, bool masked, bool poisoned) {
+            auto sees = [&](int k) { const int pos = my_pos; return k0 + k <= pos && (!a.window || (uint32_t)(pos - k0 - k) < a.window) && !(gaps >> (k / 16) & 1); };
             // ---- scores; a lane's are of keys 32 kb + 8 (i / 4) + 4 half + i % 4.  K's
             // fragments are read AHEAD products before they are used (the order is pinned:
             // left alone, each read is put right before its product)
@@ -343,12 +342,16 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
                     }
             }
             if (masked) {
-                const int at = 4 * (int)here(half);
+                // key c of the tile is seen if it is 0 to span before the row's own
+                const int own = (int)here(my_pos) - k0 - 4 * (int)half;
+                const uint32_t span = a.window ? min(a.window - 1, 0x7FFFFFFFu) : 0x7FFFFFFFu;
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float x = sees(32 * kb + 8 * (i / 4) + i % 4 + at) ? s[kb][i] : -INFINITY;
+                        float x = (uint32_t)(own - (32 * kb + 8 * (i / 4) + i % 4)) <= span ? s[kb][i] : -INFINITY;
+                        if (gaps >> (2 * kb + i / 8) & 1)
+                            x = -INFINITY;
                         asm volatile("" : "+v"(x));     // computed in this branch alone
                         s[kb][i] = x;
                     }
@@ -416,20 +419,15 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
             }
             __builtin_amdgcn_sched_barrier(0);
             l += (part[0] + part[1]) + (part[2] + part[3]);
-            if (masked) {
-                uint32_t any = 0;
-                for (uint32_t u = 0; u < NW; ++u)
-                    any |= odd[u];
-                if (uniform(any)) {
-                    // NaN and infinities, in whose places V has zeros, for the rows that see them
+            if (poisoned) {
+                // NaN and infinities, in whose places V has zeros, for the rows that see them
 #pragma unroll 1
-                    for (int k = 0; k < (int)KT; ++k)
-                        if (sees(k)) {
+                for (int k = 0; k < (int)KT; ++k)
+                    if (sees(k)) {
 #pragma unroll
-                            for (uint32_t c = 0; c < CH; ++c)
-                                nans[c / 8] |= (odd_bits[k][c] >> 4 * half & 15u) << (4 * (c % 8));
-                        }
-                }
+                        for (uint32_t c = 0; c < CH; ++c)
+                            nans[c / 8] |= (odd_bits[k][c] >> 4 * half & 15u) << (4 * (c % 8));
+                    }
             }
         };
 
@@ -448,35 +446,46 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
             if (more)
                 gaps_next = load(tile + 1, k_next, v_next);
             const int k0 = tile * KT;
+            uint32_t poisoned = 0;
             if (k0 + (int)KT - 1 > block_lo || (a.window && k0 <= block_hi - (int64_t)a.window) || gaps) {
-                // some row of the block does not see some key, and 0 times NaN would be
-                // NaN: those of V go, and are noted for the rows that see them
+                // some row of the block does not see some key, and 0 times NaN would be NaN
                 uint32_t bad = 0;
+#pragma unroll 2
                 for (uint32_t i = here(threadIdx.x); i < KT * CH; i += WG) {
-                    u32x4 v = *(const u32x4 *)(vt + 16 * i);
-                    uint32_t bits = 0;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t z = not_finite(v[j]);
-                        bits |= (z & 1) << (2 * j) | (z >> 31) << (2 * j + 1);
-                        v[j] &= ~z;
-                    }
-                    const uint32_t r = i / CH;
-                    odd_bits[r][i % CH ^ swizzle<DP>(r)] = bits;
-                    if (bits)
-                        *(u32x4 *)(vt + 16 * i) = v;
-                    bad |= bits;
+                    const u32x4 v = *(const u32x4 *)(vt + 16 * i);
+                    bad |= odd_tops(v[0]) | odd_tops(v[1]) | odd_tops(v[2]) | odd_tops(v[3]);
                 }
                 const bool any = __any(bad != 0);
                 if (lane == 0)
                     odd[wave] = any;
                 __syncthreads();
+                uint32_t some = 0;
+                for (uint32_t u = 0; u < NW; ++u)
+                    some |= odd[u];
+                poisoned = uniform(some);
+                if (poisoned) {
+                    // those of V go, and are noted for the rows that see them
+                    for (uint32_t i = here(threadIdx.x); i < KT * CH; i += WG) {
+                        u32x4 v = *(const u32x4 *)(vt + 16 * i);
+                        uint32_t bits = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t z = not_finite(v[j]);
+                            bits |= (z & 1) << (2 * j) | (z >> 31) << (2 * j + 1);
+                            v[j] &= ~z;
+                        }
+                        const uint32_t r = i / CH;
+                        odd_bits[r][i % CH ^ swizzle<DP>(r)] = bits;
+                        *(u32x4 *)(vt + 16 * i) = v;
+                    }
+                    __syncthreads();
+                }
             }
             const bool none = !wave_live || k0 > pos_hi || (a.window && k0 + (int)KT - 1 <= pos_lo - (int64_t)a.window);
             const bool whole = k0 + (int)KT - 1 <= pos_lo && (!a.window || k0 > pos_hi - (int64_t)a.window) && gaps == 0;
             const int way = uniform(none ? 0u : whole ? 1u : 2u);
             if (way != 0)
-                step(kt, vt, k0, buf, gaps, way == 2);
+                step(kt, vt, k0, buf, gaps, way == 2, poisoned != 0);
             if (more)
                 store(buf ^ 1, k_next, v_next);
             ++tile;
