@@ -23,7 +23,9 @@ namespace qp {
 namespace attn {
 namespace {
 
-constexpr uint32_t KT = 64;                // keys of a tile
+// Keys of a tile: as many as two buffers of them leave room for two workgroups (or
+// eight waves) a compute unit.
+constexpr uint32_t tile_keys(uint32_t d) { return d <= 64 ? 128 : 64; }
 
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -43,6 +45,7 @@ struct Block {
     uint32_t first_tile, tiles;
 };
 
+template <uint32_t KT>
 __device__ __forceinline__ Block block_of(const AttnArgs &a, int n, int len, uint32_t row, uint32_t rows, uint32_t group)
 {
     Block b;
@@ -59,7 +62,7 @@ __device__ __forceinline__ Block block_of(const AttnArgs &a, int n, int len, uin
 template <int DP, int NW, bool FP8>
 __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnArgs a, Parts parts, uint32_t max_shares)
 {
-    constexpr uint32_t WG = 64 * NW;
+    constexpr uint32_t WG = 64 * NW, KT = tile_keys(DP), GROUPS = KT / 16, AHEAD_TILES = 64 / GROUPS;
     constexpr uint32_t ROWS = 32 * NW;
     constexpr int KS = DP / 16;            // MFMAs over d
     constexpr int DB = DP / 32;            // blocks of O's d
@@ -124,7 +127,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
                             s = mid + 1;
                     }
                     row = (b - (s ? seq_end[s - 1] : 0)) * ROWS;
-                    tiles = block_of(a, seq_n[s], seq_len[s], row, ROWS, group).tiles;
+                    tiles = block_of<KT>(a, seq_n[s], seq_len[s], row, ROWS, group).tiles;
                 }
                 uint32_t all;
                 const uint64_t to = before + block_scan(tiles, all), from = to - tiles;
@@ -188,7 +191,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
             }
             continue;
         }
-        const Block blk = block_of(a, q.n, q.len, row0, ROWS, group);
+        const Block blk = block_of<KT>(a, q.n, q.len, row0, ROWS, group);
         const uint32_t off = (uint32_t)(x - unit);
         if (off >= blk.tiles)
             break;
@@ -240,8 +243,8 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
         }
         u32x4 kr[FP8 ? ITEMS : 1], vr[FP8 ? ITEMS : 1];
         float ksr = 0.0f, vsr = 0.0f;
-        // Where 16 tiles' 16s of keys lie, in elements: lane i's is of the keys 16 i
-        // behind the first tile's (or 16, 32, ... tiles later); and which of them are holes.
+        // Where 1024 keys lie, in elements: lane i's are the 16 that begin 16 i behind the
+        // first tile's (or 1024, 2048, ... further); and which of them are holes.
         uint32_t at_lo = 0, at_hi = 0, page_next = 0;
         uint64_t missing = 0, row_at = 0;                  // (the same in rows, for the scales)
         auto look = [&](uint32_t tile) {
@@ -250,7 +253,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
         };
         // Starts a tile's loads; returns its 16s of keys that are holes, as bits.
         auto load = [&](uint32_t tile, uint8_t *kd, uint8_t *vd) {
-            const uint32_t nth = (tile - (blk.first_tile + off)) % 16;
+            const uint32_t nth = (tile - (blk.first_tile + off)) % AHEAD_TILES;
             if (nth == 0) {
                 const bool hole = page_next >= a.cache.pages;
                 const uint64_t at = (uint64_t)(hole ? 0 : page_next) * page_elems + (head_elems + ((tile * KT + 16 * lane) & mask) * d);
@@ -259,16 +262,16 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
                 at_hi = (uint32_t)(at >> 32);
                 if (FP8)
                     row_at = (((hole ? 0 : page_next) * (uint64_t)kv + head) << pl) + ((tile * KT + 16 * lane) & mask);
-                look(tile + 16);
+                look(tile + AHEAD_TILES);
             }
-            const uint32_t gaps = (uint32_t)(missing >> 4 * nth) & 15;
+            const uint32_t gaps = (uint32_t)(missing >> GROUPS * nth) & ((1u << GROUPS) - 1);
 #pragma unroll
             for (uint32_t i = 0; i < ITEMS; ++i) {
                 // the 16 keys that this wave's pieces are of
                 constexpr uint32_t WAVE_ROWS = 64 / CPR;
                 const uint32_t g = i * (WG / CPR) / 16 + (WAVE_ROWS * NW > 16 ? wave * WAVE_ROWS / 16 : 0);
-                const uint64_t row = (uint64_t)(uint32_t)__builtin_amdgcn_readlane(at_hi, 4 * nth + g) << 32 |
-                                     (uint32_t)__builtin_amdgcn_readlane(at_lo, 4 * nth + g);
+                const uint64_t row = (uint64_t)(uint32_t)__builtin_amdgcn_readlane(at_hi, GROUPS * nth + g) << 32 |
+                                     (uint32_t)__builtin_amdgcn_readlane(at_lo, GROUPS * nth + g);
                 const uint32_t bytes = gaps >> g & 1 ? 0 : 16 * d * EB;                // a hole is read as zeros
                 const __amdgpu_buffer_rsrc_t kp = window_at(a.cache.k, row * EB, bytes), vp = window_at(a.cache.v, row * EB, bytes);
                 if constexpr (FP8) {
@@ -281,9 +284,9 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
                 }
             }
             if (FP8 && tid < KT) {
-                // the first wave: a scale of K and of V each, of the keys' rows of the cache
-                const uint64_t row = __shfl(row_at, 4 * nth + lane / 16, 64) + lane % 16;
-                const bool hole = gaps >> lane / 16 & 1;
+                // the first waves: a scale of K and of V each, of the keys' rows of the cache
+                const uint64_t row = __shfl(row_at, GROUPS * nth + tid / 16, 64) + lane % 16;
+                const bool hole = gaps >> tid / 16 & 1;
                 ksr = hole ? 0.0f : a.cache.ks[row];
                 vsr = hole ? 0.0f : a.cache.vs[row];
             }
@@ -315,24 +318,28 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
             // fragments are read AHEAD products before they are used (the order is pinned:
             // left alone, each read is put right before its product)
             constexpr int AHEAD = 4;
-            f32x16 s[2] = {(f32x16)0.0f, (f32x16)0.0f};
+            constexpr int KB = KT / 32;
+            f32x16 s[KB];
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+                s[kb] = (f32x16)0.0f;
             bf16x8 kf[AHEAD];
-            auto k_frag = [&](int n) { return *(const bf16x8 *)(kt + n % 2 * 32 * DP * 2 + k_addr[n / 2]); };
+            auto k_frag = [&](int n) { return *(const bf16x8 *)(kt + n % KB * 32 * DP * 2 + k_addr[n / KB]); };
 #pragma unroll
             for (int n = 0; n < AHEAD; ++n)
                 kf[n] = k_frag(n);
 #pragma unroll
-            for (int n = 0; n < 2 * KS; ++n) {
+            for (int n = 0; n < KB * KS; ++n) {
                 __builtin_amdgcn_sched_barrier(0);
-                s[n % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[n % AHEAD], qf[n / 2], s[n % 2], 0, 0, 0);
-                if (n + AHEAD < 2 * KS)
+                s[n % KB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[n % AHEAD], qf[n / KB], s[n % KB], 0, 0, 0);
+                if (n + AHEAD < KB * KS)
                     kf[n % AHEAD] = k_frag(n + AHEAD);
             }
             __builtin_amdgcn_sched_barrier(0);
             const float unit_scale = FP8 ? 1.0f : scale;
             if constexpr (FP8) {
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
+                for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
                         const f32x4 z = *(const f32x4 *)&scales[buf][0][32 * kb + 2 * i + 4 * half];
@@ -346,7 +353,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
                 const int own = (int)here(my_pos) - k0 - 4 * (int)half;
                 const uint32_t span = a.window ? min(a.window - 1, 0x7FFFFFFFu) : 0x7FFFFFFFu;
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
+                for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float x = (uint32_t)(own - (32 * kb + 8 * (i / 4) + i % 4)) <= span ? s[kb][i] : -INFINITY;
@@ -359,8 +366,10 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
             // ---- probabilities
             float top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                top = __builtin_fmaxf(__builtin_fmaxf(top, s[0][i]), s[1][i]);
+            for (int kb = 0; kb < KB; kb += 2)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    top = __builtin_fmaxf(__builtin_fmaxf(top, s[kb][i]), s[kb + 1][i]);
             top *= unit_scale;
             if (__any(top > m + 8.0f)) {
                 top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
@@ -402,13 +411,13 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
             for (int i = 0; i < 4; ++i)
                 pf[i] = pk_bf16(probability(0, 2 * i), probability(0, 2 * i + 1));
 #pragma unroll
-            for (int blk = 0; blk < 4; ++blk) {
+            for (int blk = 0; blk < 2 * KB; ++blk) {
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
                     __builtin_amdgcn_sched_barrier(0);
                     acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[db]),
                                                                       __builtin_bit_cast(bf16x8, pf), acc[db], 0, 0, 0);
-                    if (blk == 3)
+                    if (blk == 2 * KB - 1)
                         continue;
                     vf[db] = v_frag(blk + 1, db);
 #pragma unroll
