@@ -22,14 +22,14 @@ namespace attn {
 
 constexpr float LOG2E = 1.4426950408889634f;
 
-// One entry per share: the unit that it began and did not finish.
+// One entry per share: the unit that goes on in the next share.
 struct Begun {
-    int32_t last;        // the share that holds the unit's last tile; -1: no such unit
+    int32_t first, last; // the shares that hold its first and its last tile; last = -1: no such unit
     int32_t token;       // the row of q of the sequence's first row
     int32_t row;         // the unit's first flattened row
     int32_t rows;        // its rows
     int32_t head;        // its kv head
-    int32_t pad[3];
+    int32_t pad[2];
 };
 
 // The workspace of `shares` shares of units of up to `rows` rows.
@@ -144,9 +144,19 @@ __device__ __forceinline__ uint32_t share_of(uint64_t x, uint64_t n, uint64_t sh
 hipError_t launch_attn_join(const AttnArgs &a, const Parts &p, uint32_t shares, uint32_t rows, uint32_t live,
                             hipStream_t st);
 
-// Rows of a sequence times heads of a kv head up to decode_rows(d):
-// attn_decode.hip; more: attn_tiles.hip.
-constexpr uint32_t decode_rows(uint32_t d) { return d <= 128 ? 128 : 64; }
+// Rows of a sequence (times heads of a kv head) up to which attn_decode.hip is the
+// faster one.  Measured, 16 sequences over 9001 positions, 4 kv heads, few rows'
+// kernel and tiles', us:
+//   rows            16           32           64          128
+//   BF16 d =  64    34 and  39   35 and  40   40 and  42   65 and  46
+//   BF16 d = 128    56 and  64   61 and  65   76 and  67  121 and  74
+//   BF16 d = 192    88 and  97  110 and  97  183 and 107
+//   BF16 d = 256   117 and 115  125 and 117  198 and 126
+//   E4M3 d =  64    25 and  41   28 and  41   40 and  46   65 and  50
+//   E4M3 d = 128    37 and  92   40 and  93   55 and  94   90 and  98
+//   E4M3 d = 256    57 and 111   74 and 113  116 and 116
+// (the same order over 1 sequence of 32000 and 64 of 1000).
+constexpr uint32_t decode_rows(uint32_t d, bool fp8) { return fp8 || d <= 64 ? 64 : d <= 128 ? 32 : 16; }
 uint64_t decode_work(uint32_t rows, uint32_t d);
 hipError_t launch_attn_decode(const AttnArgs &a, hipStream_t st);
 uint64_t tiles_work(uint32_t d);

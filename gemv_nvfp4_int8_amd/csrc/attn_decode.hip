@@ -110,7 +110,7 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
     const uint32_t w = blockIdx.x;
     if (w >= shares) {
         if (tid == 0)
-            parts.begun[w].last = -1;
+            parts.begun[w] = {0, -1, 0, 0, 0, 0, {0, 0}};
         return;
     }
     uint64_t x = uniform(w * total / shares);
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
     seq = min(uniform(seq), a.seqs - 1);
     seq_tile = uniform(seq_tile);
 
-    bool began = false;
+    bool goes_on = false;
     while (x < share_end) {
         const Seq q = read_seq_uniform(a, seq);
         const uint32_t tiles = tiles_of(q);
@@ -323,6 +323,13 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
         places(key);
         load_k();
         load_v();
+        // (under the first loads)
+        if (off + count < tiles) {
+            goes_on = true;
+            const uint32_t last = min(share_of(unit + tiles - 1, total, shares), (uint32_t)shares - 1);
+            if (tid == 0)
+                parts.begun[w] = {off == 0 ? (int)w : (int)share_of(unit, total, shares), (int)last, q.token, 0, (int)all_rows, (int)head, {0, 0}};
+        }
 #pragma unroll 1
         for (; key < key_to; key += hop) {
             const uint32_t hole_now = hole, next = key + hop;
@@ -533,39 +540,36 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
                     parts.ml[slot + r] = (f32x2){top, sum};
             }
         }
-        if (begins && !finished) {
-            began = true;
-            if (tid == 0)
-                parts.begun[w] = {(int)share_of(unit + tiles - 1, total, shares), q.token, 0, (int)all_rows, (int)head, {0, 0, 0}};
-        }
         x += count;
     }
-    if (!began && tid == 0)
-        parts.begun[w].last = -1;
+    if (!goes_on && tid == 0)
+        parts.begun[w] = {0, -1, 0, 0, 0, 0, {0, 0}};
 }
 
-// LP lanes take a row of a part, 16 bytes each, and a workgroup has G such groups.
-// BY_ROW: a group goes through all parts of a row of its own.  Otherwise (few rows
-// of many parts) the groups share a row's parts and join through LDS.
-template <int LP, bool BY_ROW>
+// A unit's rows go to the workgroups of all its shares but the last (no other unit
+// goes on from those).  LP lanes take a row of a part, 16 bytes each, and a
+// workgroup has G such groups: of few parts (by_row) each goes through all parts
+// of a row of its own; of many, they share a row's parts and join through LDS.
+template <int LP>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, Parts parts, uint32_t rows)
 {
     constexpr uint32_t G = 256 / LP;
-    __shared__ float o_lds[BY_ROW ? 1 : G][4 * LP];
-    __shared__ f32x2 ml_lds[BY_ROW ? 1 : G];
+    __shared__ float o_lds[G][4 * LP];
+    __shared__ f32x2 ml_lds[G];
     const Begun b = parts.begun[blockIdx.x];
-    if (b.last < 0)
+    if (b.last <= b.first)
         return;
     const uint32_t d = a.cache.d, group = a.q_heads / a.cache.heads, g = threadIdx.x / LP, e = 4 * (threadIdx.x % LP);
-    const uint32_t from = blockIdx.x, count = b.last - from + 1;
-    const uint32_t per = BY_ROW ? G : 1;
-    for (uint32_t r0 = blockIdx.y * per; r0 < (uint32_t)b.rows; r0 += gridDim.y * per) {
-        const uint32_t r = r0 + (BY_ROW ? g : 0);
+    const uint32_t from = b.first, count = b.last - from + 1;
+    const bool by_row = count <= 4 || (count <= 8 && (uint32_t)b.rows >= G);
+    const uint32_t per = by_row ? G : 1, each = (count - 1) * per;
+    for (uint32_t r0 = blockIdx.y * each + (blockIdx.x - from) * per; r0 < (uint32_t)b.rows; r0 += gridDim.y * each) {
+        const uint32_t r = r0 + (by_row ? g : 0);
         float m = -INFINITY, l = 0.0f;
         f32x4 acc = {0, 0, 0, 0};
         constexpr int U = 4;
-        const uint32_t step = BY_ROW ? 1 : G;
-        for (uint32_t p0 = BY_ROW ? 0 : g; p0 < count; p0 += U * step) {
+        const uint32_t step = by_row ? 1 : G;
+        for (uint32_t p0 = by_row ? 0 : g; p0 < count; p0 += U * step) {
             f32x2 ml[U];
             f32x4 o[U];
 #pragma unroll
@@ -596,7 +600,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, Parts parts, uint
             }
             m = top;
         }
-        if constexpr (!BY_ROW) {
+        if (!by_row) {
             __syncthreads();
             *(f32x4 *)&o_lds[g][e] = acc;
             if (e == 0)
@@ -629,12 +633,7 @@ template <int LP>
 void join(const AttnArgs &a, const Parts &p, uint32_t shares, uint32_t rows, uint32_t live, hipStream_t st)
 {
     constexpr uint32_t G = 256 / LP;
-    // a unit has about shares / units parts
-    const uint64_t units = max((uint64_t)a.seqs * a.cache.heads, (uint64_t)a.t * a.q_heads / rows);
-    if (live >= G && shares <= 8 * units)
-        k_attn_join<LP, true><<<dim3(shares, (live + G - 1) / G), 256, 0, st>>>(a, p, rows);
-    else
-        k_attn_join<LP, false><<<dim3(shares, min(live, 32u)), 256, 0, st>>>(a, p, rows);
+    k_attn_join<LP><<<dim3(shares, (live + G - 1) / G), 256, 0, st>>>(a, p, rows);
 }
 
 template <int DP, int NQ>

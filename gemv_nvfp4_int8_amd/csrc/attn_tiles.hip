@@ -1,10 +1,10 @@
 // attn_tiles.hip -- attention of many rows a sequence (chunks of a prompt, whole
 // prompts, large verify batches).
 //
-// A workgroup takes a unit of 32 rows a wave and goes through its keys 64 at a
-// time; K and V of the next 64 are on their way (straight to LDS, or through
-// registers where they have to be decoded) while these are worked on, two buffers
-// in turn with one barrier.  A wave computes
+// A workgroup takes a unit of 32 rows a wave (d > 128: every two waves) and goes
+// through its keys a tile at a time; K and V of the next tile are on their way
+// (straight to LDS, or through registers where they have to be decoded) while this
+// one is worked on, two buffers in turn with one barrier.  A wave computes
 //   S^T [key, row] = K Q^T   32x32x16 MFMAs, K from LDS, Q in registers
 //   P^T = exp2(S^T - m)      a lane holds 32 scores of ONE row: its maximum and sum
 //                            need one exchange with the lane 32 further, the
@@ -16,6 +16,15 @@
 // LDS rows hold 16-byte pieces in an order turned by the row number (`swizzle`),
 // so that both 16 rows of one piece (K) and 4 rows of 64 bytes (V) lie in
 // different banks.
+//
+// Where d > 128 a row of O would take twice the registers that leave room for two
+// waves a SIMD: two waves have the same 32 rows, each half of O's d, and both compute
+// S, which is half as many matrix operations again (4096 rows over themselves, 32
+// heads of 256: 600 us, in E4M3 670; one wave a SIMD with all of O: 862 and 1508).
+//
+// What bounds it: at two waves a SIMD, the softmax's vector work beside the matrix
+// operations (an exponential takes 8 cycles of a wave, a product of 32x32x16 32), and
+// the LDS reads, which 32 rows a wave just balance with the matrix operations.
 #include "attn_common.hpp"
 #include "qp_launch.hpp"
 
@@ -23,9 +32,10 @@ namespace qp {
 namespace attn {
 namespace {
 
-// Keys of a tile: as many as two buffers of them leave room for two workgroups (or
-// eight waves) a compute unit.
-constexpr uint32_t tile_keys(uint32_t d) { return d <= 64 ? 128 : 64; }
+// Keys of a tile: as many as two buffers of them leave room for eight waves a
+// compute unit.  (d = 64 with tiles of 64 and three waves a SIMD: 329 us where this
+// takes 305, 7 prompts of up to 2500 in a window of 1024.)
+constexpr uint32_t tile_keys(uint32_t d) { return d <= 64 ? 128 : d <= 128 ? 64 : 32; }
 
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -60,13 +70,15 @@ __device__ __forceinline__ Block block_of(const AttnArgs &a, int n, int len, uin
 }
 
 template <int DP, int NW, bool FP8>
-__global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnArgs a, Parts parts, uint32_t max_shares)
+__global__ __launch_bounds__(64 * NW, 2) void k_attn_tiles(AttnArgs a, Parts parts, uint32_t max_shares)
 {
     constexpr uint32_t WG = 64 * NW, KT = tile_keys(DP), GROUPS = KT / 16, AHEAD_TILES = 64 / GROUPS;
-    constexpr uint32_t ROWS = 32 * NW;
+    constexpr uint32_t SPLIT = DP <= 128 ? 1 : 2;      // waves that have the same rows, and each a part of O's d
+    constexpr uint32_t ROWS = 32 * NW / SPLIT;
     constexpr int KS = DP / 16;            // MFMAs over d
-    constexpr int DB = DP / 32;            // blocks of O's d
+    constexpr int DB = DP / 32 / SPLIT;    // blocks of a wave's part of O's d
     constexpr uint32_t CH = DP / 8;        // 16-byte pieces of a row in LDS
+    constexpr uint32_t CW = CH / SPLIT;    // those of a wave's part of d
     constexpr uint32_t CPR = FP8 ? DP / 16 : DP / 8;   // 16-byte pieces of a row in memory
     constexpr uint32_t ITEMS = KT * CPR / WG;          // of a thread, of K and of V each
     constexpr uint32_t TILE_BYTES = KT * DP * 2;
@@ -81,6 +93,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
 
     const uint32_t tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const uint32_t col = lane % 32, half = lane / 32;
+    const uint32_t strip = wave / SPLIT, part_d = wave % SPLIT * (DP / SPLIT);         // the wave's rows and first d
     const uint32_t d = a.cache.d, kv = a.cache.heads, group = a.q_heads / kv, pl = a.cache.page_log2;
 
     auto block_scan = [&](uint32_t v, uint32_t &all) {  // inclusive over the workgroup
@@ -152,7 +165,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
     const uint32_t w = xcd_remap(blockIdx.x, gridDim.x);
     if (w >= shares) {
         if (tid == 0)
-            parts.begun[w].last = -1;
+            parts.begun[w] = {0, -1, 0, 0, 0, 0, {0, 0}};
         return;
     }
     uint64_t x = uniform(w * total / shares);
@@ -163,12 +176,14 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
     uint64_t unit = (uint64_t)head * line + uniform((uint64_t)found[3] << 32 | found[2]);
 
     const float scale = a.scale * LOG2E;
-    bool began = false;
+    bool goes_on = false;
     // LDS addresses of a lane's fragments: K's piece 2 ks + half of row col, V's
     // pieces of rows 4 half + (lane % 16) / 4 (+ 8) that hold its group's 16 of d
-    uint32_t k_addr[KS];
+    // (the swizzle turns pieces within 16, so that the next 16 lie 256 bytes on)
+    constexpr int KA = KS < 8 ? KS : 8;
+    uint32_t k_addr[KA];
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
+    for (int ks = 0; ks < KA; ++ks)
         k_addr[ks] = col * DP * 2 + ((2 * ks + half) ^ swizzle<DP>(col)) * 16;
     const uint32_t v_row = 4 * half + lane % 16 / 4, v_piece = 2 * (lane / 16 % 2) + lane % 4 / 2;
     uint32_t v_addr[2][DB];
@@ -177,7 +192,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
 #pragma unroll
         for (int db = 0; db < DB; ++db) {
             const uint32_t r = v_row + 8 * jj;
-            v_addr[jj][db] = r * DP * 2 + ((4 * db + v_piece) ^ swizzle<DP>(r)) * 16 + lane % 2 * 8;
+            v_addr[jj][db] = r * DP * 2 + ((4 * db + v_piece) ^ swizzle<DP>(r)) * 16 + lane % 2 * 8 + part_d * 2;
         }
 
     while (x < share_end) {
@@ -199,8 +214,8 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
         const uint32_t rows = min(ROWS, (uint32_t)q.n * group - row0);
 
         // ---- the wave's rows
-        const uint32_t first_row = row0 + 32 * wave, my_row = first_row + col;
-        const bool wave_live = 32 * wave < rows, row_live = 32 * wave + col < rows;
+        const uint32_t first_row = row0 + 32 * strip, my_row = first_row + col;
+        const bool wave_live = 32 * strip < rows, row_live = 32 * strip + col < rows;
         const int old = q.len - q.n;
         const int my_pos = old + (int)(my_row / group);
         const int pos_lo = old + (int)(first_row / group), pos_hi = old + (int)((min(first_row + 32, row0 + rows) - 1) / group);
@@ -214,9 +229,9 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
             qf[ks] = __builtin_bit_cast(bf16x8, v);
         }
         float m = -INFINITY, base = 0.0f, l = 0.0f;
-        uint32_t nans[CH / 8];             // bit 4 c + j: the row's d = 8 c + 4 half + j has met NaN or an infinity
+        uint32_t nans[CW / 8];             // bit 4 c + j: the row's d = part_d + 8 c + 4 half + j has met NaN or an infinity
 #pragma unroll
-        for (uint32_t i = 0; i < CH / 8; ++i)
+        for (uint32_t i = 0; i < CW / 8; ++i)
             nans[i] = 0;
         f32x16 acc[DB];
 #pragma unroll
@@ -324,7 +339,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
             for (int kb = 0; kb < KB; ++kb)
                 s[kb] = (f32x16)0.0f;
             bf16x8 kf[AHEAD];
-            auto k_frag = [&](int n) { return *(const bf16x8 *)(kt + n % KB * 32 * DP * 2 + k_addr[n / KB]); };
+            auto k_frag = [&](int n) { return *(const bf16x8 *)(kt + n % KB * 32 * DP * 2 + k_addr[n / KB % KA] + n / KB / KA * 256); };
 #pragma unroll
             for (int n = 0; n < AHEAD; ++n)
                 kf[n] = k_frag(n);
@@ -366,10 +381,10 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
             // ---- probabilities
             float top = -INFINITY;
 #pragma unroll
-            for (int kb = 0; kb < KB; kb += 2)
+            for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    top = __builtin_fmaxf(__builtin_fmaxf(top, s[kb][i]), s[kb + 1][i]);
+                for (int i = 0; i < 16; i += 2)
+                    top = __builtin_fmaxf(__builtin_fmaxf(top, s[kb][i]), s[kb][i + 1]);
             top *= unit_scale;
             if (__any(top > m + 8.0f)) {
                 top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
@@ -402,29 +417,29 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
                 }
                 return v;
             };
-            u32x4 vf[DB], pf, pn;
+            constexpr int VN = 2 * KB * DB, VR = DB;                    // products; V's fragments in flight
+            u32x4 vf[VR], pf, pn;
 #pragma unroll
-            for (int db = 0; db < DB; ++db)
-                vf[db] = v_frag(0, db);
+            for (int n = 0; n < VR; ++n)
+                vf[n] = v_frag(0, n);
             // rounded to BF16, the operand's type (2^-9 of each on average over keys, as the output's own rounding)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 pf[i] = pk_bf16(probability(0, 2 * i), probability(0, 2 * i + 1));
 #pragma unroll
-            for (int blk = 0; blk < 2 * KB; ++blk) {
-#pragma unroll
-                for (int db = 0; db < DB; ++db) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[db]),
-                                                                      __builtin_bit_cast(bf16x8, pf), acc[db], 0, 0, 0);
-                    if (blk == 2 * KB - 1)
-                        continue;
-                    vf[db] = v_frag(blk + 1, db);
+            for (int n = 0; n < VN; ++n) {
+                const int blk = n / DB, db = n % DB;
+                __builtin_amdgcn_sched_barrier(0);
+                acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[n % VR]),
+                                                                  __builtin_bit_cast(bf16x8, pf), acc[db], 0, 0, 0);
+                if (n + VR < VN)
+                    vf[n % VR] = v_frag((n + VR) / DB, (n + VR) % DB);
+                if (blk < 2 * KB - 1)
 #pragma unroll
                     for (int i = 4 * db / DB; i < 4 * (db + 1) / DB; ++i)
                         pn[i] = pk_bf16(probability(blk + 1, 2 * i), probability(blk + 1, 2 * i + 1));
-                }
-                pf = pn;
+                if (db == DB - 1)
+                    pf = pn;
             }
             __builtin_amdgcn_sched_barrier(0);
             l += (part[0] + part[1]) + (part[2] + part[3]);
@@ -434,8 +449,8 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
                 for (int k = 0; k < (int)KT; ++k)
                     if (sees(k)) {
 #pragma unroll
-                        for (uint32_t c = 0; c < CH; ++c)
-                            nans[c / 8] |= (odd_bits[k][c] >> 4 * half & 15u) << (4 * (c % 8));
+                        for (uint32_t c = 0; c < CW; ++c)
+                            nans[c / 8] |= (odd_bits[k][part_d / 8 + c] >> 4 * half & 15u) << (4 * (c % 8));
                     }
             }
         };
@@ -445,6 +460,13 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
         look(tile);
         __syncthreads();                   // the last unit's tiles have been read
         uint32_t gaps_next = load(tile, k_lds0, v_lds0);
+        // (under the first loads)
+        if (off + count < blk.tiles) {
+            goes_on = true;
+            const uint32_t last = min(share_of(unit + blk.tiles - 1, total, shares), (uint32_t)shares - 1);
+            if (tid == 0)
+                parts.begun[w] = {off == 0 ? (int)w : (int)share_of(unit, total, shares), (int)last, q.token, (int)row0, (int)rows, (int)head, {0, 0}};
+        }
         store(0, k_lds0, v_lds0);
         // A tile from one buffer while the next comes to the other.
         auto turn = [&](uint32_t buf, const uint8_t *kt, uint8_t *vt, uint8_t *k_next, uint8_t *v_next) {
@@ -512,15 +534,15 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
         l += __shfl_xor(l, 32, 64);
         const bool begins = off == 0, finished = count == blk.tiles;
         if (row_live) {
-            const size_t slot = (2 * (size_t)w + begins) * ROWS + 32 * wave + col;
+            const size_t slot = (2 * (size_t)w + begins) * ROWS + 32 * strip + col;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            if (!finished && half == 0)
+            if (!finished && half == 0 && part_d == 0)
                 parts.ml[slot] = (f32x2){m, l};
 #pragma unroll
             for (int db = 0; db < DB; ++db)
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
-                    const uint32_t e = 32 * db + 2 * i + 4 * half;
+                    const uint32_t e = part_d + 32 * db + 2 * i + 4 * half;
                     if (e >= d)
                         continue;
                     f32x4 v = {acc[db][i], acc[db][i + 1], acc[db][i + 2], acc[db][i + 3]};
@@ -533,19 +555,14 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void k_attn_tiles(AttnA
                         *(f32x4 *)(parts.o + slot * d + e) = v;
                 }
         }
-        if (begins && !finished) {
-            began = true;
-            if (tid == 0)
-                parts.begun[w] = {(int)share_of(unit + blk.tiles - 1, total, shares), q.token, (int)row0, (int)rows, (int)head, {0, 0, 0}};
-        }
         x += count;
         if (x == unit + blk.tiles) {
             unit = x;
             row0 += ROWS;
         }
     }
-    if (!began && tid == 0)
-        parts.begun[w].last = -1;
+    if (!goes_on && tid == 0)
+        parts.begun[w] = {0, -1, 0, 0, 0, 0, {0, 0}};
 }
 
 template <int DP, int NW>
@@ -557,7 +574,9 @@ void launch(const AttnArgs &a, const Parts &p, uint32_t shares, hipStream_t st)
         k_attn_tiles<DP, NW, false><<<shares, 64 * NW, 0, st>>>(a, p, shares);
 }
 
-// Rows of a unit: four waves', or (64 < d <= 128) eight waves'.
+// Rows of a unit: four waves' (of eight in pairs for d > 128), or eight waves'.  At
+// d <= 64 two workgroups of four waves fit side by side, so that one's barrier is
+// the other's time to work; beyond, one of eight reads K and V half as often.
 constexpr uint32_t unit_rows(uint32_t d) { return d > 64 && d <= 128 ? 256 : 128; }
 
 // As many workgroups as the chip holds at a time.
@@ -579,7 +598,7 @@ hipError_t launch_attn_tiles(const AttnArgs &a, hipStream_t st)
     else if (a.cache.d <= 128)
         launch<128, 8>(a, p, shares, st);
     else
-        launch<256, 4>(a, p, shares, st);
+        launch<256, 8>(a, p, shares, st);
     count_launch();
     if (hipError_t e = hipGetLastError())
         return e;
