@@ -298,12 +298,15 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tiles(AttnArgs a, Parts par
                     __builtin_amdgcn_raw_ptr_buffer_load_lds(vp, (lds_void *)(vd + to), 16, lane_at[i % 2], 0, 0, 0);
                 }
             }
-            if (FP8 && tid < KT) {
+            if (FP8 && 64 * wave < KT) {
                 // the first waves: a scale of K and of V each, of the keys' rows of the cache
+                // (all lanes take part in the exchange: any may hold the row asked for)
                 const uint64_t row = __shfl(row_at, GROUPS * nth + tid / 16, 64) + lane % 16;
-                const bool hole = gaps >> tid / 16 & 1;
-                ksr = hole ? 0.0f : a.cache.ks[row];
-                vsr = hole ? 0.0f : a.cache.vs[row];
+                if (tid < KT) {
+                    const bool hole = gaps >> tid / 16 & 1;
+                    ksr = hole ? 0.0f : a.cache.ks[row];
+                    vsr = hole ? 0.0f : a.cache.vs[row];
+                }
             }
             return gaps;
         };

@@ -1,0 +1,61 @@
+"""paged_attention where one kernel ends and another begins: rows of a sequence
+(times heads of a kv head) around 16, 32, 64 and 128, for every padded head size
+and both cache forms, over few keys and over so many that they are split; what a
+row does not see, at every head size; and rows joined from few and many parts."""
+import math
+
+import pytest
+import torch
+
+from tests import decoder_ref as ref
+from tests.test_gpu_attention import FORMS, Batch
+
+pytestmark = pytest.mark.gpu
+
+
+@FORMS
+@pytest.mark.parametrize("d", [32, 64, 80, 128, 192, 256])
+@pytest.mark.parametrize("heads,n", [(15, 1), (16, 1), (17, 1), (8, 4), (11, 3), (33, 1), (16, 4), (13, 5), (65, 1), (32, 4),
+                                     (43, 3)])
+def test_around_the_boundaries(heads, n, d, fp8):
+    Batch([(n, 333), (n, n), (max(n - 1, 0), 40)], heads, 1, d, fp8, seed=heads).check()
+    Batch([(n, 5003)], heads, 1, d, fp8, seed=heads).check()
+
+
+@FORMS
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("heads,n", [(1, 1), (3, 1), (8, 1), (5, 4), (60, 1), (8, 50)])
+def test_joins_of_few_and_many_parts(heads, n, d, fp8):
+    Batch([(n, 40000)], heads, 1, d, fp8, page=64, seed=n).check()
+    Batch([(n, 2100 + 700 * (i % 3)) for i in range(60)], heads, 1, d, fp8, page=64, seed=n).check()
+
+
+@FORMS
+@pytest.mark.parametrize("d", [48, 64, 192, 256])
+@pytest.mark.parametrize("heads,n", [(2, 1), (2, 3), (24, 2), (4, 40), (2, 150)])
+def test_what_a_row_does_not_see_at_every_head_size(heads, n, d, fp8):
+    """A NaN in one element of V: it reaches the rows that see its position, in
+    that element alone, and no other row."""
+    b = Batch([(n, n + 37), (n, 2 * n + 3)], heads, 2, d, fp8, seed=n)
+    want = b.check()
+    for element in (0, 1, 15, 16, d // 2 - 1, d // 2, d - 9, d - 1):
+        for back in (0, n // 2):
+            pos = n + 37 - 1 - back
+            at = b.table[0, pos // 16], 1, pos % 16, element
+            kept = b.cache.v[at].clone()
+            b.cache.v[at] = ref.NAN_CODE if fp8 else math.nan
+            out = b.call()
+            hit = torch.zeros_like(out, dtype=torch.bool)
+            hit[n - 1 - back:n, heads // 2:, element] = True
+            assert torch.isnan(out[hit].float()).all(), (element, back)
+            assert torch.equal(out[~hit], want[~hit]), (element, back)
+            b.cache.v[at] = kept
+
+
+@FORMS
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_windows_and_holes_over_split_keys(d, fp8):
+    for heads, n in ((4, 1), (4, 7), (4, 40), (2, 300)):
+        for window in (0, 1500):
+            Batch([(n, 6000), (n, 900 + n)], heads, 2, d, fp8, page=32, window=window, seed=n,
+                  holes=[(0, 0, -1), (0, 130, 1 << 29), (0, 187, -5), (1, 3, -1)]).check()
