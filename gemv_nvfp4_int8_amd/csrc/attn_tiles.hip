@@ -117,6 +117,16 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tiles(AttnArgs a, Parts par
     // Walks all blocks in order, WG sequences and then WG blocks at a time; with
     // `want` below the total, leaves the block that holds that tile in found[]:
     // sequence, first row, the tiles before it.  Returns the tiles walked.
+    uint32_t walks = 0, at_seq = 0, at_row = 0;         // runs of WG blocks; the thread's block of the last run
+    uint64_t at_from = 0, at_to = 0;
+    auto find = [&](uint64_t want) {
+        if (want >= at_from && want < at_to) {
+            found[0] = at_seq;
+            found[1] = at_row;
+            found[2] = (uint32_t)at_from;
+            found[3] = (uint32_t)(at_from >> 32);
+        }
+    };
     auto walk = [&](uint64_t want) {
         uint64_t before = 0;
         for (uint32_t s0 = 0; s0 < a.seqs; s0 += WG) {
@@ -143,13 +153,12 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tiles(AttnArgs a, Parts par
                     tiles = block_of<KT>(a, seq_n[s], seq_len[s], row, ROWS, group).tiles;
                 }
                 uint32_t all;
-                const uint64_t to = before + block_scan(tiles, all), from = to - tiles;
-                if (want >= from && want < to) {
-                    found[0] = s0 + s;
-                    found[1] = row;
-                    found[2] = (uint32_t)from;
-                    found[3] = (uint32_t)(from >> 32);
-                }
+                at_to = before + block_scan(tiles, all);
+                at_from = at_to - tiles;
+                at_seq = s0 + s;
+                at_row = row;
+                ++walks;
+                find(want);
                 before += all;
                 if (want < before)
                     break;
@@ -171,7 +180,12 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tiles(AttnArgs a, Parts par
     uint64_t x = uniform(w * total / shares);
     const uint64_t share_end = uniform((w + 1) * total / shares);
     uint32_t head = uniform((uint32_t)(x / line));
-    walk(x % line);
+    if (walks == 1) {                      // all there is was one run
+        find(x % line);
+        __syncthreads();
+    } else {
+        walk(x % line);
+    }
     uint32_t seq = uniform(found[0]), row0 = uniform(found[1]);
     uint64_t unit = (uint64_t)head * line + uniform((uint64_t)found[3] << 32 | found[2]);
 
