@@ -34,7 +34,9 @@ namespace {
 
 // Keys of a tile: as many as two buffers of them leave room for eight waves a
 // compute unit.  (d = 64 with tiles of 64 and three waves a SIMD: 329 us where this
-// takes 305, 7 prompts of up to 2500 in a window of 1024.)
+// takes 305, 7 prompts of up to 2500 in a window of 1024.  d = 128 with tiles of 128:
+// 2000 rows over 32000 937 for 955, but 32 prompts of 128 45 for 41, 2048 rows over
+// themselves 88 to 93 either way, and E4M3 spills.)
 constexpr uint32_t tile_keys(uint32_t d) { return d <= 64 ? 128 : d <= 128 ? 64 : 32; }
 
 typedef __attribute__((ext_vector_type(4))) short s16x4;
@@ -417,6 +419,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tiles(AttnArgs a, Parts par
             }
             // ---- V: 16 keys' probabilities, then their products with every 32 of d; under
             // these the next 16 keys' probabilities and V's fragments
+            // (this wave before the SIMD's other, whose scores and masks then fill the gaps: 298 -> 289 us
+            // at heads of 64 with a window of 1024, 943 -> 929 at 2000 rows over 32000)
+            __builtin_amdgcn_s_setprio(1);
             float part[4] = {0, 0, 0, 0};
             auto probability = [&](int blk, int i) {
                 const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[blk / 2][8 * (blk % 2) + i], unit_scale, -base));
@@ -459,6 +464,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tiles(AttnArgs a, Parts par
                     pf = pn;
             }
             __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(0);
             l += (part[0] + part[1]) + (part[2] + part[3]);
             if (poisoned) {
                 // NaN and infinities, in whose places V has zeros, for the rows that see them
