@@ -136,14 +136,14 @@ int paged_attention(const uint16_t *q, int kv_format, const void *k_cache, const
     if (int e = check_cache(kv_format, k_cache, v_cache, k_scale, v_scale, kv_heads, d, pages, page_size))
         return e;
     if (!attention_shape(t, seqs, q_heads, kv_heads, d) || table_width == 0 || !fits(seqs, table_width) ||
-        !fits(table_width, page_size))
-        return QP_ERR_SHAPE;
+        (uint64_t)table_width * page_size >= 1u << 27 || (uint64_t)seqs * table_width * page_size >= 1ull << 38)
+        return QP_ERR_SHAPE;               // (tiles of 32 keys or more are counted in 32 bits, 512 blocks at a time)
     if (max_q < 1 || max_q > t || !(scale > 0.0f) || !std::isfinite(scale))
         return QP_ERR_RANGE;
     if (workspace_bytes < qp::paged_attention_work(t, seqs, max_q, q_heads, kv_heads, d))
         return QP_ERR_SCRATCH;
     return done(qp::launch_paged_attention(
-        {q, out, page_table, q_start, kv_len, workspace, scale, window, t, seqs, max_q, q_heads, table_width,
+        {q, out, page_table, q_start, kv_len, workspace, scale, window < 1u << 27 ? window : 0, t, seqs, max_q, q_heads, table_width,
          cache_of(kv_format, k_cache, v_cache, k_scale, v_scale, kv_heads, d, pages, page_size)},
         S(stream)));
 }

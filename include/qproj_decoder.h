@@ -7,7 +7,7 @@
  * The conventions of qproj.h hold (device pointers to dense row-major memory,
  * 16-byte alignment, caller-owned buffers and scratch, no allocation, no
  * synchronisation, work enqueued on `stream`, host-side checks that enqueue
- * nothing).  What the host cannot see (slots, page numbers, lengths, tokens)
+ * nothing).  What a call writes overlaps nothing else that it is given.  What the host cannot see (slots, page numbers, lengths, tokens)
  * is checked on the GPU: a value that fits no buffer is skipped as stated at
  * the operator and never leads outside one.
  */
@@ -113,7 +113,8 @@ int qk_norm_rope_cache(const uint16_t *qkv, const uint16_t *q_norm, const uint16
  * the sizes choose the kernel).
  * Scores, maxima, sums and outputs are F32; the probabilities that the matrix
  * cores multiply with V are rounded to BF16 (their sum is of the unrounded
- * ones).  What the cache holds at a position that a row does not attend to,
+ * ones).  An E4M3 cache's scales of V count as the nearest number of 0 to
+ * 3.4e38 (NaN as 0).  What the cache holds at a position that a row does not attend to,
  * NaN and infinities included, has no influence on that row.  No atomics: the
  * same call gives the same bits; another batch may change a row's last bits.
  * A page number outside 0..pages-1 is a hole: none of its positions is
@@ -124,8 +125,9 @@ int qk_norm_rope_cache(const uint16_t *qkv, const uint16_t *q_norm, const uint16
  * is QP_ERR_SCRATCH), contents before and after unspecified, not shared by
  * calls that may overlap.
  * Refusals: zero extents, q_heads not a multiple of kv_heads, d, page_size,
- * t * q_heads * d, pages * page_size, seqs * table_width or table_width *
- * page_size of 2^31 or more: QP_ERR_SHAPE; max_q outside 1..t, scale not
+ * t * q_heads * d, pages * page_size or seqs * table_width of 2^31 or more,
+ * table_width * page_size of 2^27 or more, seqs * table_width * page_size of
+ * 2^38 or more: QP_ERR_SHAPE; max_q outside 1..t, scale not
  * positive and finite: QP_ERR_RANGE; unknown format: QP_ERR_FORMAT.
  * ---------------------------------------------------------------------- */
 uint64_t paged_attention_workspace(uint32_t t, uint32_t seqs, uint32_t max_q, uint32_t q_heads,
@@ -149,8 +151,10 @@ int paged_attention(const uint16_t *q, int kv_format, const void *k_cache, const
  * with top = 0 the last two are not used; something has to be asked for.
  * A logit of -inf has probability 0 and adds nothing to the entropy; a row of
  * nothing else has logprobs of -inf and entropy 0.  A target outside
- * 0..vocab-1 gives 0.  Sums are F32.  A row that holds NaN or +inf gives
- * unspecified numbers and tokens within 0..vocab-1.
+ * 0..vocab-1 gives 0.  Sums are F32; how many workgroups a row has follows from
+ * rows and vocab, so that a row's last bits may be others in another batch.  The
+ * same call gives the same bits.  A row that holds NaN or +inf gives unspecified
+ * numbers and tokens within 0..vocab-1.
  * workspace: token_logprobs_workspace(rows, vocab, top) bytes (fewer is
  * QP_ERR_SCRATCH), not shared by calls that may overlap.
  * Refusals: rows or vocab 0, rows * vocab >= 2^31: QP_ERR_SHAPE; top above

@@ -118,7 +118,7 @@ def test_rope_refusals():
 def test_attention_refusals():
     assert attn(q_heads=9) == qp.QP_ERR_SHAPE
     for bad in (dict(seqs=0), dict(width=0), dict(t=1 << 22), dict(seqs=1 << 29), dict(width=1 << 27),
-                dict(seqs=0xFFFFFFFF, width=1)):
+                dict(seqs=0xFFFFFFFF, width=1), dict(width=1 << 23), dict(seqs=1 << 13, width=1 << 21)):
         assert attn(**bad) == qp.QP_ERR_SHAPE, bad
     for bad in (dict(max_q=0), dict(max_q=5), dict(scale=0.0), dict(scale=-1.0), dict(scale=NAN), dict(scale=INF)):
         assert attn(**bad) == qp.QP_ERR_RANGE, bad

@@ -59,3 +59,25 @@ def test_windows_and_holes_over_split_keys(d, fp8):
         for window in (0, 1500):
             Batch([(n, 6000), (n, 900 + n)], heads, 2, d, fp8, page=32, window=window, seed=n,
                   holes=[(0, 0, -1), (0, 130, 1 << 29), (0, 187, -5), (1, 3, -1)]).check()
+
+
+@FORMS
+def test_windows_larger_than_any_length(fp8):
+    """The largest windows are the call without one."""
+    for n in (1, 5, 90):
+        b = Batch([(n, 700), (n, 95 + n)], 8, 2, 128, fp8, seed=n)
+        want = b.check().clone()
+        for window in (701, (1 << 27) - 1, 1 << 27, (1 << 31) - 1, 1 << 31, (1 << 32) - 1):
+            b.window = window
+            assert torch.equal(b.call(), want), window
+
+
+@FORMS
+def test_rows_of_another_sequence_and_shared_pages(fp8):
+    """Sequences that share a prefix's pages read the same keys."""
+    b = Batch([(1, 640), (3, 643), (70, 710), (1, 640)], 8, 2, 128, fp8, page=64, seed=3)
+    pages = b.table[0, :10].clone()
+    for i in (1, 2, 3):
+        b.table[i, :10] = pages
+        b.k[i][:640], b.v[i][:640] = b.k[0], b.v[0]
+    b.check()
