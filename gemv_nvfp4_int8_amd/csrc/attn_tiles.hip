@@ -24,7 +24,11 @@
 //
 // What bounds it: at two waves a SIMD, the softmax's vector work beside the matrix
 // operations (an exponential takes 8 cycles of a wave, a product of 32x32x16 32), and
-// the LDS reads, which 32 rows a wave just balance with the matrix operations.
+// the LDS reads, which 32 rows a wave just balance with the matrix operations; with
+// heads of 128 and long keys also the part's power (1.84 GHz under 2000 rows over
+// 32000).  Measured, 32 heads of 128 over 8: 8192 rows over themselves 660 us, 830
+// TFLOP/s; 2000 rows over 32000 0.95 ms, 1.07 PFLOP/s; 64 heads of 64, 7 prompts of up
+// to 2500 in a window of 1024: 295 us, 470 TFLOP/s of what is seen.
 #include "attn_common.hpp"
 #include "qp_launch.hpp"
 

@@ -6,13 +6,19 @@
 // H = ln s - ln 2 * t / s.
 // The most probable tokens cost the pass nothing: its 256 lanes' maxima are there
 // at its end, and what the n-th largest of them is, at least n elements reach.
-// The lanes that reach it (n of them, but for ties) have their elements looked
-// through again, n / 256 of the row; those that reach the bound, little more than
-// n, go to LDS as 64-bit keys (value, then the lower token), where each counts the
-// larger ones: its place.  Where more reach it than there is room for (many equal
+// A lane keeps a maximum for each of its four loads of a piece as well: those that
+// reach the bound (n, and few more) have their elements looked through again, about
+// n / 1024 of the row, though in whole lines of 128 bytes n / 128; the elements that
+// reach it, little more than n, go to LDS as 64-bit keys (value, then the lower
+// token), where each counts the larger ones: its place.  Where more reach it than there is room for (many equal
 // logits), all elements go through a list in a register, one lane a place.
 // Rows are a workgroup's each; those of a last round that would leave much of the
 // chip empty are split, and a second launch joins their parts.
+//
+// Bound by HBM when large: 2048 rows of 152064 in BF16, the 8 best, take 121 us, 5.1
+// TB/s (126 us where the maxima are a lane's alone, and its four loads of a piece are
+// looked through: a fifth more bytes).  Small calls are two launches and their trips
+// to memory: 12 us for one such row, 11 for 16 rows of 129281 in F32.
 #include "qp_device.hpp"
 #include "qp_launch.hpp"
 #include "decoder.hpp"
@@ -77,6 +83,7 @@ constexpr uint32_t BATCH = 16;
 struct Bench {
     uint64_t in[ROOM + BATCH], out[64];
     uint32_t n;                            // keys that reached it: more than ROOM are not all there
+    uint32_t loads;                        // entries of the list of loads to look through
 };
 
 __device__ __forceinline__ void collect(Bench &bench, uint64_t key)
@@ -280,18 +287,19 @@ struct Part {
 };
 
 // The whole workgroup: the `top` largest elements of its part, in order, to
-// bench.out (0 behind them, where there are fewer).  m: the lane's maximum.
+// bench.out (0 behind them, where there are fewer).  m: the lane's maxima, by load.
 template <bool F32>
-__device__ __forceinline__ void largest(const LogprobArgs &a, const Part<F32> &p, float m, float *lane_max, uint64_t *keys,
-                                        Bench &bench, uint32_t lane, uint32_t wave)
+__device__ __forceinline__ void largest(const LogprobArgs &a, const Part<F32> &p, const float *m, float *lane_max,
+                                        uint16_t *loads, uint64_t *keys, Bench &bench, uint32_t lane, uint32_t wave)
 {
     constexpr uint32_t V = Part<F32>::V, PIECE = Part<F32>::PIECE;
     const uint32_t tid = threadIdx.x;
-    lane_max[tid] = m;
+    static_assert(NV == 4, "the maximum of four");
+    lane_max[tid] = __builtin_fmaxf(__builtin_fmaxf(m[0], m[1]), __builtin_fmaxf(m[2], m[3]));
     if (tid < 64)
         bench.out[tid] = 0;
     if (tid == 0)
-        bench.n = 0;
+        bench.n = bench.loads = 0;
     __syncthreads();
     // the largest value with 16 zeros behind it that `top` lanes' maxima reach
     uint32_t u[WAVES], bound = 0;
@@ -311,23 +319,30 @@ __device__ __forceinline__ void largest(const LogprobArgs &a, const Part<F32> &p
     // more are looked for, and then the first tokens that are not
     const bool rest = bound <= ordered(-INFINITY);
     const uint32_t reach = rest ? ordered(-INFINITY) + 1 : bound;
-    uint32_t lanes = 0, before = 0;        // lanes that reach it; those before this wave's
-    uint64_t who = 0;
+    // the loads that reach it (in any order: the elements are put in theirs)
+    uint64_t who[NV];
+    uint32_t mine = 0;
 #pragma unroll
-    for (uint32_t w = 0; w < WAVES; ++w) {
-        const uint64_t mask = __ballot(u[w] >= reach);
-        before += w < wave ? __popcll(mask) : 0;
-        lanes += __popcll(mask);
-        who = w == wave ? mask : who;
+    for (int v = 0; v < NV; ++v) {
+        who[v] = __ballot(ordered(m[v]) >= reach);
+        mine += __popcll(who[v]);
     }
-    __syncthreads();                       // lane_max has been read; now it lists those lanes
-    if (who >> lane & 1)
-        ((uint32_t *)lane_max)[before + __popcll(who & ((1ull << lane) - 1))] = tid;
+    uint32_t to = 0;
+    if (lane == 0 && mine != 0)
+        to = atomicAdd(&bench.loads, mine);
+    to = __builtin_amdgcn_readfirstlane(to);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        if (who[v] >> lane & 1)
+            loads[to + __popcll(who[v] & ((1ull << lane) - 1))] = (uint16_t)(tid * NV + v);
+        to += __popcll(who[v]);
+    }
     __syncthreads();
+    const uint32_t some = bench.loads;
     const uint32_t pieces = (p.end - p.first + p.stride - 1) / p.stride;    // of the first wave; p.first < p.end
-    for (uint32_t i = tid; i < lanes * pieces * NV; i += WG) {
-        const uint32_t t = ((const uint32_t *)lane_max)[i % lanes], v = i / lanes % NV, nth = i / lanes / NV;
-        const uint32_t at = p.first + PIECE * (t / 64) + nth * p.stride + (64 * v + t % 64) * V;
+    for (uint32_t i = tid; i < some * pieces; i += WG) {
+        const uint32_t t = loads[i % some] / NV, v = loads[i % some] % NV;
+        const uint32_t at = p.first + PIECE * (t / 64) + i / some * p.stride + (64 * v + t % 64) * V;
         if (at >= p.end)
             continue;
         float x[V];
@@ -394,6 +409,7 @@ __global__ __launch_bounds__(WG, RESIDENT) void k_logprobs(LogprobArgs a, uint32
     constexpr uint32_t V = Part<F32>::V, PIECE = Part<F32>::PIECE;
     __shared__ Sums sums[WAVES];
     __shared__ float lane_max[WG];
+    __shared__ uint16_t loads[WG * NV];
     __shared__ uint64_t keys[WAVES * 32];
     __shared__ Bench bench;
     const bool alone = blockIdx.x < whole;
@@ -415,7 +431,10 @@ __global__ __launch_bounds__(WG, RESIDENT) void k_logprobs(LogprobArgs a, uint32
     Target given = {false, 0.0f};
     if (parts == 1 && wave == 0)
         given = target_of<F32>(a, row);
-    float m = -INFINITY, s = 0.0f, t = 0.0f;
+    float m = -INFINITY, s = 0.0f, t = 0.0f, most_of[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+        most_of[v] = -INFINITY;
     uint32_t pos = p.first + PIECE * wave;
     if (pos < p.end)
         load(pos);
@@ -426,7 +445,8 @@ __global__ __launch_bounds__(WG, RESIDENT) void k_logprobs(LogprobArgs a, uint32
             values<F32>(raw[v], x[v]);
 #pragma unroll
             for (uint32_t j = 0; j < V; ++j)
-                top = __builtin_fmaxf(top, x[v][j]);
+                most_of[v] = __builtin_fmaxf(most_of[v], x[v][j]);
+            top = __builtin_fmaxf(top, most_of[v]);
         }
         if (pos + p.stride < p.end)
             load(pos + p.stride);
@@ -464,7 +484,7 @@ __global__ __launch_bounds__(WG, RESIDENT) void k_logprobs(LogprobArgs a, uint32
 
     const float most = wave_max(m);
     if (a.top != 0)
-        largest<F32>(a, p, m, lane_max, keys, bench, lane, wave);
+        largest<F32>(a, p, most_of, lane_max, loads, keys, bench, lane, wave);
     fade_to(most, m, s, t);
     s = sum_over_wave(s);
     t = sum_over_wave(t);
