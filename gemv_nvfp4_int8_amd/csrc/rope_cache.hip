@@ -4,12 +4,14 @@
 // A head is taken by G lanes (8, 16 or 32: the next power of two of d/8), 16
 // bytes each, so that its sum of squares and its largest magnitude are a few
 // cross-lane steps.  A lane's partners of the half layout lie rot/2 further on or
-// back, in another lane's 16 bytes, and are loaded once more (from L1).  Cosines
+// back, in another lane's 16 bytes, and come from that lane when they are normed
+// (8192 tokens of 32 + 2 * 8 heads of 128: 33 us; loaded and normed once more, 41:
+// the vector instructions bound it then).  Cosines
 // and sines are the same for all heads of a token: one thread a pair computes them
 // into LDS while the heads' loads are on their way; what is not turned has the
 // angle 0 there, so that all lanes do the same.
 //
-// Bound by HBM when large: 8192 tokens of 32 + 2 * 8 heads of 128 take 41 us, 4.9 TB/s
+// Bound by HBM when large: 8192 tokens of 32 + 2 * 8 heads of 128 take 33 us, 6.1 TB/s
 // read and written; 2047 of 40 + 2 * 4 with an E4M3 cache 9.7 us (5.0 TB/s).  A single
 // token takes 4 us: a launch, one trip to memory, the sums across lanes.
 #include <type_traits>
@@ -26,8 +28,11 @@ constexpr uint32_t MAX_TOKENS = 8;         // of a workgroup
 constexpr uint32_t MAX_HALF = 128;
 
 // How pairs lie: 8 partners in one lane's 16 bytes (rot/2 a multiple of 8), in the
-// same lane, or anywhere.
-enum Layout { HALF, PAIRS, HALF_ANY };
+// same lane, anywhere, or (rot = d = 64 or 128) in the lane G/2 further on or back,
+// from which data-parallel moves bring them (d = 128, E4M3: 33.5 us where the general
+// exchange through LDS' crossbar takes 35.2; at d = 256, where such a move would cross
+// rows of 16 lanes, nothing is gained).
+enum Layout { HALF, PAIRS, HALF_ANY, FULL };
 
 // All lanes of G: op over their values, within 16 lanes by data-parallel moves.
 template <int G, typename Op>
@@ -44,6 +49,19 @@ __device__ __forceinline__ float over_group(float v, Op op)
     if (G >= 32)
         v = op(v, __shfl_xor(v, 16, WAVE));
     return v;
+}
+
+// The value of the lane G/2 further on or back in the group.
+template <int G>
+__device__ __forceinline__ float across(float x)
+{
+    auto moved = [](float x, auto ctrl) {
+        return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, false));
+    };
+    if constexpr (G == 8)                  // 7 - lane, then that of 4 turned round
+        return moved(moved(x, std::integral_constant<int, 0x141>()), std::integral_constant<int, 0x1B>());
+    else
+        return moved(x, std::integral_constant<int, 0x128>());          // turned by 8, of 16
 }
 
 __device__ __forceinline__ void unpack(u32x4 w, float *x)
@@ -79,20 +97,17 @@ __global__ __launch_bounds__(WG) void k_qk_norm_rope(RopeArgs a, uint32_t tokens
     // where the lane's angles are, and its partners
     const bool turned = live && c0 < a.rot;
     const uint32_t angle = L == PAIRS ? c0 / 2 : !turned ? MAX_HALF : c0 < half ? c0 : c0 - half;
-    const uint32_t other = c0 < half ? c0 + half : c0 - half;
+    const uint32_t from = threadIdx.x % WAVE / G * G + (turned ? c0 < half ? c0 + half : c0 - half : c0) / 8;
 
-    u32x4 own[U], partner[U];
+    u32x4 own[U];
     auto load = [&](uint32_t h) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            own[u] = partner[u] = (u32x4){0, 0, 0, 0};
+            own[u] = (u32x4){0, 0, 0, 0};
             const uint32_t head = h + u * NG;
             if (head >= heads || nth >= nt || !live)
                 continue;
-            const uint16_t *x = a.qkv + ((size_t)tok * heads + head) * d;
-            own[u] = *(const u32x4 *)(x + c0);
-            if (L == HALF && turned && head < heads - kv)
-                partner[u] = *(const u32x4 *)(x + other);
+            own[u] = *(const u32x4 *)(a.qkv + ((size_t)tok * heads + head) * d + c0);
         }
     };
     load(h0);
@@ -126,7 +141,7 @@ __global__ __launch_bounds__(WG) void k_qk_norm_rope(RopeArgs a, uint32_t tokens
             c[j + 1] = v[2];
             s[j + 1] = v[3];
         }
-        if (L == HALF && c0 < half) {
+        if ((L == HALF || L == FULL) && c0 < half) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 s[j] = -s[j];
@@ -170,21 +185,16 @@ __global__ __launch_bounds__(WG) void k_qk_norm_rope(RopeArgs a, uint32_t tokens
                         x[j] = __builtin_fmaf(lo, c[j / 2], -(hi * s[j / 2]));
                         x[j + 1] = __builtin_fmaf(hi, c[j / 2], lo * s[j / 2]);
                     }
-                } else if constexpr (L == HALF) {
-                    unpack(partner[u], y);
-                    if (w) {
-                        u32x4 g = {0, 0, 0, 0};
-                        if (turned)
-                            g = *(const u32x4 *)(w + other);
-                        float z[8];
-                        unpack(g, z);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            y[j] = y[j] * rstd * z[j];
-                    }
+                } else if constexpr (L == FULL) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        x[j] = __builtin_fmaf(x[j], c[j], y[j] * s[j]);
+                        x[j] = __builtin_fmaf(x[j], c[j], across<G>(x[j]) * s[j]);
+                } else if constexpr (L == HALF) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float z = __shfl(x[j], from, WAVE);
+                        x[j] = __builtin_fmaf(x[j], c[j], (turned ? z : 0.0f) * s[j]);
+                    }
                 } else if (turned) {
                     const uint16_t *raw = a.qkv + ((size_t)tok * heads + head) * d;
 #pragma unroll
@@ -251,6 +261,8 @@ void launch(const RopeArgs &a, hipStream_t st)
 {
     if (a.interleaved)
         launch_layout<G, PAIRS>(a, st);
+    else if (G <= 16 && a.rot == 8 * G && a.cache.d == 8 * G)
+        launch_layout<(G < 16 ? G : 16), FULL>(a, st);
     else if (a.rot % 16 == 0)
         launch_layout<G, HALF>(a, st);
     else
