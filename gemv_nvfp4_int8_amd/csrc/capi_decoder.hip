@@ -44,6 +44,12 @@ bool attention_shape(uint32_t t, uint32_t seqs, uint32_t q_heads, uint32_t kv_he
            fits((uint64_t)t * q_heads, d) && seqs <= MAX_ELEMS - 1;
 }
 
+// (a launch has a workgroup of 256 a row, and holds fewer than 2^32 threads)
+bool logits_shape(uint32_t rows, uint32_t vocab)
+{
+    return rows != 0 && vocab != 0 && rows < 1u << 24 && fits(rows, vocab);
+}
+
 } // namespace
 
 extern "C" {
@@ -150,7 +156,7 @@ int paged_attention(const uint16_t *q, int kv_format, const void *k_cache, const
 
 uint64_t token_logprobs_workspace(uint32_t rows, uint32_t vocab, uint32_t top)
 {
-    if (rows == 0 || vocab == 0 || !fits(rows, vocab) || top > QP_LOGPROBS_MAX_TOP || top > vocab)
+    if (!logits_shape(rows, vocab) || top > QP_LOGPROBS_MAX_TOP || top > vocab)
         return 0;
     return qp::token_logprobs_work(rows, vocab, top);
 }
@@ -169,7 +175,7 @@ int token_logprobs(const void *logits, int logits_format, const int32_t *targets
         return QP_ERR_ALIGN;
     if (logits_format != QP_LOGITS_BF16 && logits_format != QP_LOGITS_F32)
         return QP_ERR_FORMAT;
-    if (rows == 0 || vocab == 0 || !fits(rows, vocab))
+    if (!logits_shape(rows, vocab))
         return QP_ERR_SHAPE;
     if (top > QP_LOGPROBS_MAX_TOP || top > vocab)
         return QP_ERR_RANGE;

@@ -157,8 +157,9 @@ int paged_attention(const uint16_t *q, int kv_format, const void *k_cache, const
  * numbers and tokens within 0..vocab-1.
  * workspace: token_logprobs_workspace(rows, vocab, top) bytes (fewer is
  * QP_ERR_SCRATCH), not shared by calls that may overlap.
- * Refusals: rows or vocab 0, rows * vocab >= 2^31: QP_ERR_SHAPE; top above
- * QP_LOGPROBS_MAX_TOP or vocab: QP_ERR_RANGE; unknown format: QP_ERR_FORMAT.
+ * Refusals: rows or vocab 0, rows >= 2^24, rows * vocab >= 2^31: QP_ERR_SHAPE;
+ * top above QP_LOGPROBS_MAX_TOP or vocab: QP_ERR_RANGE; unknown format:
+ * QP_ERR_FORMAT.
  * ---------------------------------------------------------------------- */
 enum qp_logits_format { QP_LOGITS_BF16 = 0, QP_LOGITS_F32 = 1 };
 #define QP_LOGPROBS_MAX_TOP 32

@@ -128,7 +128,7 @@ def test_attention_refusals():
 
 
 def test_logits_refusals():
-    for bad in (dict(rows=0), dict(vocab=0), dict(rows=1 << 16, vocab=1 << 15)):
+    for bad in (dict(rows=0), dict(vocab=0), dict(rows=1 << 16, vocab=1 << 15), dict(rows=1 << 24, vocab=4)):
         assert logp(**bad) == qp.QP_ERR_SHAPE, bad
     for bad in (dict(top=33), dict(top=101), dict(vocab=2)):
         assert logp(**bad) == qp.QP_ERR_RANGE, bad

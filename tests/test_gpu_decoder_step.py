@@ -261,3 +261,70 @@ def test_ties_in_rows_that_are_not_split(dtype):
     qp.token_logprobs(x, torch.zeros(rows, dtype=I32, device=DEV), *found, work)
     first = torch.where(torch.arange(rows, device=DEV) % 2 == 1, 1000, 0)
     assert torch.equal(found[2], (first[:, None] + torch.arange(top, device=DEV)).to(I32))
+
+
+# ------------------------------------------------------------------ the largest calls
+def test_the_most_rows_of_logits():
+    rows, vocab = (1 << 24) - 1, 3
+    x = torch.empty((rows, vocab), dtype=BF16, device=DEV).normal_(generator=gen(1))
+    targets = torch.randint(0, 3, (rows,), generator=gen(2), device=DEV, dtype=I32)
+    found = (torch.full((rows,), 9.0, device=DEV), torch.full((rows,), 9.0, device=DEV),
+             torch.full((rows, 2), 9, dtype=I32, device=DEV), torch.full((rows, 2), 9.0, device=DEV))
+    work = torch.empty(qp.token_logprobs_workspace(rows, vocab, 2), dtype=U8, device=DEV)
+    qp.token_logprobs(x, targets, *found, work)
+    for at in range(0, rows, 1 << 22):
+        want, _, order, best, rel = ref.logprobs(x[at:at + (1 << 22)], targets[at:at + (1 << 22)], 2)
+        got = [f[at:at + (1 << 22)] for f in found]
+        assert torch.equal(got[2].long(), order)
+        ref.assert_logprobs(got[0][:, None], want[:, None], rel)
+        ref.assert_logprobs(got[3], best, rel)
+
+
+def test_the_most_tokens_of_heads():
+    """Nearly 2^31 elements of 17 heads of 16; a token's outputs depend on it alone."""
+    heads, d = 15, 16
+    t = ((1 << 31) - 1) // ((heads + 2) * d)
+    qkv = torch.empty((t, (heads + 2) * d), dtype=BF16, device=DEV)
+    for at in range(0, t, 1 << 20):
+        qkv[at:at + (1 << 20)].normal_(generator=gen(at))
+    some = torch.tensor([0, 1, 4097, t // 2, t - 2, t - 1], device=DEV)
+    positions = torch.arange(t, dtype=I32, device=DEV)
+    slots = torch.full((t,), -1, dtype=I32, device=DEV)
+    slots[some] = torch.arange(1, 7, dtype=I32, device=DEV)
+    inv_freq = qp.rope_inv_freq(d, 10000.0).to(DEV)
+    out = []
+    for rows in (slice(None), some):
+        cache = Cache(1, 1, 16, d, False)
+        q = torch.full((len(positions[rows]), heads, d), -3.0, dtype=BF16, device=DEV)
+        qp.qk_norm_rope_cache(qkv[rows], None, None, 1e-6, positions[rows], inv_freq, 1.0, qp.QP_ROPE_HALF, slots[rows],
+                              qp.KVCache(cache.k, cache.v), q)
+        out.append([q[some] if isinstance(rows, slice) else q, cache.k, cache.v])
+    assert same(*out)
+    assert not torch.isnan(out[0][1][0, 0, 1:7].float()).any() and torch.isnan(out[0][1][0, 0, 7:].float()).all()
+
+
+def test_the_most_sequences():
+    """Nearly 2^31 elements of queries, a token each of a million sequences."""
+    seqs, heads, kv, d = (1 << 20) - 1, 128, 8, 16
+    g = gen(4)
+    cache = Cache(40, kv, 16, d, False)
+    slots = torch.arange(640, device=DEV)
+    cache.put("k", slots, normal(g, 640, kv, d))
+    cache.put("v", slots, normal(g, 640, kv, d))
+    q = torch.empty((seqs, heads, d), dtype=BF16, device=DEV)
+    for at in range(0, seqs, 1 << 17):
+        q[at:at + (1 << 17)].normal_(generator=gen(at))
+    table = torch.randint(0, 40, (seqs, 1), generator=g, device=DEV, dtype=I32)
+    kv_len = torch.randint(0, 17, (seqs,), generator=g, device=DEV, dtype=I32)
+    q_start = torch.arange(seqs + 1, dtype=I32, device=DEV)
+    out = torch.full_like(q, -3.0)
+    work = torch.empty(qp.paged_attention_workspace(seqs, seqs, 1, heads, kv, d), dtype=U8, device=DEV)
+    qp.paged_attention(q, qp.KVCache(cache.k, cache.v), table, q_start, kv_len, 1, 0.25, 0, work, out)
+    torch.cuda.synchronize()
+    for at in range(0, seqs, 1 << 17):
+        assert not (out[at:at + (1 << 17)] == -3.0).all(dim=(1, 2)).any()
+    for s in (0, 1, 255, 256, 70001, seqs // 2, seqs - 257, seqs - 2, seqs - 1):
+        n = int(kv_len[s])
+        at = int(table[s]) * 16 + torch.arange(n, device=DEV)
+        want, tol = ref.attention(q[s:s + 1], cache.get("k", at), cache.get("v", at), ref.visible(1, n, 0), 0.25)
+        ref.assert_rounded(out[s:s + 1], want, tol)
