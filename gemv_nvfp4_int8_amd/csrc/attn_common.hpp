@@ -54,12 +54,6 @@ inline Parts parts_at(void *work, uint64_t shares, uint64_t rows)
     return r;
 }
 
-// A value of a read-only array at an index that is the same in the whole wave.
-__device__ __forceinline__ int32_t uniform_load(const int32_t *p, size_t i)
-{
-    return ((const __attribute__((address_space(4))) int32_t *)p)[i];
-}
-
 // A value that is the same in the whole wave, in scalars.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ uint64_t uniform(uint64_t v)
@@ -139,8 +133,7 @@ __device__ __forceinline__ uint32_t share_of(uint64_t x, uint64_t n, uint64_t sh
     return (uint32_t)(((x + 1) * shares - 1) / n);
 }
 
-// Joins the parts of the units that were begun in one share and finished in
-// others (attn_decode.hip); `rows` of a part, of which `live` at most are used.
+// Joins the parts of the units that several shares have (attn_decode.hip); `rows` of a part, of which `live` at most are used.
 hipError_t launch_attn_join(const AttnArgs &a, const Parts &p, uint32_t shares, uint32_t rows, uint32_t live,
                             hipStream_t st);
 

@@ -206,7 +206,6 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
         const int last_pos = q.len - q.n + (int)((row0 + max(rows, 1) - 1) / group);
         const int all_from = a.window ? last_pos + 1 - (int64_t)a.window : 0;              // from here every row sees ...
         const int all_to = q.len - q.n + (int)(row0 / group) + 1;                          // ... up to here (exclusive)
-        const uint32_t page_elems = (kv * d) << pl, head_elems = (head * d) << pl;         // of one page: below 2^31
         const int32_t *table = a.table + (size_t)seq * a.width;
         const uint32_t mask = (1u << pl) - 1;
 
@@ -664,10 +663,13 @@ uint32_t blocks_of(uint32_t rows, uint32_t d)
 template <int DP>
 void launch(const AttnArgs &a, const Parts &p, uint32_t rows, uint32_t shares, hipStream_t st)
 {
-    if (room(rows, DP) == 16)
-        launch_rows<DP, 1>(a, p, shares, blocks_of(rows, DP), st);
-    else
-        launch_rows<DP == 256 ? 64 : DP, DP == 256 ? 1 : 2>(a, p, shares, blocks_of(rows, DP), st);
+    if constexpr (DP <= 128) {
+        if (room(rows, DP) == 32) {
+            launch_rows<DP, 2>(a, p, shares, blocks_of(rows, DP), st);
+            return;
+        }
+    }
+    launch_rows<DP, 1>(a, p, shares, blocks_of(rows, DP), st);
 }
 
 } // namespace

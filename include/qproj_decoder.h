@@ -27,8 +27,9 @@ extern "C" {
  *                  of the F32 value by it, round to nearest even, a zero row
  *                  as scale 0 and +0 codes).
  * page_size is a power of two from 16 to 4096, d a multiple of 16 up to 256,
- * pages * page_size < 2^31, a page (kv_heads * page_size * d) below 2^31
- * elements; K and V as a whole may be larger than that. */
+ * kv_heads at most 65535, pages * page_size < 2^31, a page (kv_heads *
+ * page_size * d) below 2^31 elements; K and V as a whole may be larger than
+ * that. */
 enum qp_kv_format { QP_KV_BF16 = 0, QP_KV_FP8_ROW = 1 };
 
 /* Which entries of a head one rotation turns: i and i + rot/2, or 2i and 2i+1. */
