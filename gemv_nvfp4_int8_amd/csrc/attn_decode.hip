@@ -167,12 +167,14 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
 
     bool goes_on = false;
     while (x < share_end) {
+        if (x < seq_tile)
+            break;                         // not reached unless the lengths change under the call
         const Seq q = read_seq_uniform(a, seq);
         const uint32_t tiles = tiles_of(q);
         if (tiles == 0 || x >= seq_tile + (uint64_t)tiles * kv) {
             seq_tile += (uint64_t)tiles * kv;
             if (++seq == a.seqs)
-                break;                     // not reached unless the lengths change under the call
+                break;                     // nor this
             continue;
         }
         const uint32_t head = uniform((uint32_t)((x - seq_tile) / tiles));

@@ -192,7 +192,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tiles(AttnArgs a, Parts par
     } else {
         walk(x % line);
     }
-    uint32_t seq = uniform(found[0]), row0 = uniform(found[1]);
+    uint32_t seq = min(uniform(found[0]), a.seqs - 1), row0 = uniform(found[1]);
     uint64_t unit = (uint64_t)head * line + uniform((uint64_t)found[3] << 32 | found[2]);
 
     const float scale = a.scale * LOG2E;
