@@ -28,7 +28,7 @@
 // heads of 128 and long keys also the part's power (1.84 GHz under 2000 rows over
 // 32000).  Measured, 32 heads of 128 over 8: 8192 rows over themselves 660 us, 830
 // TFLOP/s; 2000 rows over 32000 0.95 ms, 1.07 PFLOP/s; 64 heads of 64, 7 prompts of up
-// to 2500 in a window of 1024: 295 us, 470 TFLOP/s of what is seen.
+// to 2500 in a window of 1024: 276 us, 500 TFLOP/s of what is seen.
 #include "attn_common.hpp"
 #include "qp_launch.hpp"
 
@@ -601,28 +601,39 @@ void launch(const AttnArgs &a, const Parts &p, uint32_t shares, hipStream_t st)
         k_attn_tiles<DP, NW, false><<<shares, 64 * NW, 0, st>>>(a, p, shares);
 }
 
-// Rows of a unit: four waves' (of eight in pairs for d > 128), or eight waves'.  At
-// d <= 64 two workgroups of four waves fit side by side, so that one's barrier is
-// the other's time to work; beyond, one of eight reads K and V half as often.
-constexpr uint32_t unit_rows(uint32_t d) { return d > 64 && d <= 128 ? 256 : 128; }
+// Waves of a workgroup.  Eight read K and V half as often as four; at d <= 64 two
+// workgroups of four fit side by side, so that one's start and barriers are the
+// other's time to work, which counts where units are short.  Measured there, four
+// waves and eight, 64 heads on 8, us: 32 prompts of 128 40 and 51; 8 of 512 80 and
+// 73, 1 of 4096 280 and 275, 7 of up to 2500 in a window of 1024 318 and 304.
+uint32_t waves_of(uint32_t d, uint32_t max_q) { return d <= 64 && max_q <= 256 ? 4 : 8; }
+
+// Rows of a unit (two waves share them for d > 128).
+uint32_t unit_rows(uint32_t d, uint32_t max_q) { return 32 * waves_of(d, max_q) / (d <= 128 ? 1 : 2); }
 
 // As many workgroups as the chip holds at a time.
-uint32_t max_shares(uint32_t d) { return (d <= 64 ? 2 : 1) * (cu_count() ? cu_count() : 256); }
+uint32_t max_shares(uint32_t d, uint32_t max_q)
+{
+    return 8 / waves_of(d, max_q) * (cu_count() ? cu_count() : 256);
+}
 
 } // namespace
 
 uint64_t tiles_work(uint32_t d)
 {
-    return parts_bytes(max_shares(d), unit_rows(d), d);
+    // enough for any max_q: what serves a large one serves a smaller
+    return max(parts_bytes(max_shares(d, 1), unit_rows(d, 1), d), parts_bytes(max_shares(d, ~0u), unit_rows(d, ~0u), d));
 }
 
 hipError_t launch_attn_tiles(const AttnArgs &a, hipStream_t st)
 {
-    const uint32_t shares = max_shares(a.cache.d), rows = unit_rows(a.cache.d);
+    const uint32_t d = a.cache.d, shares = max_shares(d, a.max_q), rows = unit_rows(d, a.max_q);
     const Parts p = parts_at(a.work, shares, rows);
-    if (a.cache.d <= 64)
+    if (waves_of(d, a.max_q) == 4)
         launch<64, 4>(a, p, shares, st);
-    else if (a.cache.d <= 128)
+    else if (d <= 64)
+        launch<64, 8>(a, p, shares, st);
+    else if (d <= 128)
         launch<128, 8>(a, p, shares, st);
     else
         launch<256, 8>(a, p, shares, st);

@@ -123,7 +123,7 @@ int qk_norm_rope_cache(const uint16_t *qkv, const uint16_t *q_norm, const uint16
  * past t, more than max_q rows, kv_len below 0 or past table_width *
  * page_size) is left out: its rows are left as they were.
  * workspace: caller-owned scratch of paged_attention_workspace(...) bytes (fewer
- * is QP_ERR_SCRATCH), contents before and after unspecified, not shared by
+ * is QP_ERR_SCRATCH; enough for a max_q is enough for a smaller one), contents before and after unspecified, not shared by
  * calls that may overlap.
  * Refusals: zero extents, q_heads not a multiple of kv_heads, d, page_size,
  * t * q_heads * d, pages * page_size or seqs * table_width of 2^31 or more,

@@ -145,6 +145,15 @@ def test_workspaces_stay_modest():
         assert 0 < qp.token_logprobs_workspace(*args) <= 1 << 26, args
 
 
+def test_a_workspace_serves_smaller_calls():
+    """What is enough for the most rows of a sequence is enough for fewer."""
+    for d in (16, 64, 80, 128, 192, 256):
+        for heads, kv in ((8, 8), (8, 2), (40, 4), (64, 1)):
+            need = [qp.paged_attention_workspace(8192, 4, n, heads, kv, d) for n in
+                    (1, 2, 3, 4, 5, 8, 9, 16, 17, 32, 33, 64, 65, 100, 255, 256, 257, 1000, 8192)]
+            assert all(a <= b for a, b in zip(need, need[1:])), (d, heads, kv)
+
+
 def test_binding_refuses_tensors_that_do_not_fit():
     k = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="device"):

@@ -81,3 +81,12 @@ def test_rows_of_another_sequence_and_shared_pages(fp8):
         b.table[i, :10] = pages
         b.k[i][:640], b.v[i][:640] = b.k[0], b.v[0]
     b.check()
+
+
+@FORMS
+@pytest.mark.parametrize("d", [32, 64])
+@pytest.mark.parametrize("n", [255, 256, 257, 700])
+def test_small_heads_in_units_of_either_size(n, d, fp8):
+    for window in (0, 150):
+        Batch([(n, n), (3, 90), (n - 9, 2 * n), (1, 1), (64, 3000)], 8, 2, d, fp8, window=window, seed=n).check()
+        Batch([(n, 2 * n)], 14, 2, d, fp8, window=window, seed=n, holes=[(0, 3, -1), (0, 20, 1 << 30)]).check()
