@@ -4,6 +4,12 @@
 // Each lane keeps a running maximum m, the sum s of e = 2^y with y = (x - m)
 // log2(e), and the sum t of e y, which is what the entropy needs:
 // H = ln s - ln 2 * t / s.
+// One step a logit gives y' = x log2(e) + F32's -m log2(e), which is rounded by up to
+// half a unit in its last place: by little at ordinary logits, by 0.06 at a million,
+// by more than F32's exponents at masks of -1e10.  y - y' is the same for all x, and
+// one FMA has it exactly (`low`): it counts where sums move to another maximum, and
+// at the end they are brought to y.  Where it could pass 1, from 2^24 on, the maximum
+// is subtracted first, at two steps a logit.
 // The most probable tokens cost the pass nothing: its 256 lanes' maxima are there
 // at its end, and what the n-th largest of them is, at least n elements reach.
 // A lane keeps a maximum for each of its four loads of a piece as well: those that
@@ -15,10 +21,11 @@
 // Rows are a workgroup's each; those of a last round that would leave much of the
 // chip empty are split, and a second launch joins their parts.
 //
-// Bound by HBM when large: 2048 rows of 152064 in BF16, the 8 best, take 121 us, 5.1
-// TB/s (126 us where the maxima are a lane's alone, and its four loads of a piece are
-// looked through: a fifth more bytes).  Small calls are two launches and their trips
-// to memory: 12 us for one such row, 11 for 16 rows of 129281 in F32.
+// Bound by HBM when large: 2048 rows of 152064 in BF16, the 8 best, take 122 us, 5.1
+// TB/s (5 us more where the maxima are a lane's alone, and its four loads of a piece
+// are looked through: a fifth more bytes; 2 less without what `low` costs).  Small
+// calls are two launches and their trips to memory: 12 us for one such row, 11 for 16
+// rows of 129281 in F32.
 #include "qp_device.hpp"
 #include "qp_launch.hpp"
 #include "decoder.hpp"
@@ -120,15 +127,20 @@ __device__ __forceinline__ void in_order(Bench &bench, uint32_t n, uint32_t top,
     }
 }
 
-// Adds (m, s, t) of another part to this one: what was summed under the lower maximum fades.
-__device__ __forceinline__ void fade_to(float to, float m, float &s, float &t)
+// -m log2(e) less F32's of it, exactly.
+__device__ __forceinline__ float low(float m) { return __builtin_fmaf(-m, LOG2E, m * LOG2E); }
+
+// The sums s and t of y's that all grow by `by` (to another maximum, mostly far
+// down: what then is nothing in F32 is 0 in both).
+__device__ __forceinline__ void fade(float by, float &s, float &t)
 {
     if (s > 0.0f) {
-        const float y = (m - to) * LOG2E, f = __builtin_amdgcn_exp2f(y);
-        t = f > 0.0f ? f * __builtin_fmaf(y, s, t) : 0.0f;
+        const float f = __builtin_amdgcn_exp2f(by);
+        t = f > 0.0f ? f * __builtin_fmaf(by, s, t) : 0.0f;
         s *= f;
     }
 }
+__device__ __forceinline__ void fade_to(float to, float m, float &s, float &t) { fade((m - to) * LOG2E, s, t); }
 
 __device__ __forceinline__ float sum_over_wave(float v)
 {
@@ -432,6 +444,7 @@ __global__ __launch_bounds__(WG, RESIDENT) void k_logprobs(LogprobArgs a, uint32
     if (parts == 1 && wave == 0)
         given = target_of<F32>(a, row);
     float m = -INFINITY, s = 0.0f, t = 0.0f, most_of[NV];
+    bool quick = false;                    // the sums are those of y' (in all lanes)
 #pragma unroll
     for (int v = 0; v < NV; ++v)
         most_of[v] = -INFINITY;
@@ -451,12 +464,11 @@ __global__ __launch_bounds__(WG, RESIDENT) void k_logprobs(LogprobArgs a, uint32
         if (pos + p.stride < p.end)
             load(pos + p.stride);
         const float to = __builtin_fmaxf(m, top);
-        fade_to(to, m, s, t);
-        m = to;
-        // x log2(e) - m log2(e) in one step where m allows it; -200 stands for all
-        // that is nothing in F32, so that -inf adds 0 and not NaN to t
-        if (__all(__builtin_fabsf(m) < 0x1p125f)) {
-            const float by = -m * LOG2E;
+        // -200 stands for all that is nothing in F32, so that -inf adds 0 and not NaN to t
+        if (__all(__builtin_fabsf(to) < 0x1p24f)) {
+            const float by = -to * LOG2E;
+            fade(__builtin_fmaf(m - to, LOG2E, (quick ? low(m) : 0.0f) - low(to)), s, t);
+            quick = true;
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -469,7 +481,9 @@ __global__ __launch_bounds__(WG, RESIDENT) void k_logprobs(LogprobArgs a, uint32
                         t = __builtin_fmaf(e, y, t);
                 }
         } else {
-            const float by = m == -INFINITY ? 0.0f : m;
+            fade(__builtin_fmaf(m - to, LOG2E, quick ? low(m) : 0.0f), s, t);
+            quick = false;
+            const float by = to == -INFINITY ? 0.0f : to;
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -480,7 +494,10 @@ __global__ __launch_bounds__(WG, RESIDENT) void k_logprobs(LogprobArgs a, uint32
                     t = __builtin_fmaf(e, y, t);
                 }
         }
+        m = to;
     }
+    if (quick)
+        fade(low(m), s, t);
 
     const float most = wave_max(m);
     if (a.top != 0)
