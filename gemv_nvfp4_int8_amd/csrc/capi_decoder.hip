@@ -77,7 +77,7 @@ int rope_inv_freq(float *inv_freq, uint32_t rot, double base, int scaling, doubl
     double from = 0.0, to = 1.0;
     if (scaling == QP_ROPE_RAMP) {
         from = std::fmax(std::floor(pair_of(high)), 0.0);
-        to = std::fmin(std::ceil(pair_of(low)), rot / 2 - 1.0);
+        to = std::fmin(std::ceil(pair_of(low)), rot - 1.0);      // (may lie behind the last pair)
         to = std::fmax(to, from + 1e-3);          // both in one pair: a step behind it
     }
     for (uint32_t i = 0; i < rot / 2; ++i) {

@@ -44,9 +44,10 @@ enum qp_rope_layout { QP_ROPE_HALF = 0, QP_ROPE_INTERLEAVED = 1 };
  *   QP_ROPE_WAVELENGTH  divided by factor where r < low, kept where r > high,
  *                       and between them the mix of both, linear in r;
  *   QP_ROPE_RAMP        kept up to the pair that makes `high` turns (its index
- *                       rounded down), divided by factor from the pair that
- *                       makes `low` on (rounded up), and between them the mix
- *                       of both, linear in the pair's index. */
+ *                       rounded down, at least 0), divided by factor from the
+ *                       pair that makes `low` on (rounded up, at most rot - 1:
+ *                       it may lie behind the last pair, rot/2 - 1), and between
+ *                       them the mix of both, linear in the pair's index. */
 enum qp_rope_scaling {
     QP_ROPE_PLAIN = 0,
     QP_ROPE_LINEAR = 1,
