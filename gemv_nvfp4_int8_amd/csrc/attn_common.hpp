@@ -76,6 +76,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t window_at(const void *base, ui
     return __builtin_amdgcn_make_buffer_rsrc((void *)uniform((uint64_t)base + offset), (short)0, (int)uniform(bytes), 0x00020000);
 }
 
+// Bytes behind the end of any such window: a lane that has no element of K there
+// reads zeros (an element of its own, even times a zero of Q, would be NaN if infinite).
+constexpr uint32_t BEYOND = 1u << 30;
+
 // A sequence as the host's arrays give it; n = 0 where its numbers do not fit.
 struct Seq {
     int token, n, len;       // first row, rows, positions

@@ -63,8 +63,8 @@ __device__ __forceinline__ void load_dwords(__amdgpu_buffer_rsrc_t p, uint32_t a
     }
 }
 
-// DP: d rounded up to 64, 128 or 256 (what lies past d is read from the head's
-// start, meets zeros of Q, and is not stored); NQ: 16s of rows of a wave; blocks (1, 2
+// DP: d rounded up to 64, 128 or 256 (what lies past d is zeros of Q and K; of V it is
+// read from the head's start and not stored); NQ: 16s of rows of a wave; blocks (1, 2
 // or 4): of so many rows a workgroup has, whose waves then go through the same keys
 // at the same time, so that a block finds them in the L1 where another has loaded
 // them.
@@ -229,7 +229,7 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
 #pragma unroll
         for (int ks = 0; ks < KL; ++ks) {
             const uint32_t e = FP8 ? 64 * ks + 16 * quad : 32 * ks + 8 * quad;
-            k_off[ks] = (col * d + (e < d ? e : 0)) * ROWB;
+            k_off[ks] = e < d ? (col * d + e) * ROWB : BEYOND;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)

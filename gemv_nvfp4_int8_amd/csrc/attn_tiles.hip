@@ -265,16 +265,15 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tiles(AttnArgs a, Parts par
         const uint32_t page_elems = (kv * d) << pl, head_elems = (head * d) << pl;   // of one page: below 2^31
         const uint32_t mask = (1u << pl) - 1;
         // the lane's bytes of those 16 rows: piece c of LDS row r holds piece
-        // c ^ swizzle(r) of the head's row; what lies past d is read from its start and
-        // meets zeros of Q, or is not stored.  Row r % 16 is the same for every second
-        // piece of a thread at least.
+        // c ^ swizzle(r) of the head's row; what lies past d is zeros.  Row r % 16 is the
+        // same for every second piece of a thread at least.
         constexpr uint32_t EB = FP8 ? 1 : 2;               // bytes of an element
         uint32_t lane_at[2];
 #pragma unroll
         for (uint32_t i = 0; i < 2; ++i) {
             const uint32_t it = tid + WG * i, r = it / CPR;
             const uint32_t e = FP8 ? it % CPR * 16 : (it % CPR ^ swizzle<DP>(r)) * 8;
-            lane_at[i] = (r % 16 * d + (e < d ? e : 0)) * EB;
+            lane_at[i] = e < d ? (r % 16 * d + e) * EB : BEYOND;
         }
         u32x4 kr[FP8 ? ITEMS : 1], vr[FP8 ? ITEMS : 1];
         float ksr = 0.0f, vsr = 0.0f;

@@ -110,7 +110,8 @@ int qk_norm_rope_cache(const uint16_t *qkv, const uint16_t *q_norm, const uint16
  *   max(0, p-w+1)..p:
  *     out = bf16( sum_j v_j e^(scale q.k_j - m) / sum_j e^(scale q.k_j - m) ).
  * A row with nothing to attend to (p < 0, where kv_len is less than the
- * sequence's rows; or holes only) gives zeros.  Rows that belong to no sequence
+ * sequence's rows; or holes only) gives zeros.  A score of -inf has probability 0
+ * (a row of nothing else gives zeros as well), one of +inf or NaN makes the row NaN.  Rows that belong to no sequence
  * are left as they were.  max_q is the most rows of a sequence (a bound; it and
  * the sizes choose the kernel).
  * Scores, maxima, sums and outputs are F32; the probabilities that the matrix
