@@ -117,6 +117,11 @@ __device__ __forceinline__ uint32_t odd_tops(uint32_t w) { return ((w & 0x7F807F
 // The same as masks of 0xFFFF.
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return (odd_tops(w) >> 15) * 0xFFFFu; }
 
+// Scores (of base 2) from which on s * scale - m in one step, whose product is not
+// rounded as m is, could be past 1 at the maximum itself, and past F32's exponents
+// where they are 2^31: the row's scores are scaled first, and rounded.
+__device__ __forceinline__ bool far(float m) { return __builtin_fabsf(m) >= 0x1p24f; }
+
 // A scale of V, finite: 0 times it is 0 in the rows that do not see its key.
 __device__ __forceinline__ float finite_scale(float s) { return __builtin_amdgcn_fmed3f(s, 0.0f, 3.4e38f); }
 

@@ -454,11 +454,19 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
                     for (int j = 0; j < EPL; ++j)
                         acc[nq][j] *= fade;
                 }
+                float row_scale = unit_scale;
+                if (!FP8 && __any(far(base[nq]))) {
+                    if (far(base[nq])) {
+                        s[nq][0] *= unit_scale;
+                        s[nq][1] *= unit_scale;
+                        row_scale = 1.0f;
+                    }
+                }
                 float part = 0.0f;
                 u32x4 w4;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nq][i / 4][i % 4], unit_scale, -base[nq]));
+                    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nq][i / 4][i % 4], row_scale, -base[nq]));
                     part += p[i];
                     if (FP8)
                         p[i] *= finite_scale(vsc[i / 4][i % 4]);

@@ -420,6 +420,19 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tiles(AttnArgs a, Parts par
                 for (int db = 0; db < DB; ++db)
                     acc[db] *= fade;
             }
+            float row_scale = unit_scale;
+            if (!FP8 && __any(far(base))) {
+                if (far(base))
+                    row_scale = 1.0f;
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float x = far(base) ? s[kb][i] * scale : s[kb][i];
+                        asm volatile("" : "+v"(x));
+                        s[kb][i] = x;
+                    }
+            }
             // ---- V: 16 keys' probabilities, then their products with every 32 of d; under
             // these the next 16 keys' probabilities and V's fragments
             // (this wave before the SIMD's other, whose scores and masks then fill the gaps: 298 -> 289 us
@@ -427,7 +440,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tiles(AttnArgs a, Parts par
             __builtin_amdgcn_s_setprio(1);
             float part[4] = {0, 0, 0, 0};
             auto probability = [&](int blk, int i) {
-                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[blk / 2][8 * (blk % 2) + i], unit_scale, -base));
+                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[blk / 2][8 * (blk % 2) + i], row_scale, -base));
                 part[i % 4] += p;
                 return FP8 ? p * scales[buf][1][16 * blk + 8 * (i / 4) + 4 * half + i % 4] : p;
             };

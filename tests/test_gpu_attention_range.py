@@ -1,11 +1,12 @@
-"""paged_attention with infinities in K."""
+"""paged_attention with scores of any finite size and infinities in K."""
 import math
 
 import pytest
 import torch
 
-from tests.decoder_ref import DEV
-from tests.test_gpu_attention import Batch
+from tests import decoder_ref as ref
+from tests.decoder_ref import DEV, gen
+from tests.test_gpu_attention import FORMS, Batch
 
 pytestmark = pytest.mark.gpu
 
@@ -13,6 +14,34 @@ pytestmark = pytest.mark.gpu
 def slots_of(b, i):
     at = torch.arange(b.seqs[i][1], device=DEV)
     return b.table[i].long()[at // b.cache.page] * b.cache.page + at % b.cache.page
+
+
+@FORMS
+@pytest.mark.parametrize("d", [64, 128, 192])
+@pytest.mark.parametrize("n,length", [(1, 700), (5, 300), (150, 400), (1, 5000)])
+def test_scores_of_any_size(n, length, d, fp8):
+    """One entry a head, so that a score is one product: size * (1 + i / 128) of a
+    random i.  From 2^20 on scores of different i are more than 2^12 apart and the
+    softmax is even over the visible keys of the largest.  Equal scores have equal
+    probabilities, rounded to BF16 over the line alone: 2^-8 of the mean |v| and
+    the output's own rounding."""
+    b = Batch([(n, length)], 8, 2, d, fp8, seed=n, scale=0.75)
+    i = torch.randint(0, 128, (length,), generator=gen(d), device=DEV)
+    v = b.v[0]
+    pos = length - n + torch.arange(n, device=DEV)[:, None]
+    seen = torch.arange(length, device=DEV)[None] <= pos
+    for sign in (1.0, -1.0):
+        best = torch.where(seen, sign * i, -math.inf).amax(dim=1, keepdim=True)
+        w = (seen & (sign * i == best)).double()
+        w /= w.sum(dim=1, keepdim=True)
+        want, mag = ((w @ x.reshape(length, -1)).view(n, 2, d).repeat_interleave(4, dim=1) for x in (v, v.abs()))
+        for size in (20, 26, 29, 31, 33, 40, 64, 100, 120):
+            k = torch.zeros((length, 2, d), device=DEV)
+            k[..., d // 3] = (sign * 2.0 ** (size // 2) * (1.0 + i / 128.0))[:, None]
+            b.cache.put("k", slots_of(b, 0), k)
+            b.q.zero_()
+            b.q[..., d // 3] = 2.0 ** (size - size // 2)
+            ref.assert_rounded(b.call(), want, 2.0 ** -8 * mag + 1e-30)
 
 
 @pytest.mark.parametrize("d", [16, 48, 80, 96, 112, 128, 144, 192, 240, 256])
