@@ -441,10 +441,11 @@ __global__ __launch_bounds__(WG, DP <= 128 ? 2 : 1) void k_attn_decode(AttnArgs 
                     top = __builtin_fmaxf(__builtin_fmaxf(top, s[nq][0][i]), s[nq][1][i]);
                 top *= unit_scale;
                 if (__any(top > m[nq] + 8.0f)) {
-                    // the row's four lanes agree on a new maximum; what was summed under the old one fades
+                    // a row's four lanes agree on a new maximum; what was summed under the old one fades.
+                    // The other rows keep theirs, so that no row depends on keys that it does not see
                     top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
                     top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-                    top = __builtin_fmaxf(top, m[nq]);
+                    top = top > m[nq] + 8.0f ? top : m[nq];
                     const float to = top == -INFINITY ? 0.0f : top;
                     const float fade = __builtin_amdgcn_exp2f(m[nq] - to);
                     m[nq] = top;

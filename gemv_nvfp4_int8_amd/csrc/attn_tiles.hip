@@ -409,8 +409,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tiles(AttnArgs a, Parts par
                     top = __builtin_fmaxf(__builtin_fmaxf(top, s[kb][i]), s[kb][i + 1]);
             top *= unit_scale;
             if (__any(top > m + 8.0f)) {
+                // (rows whose own has not grown keep theirs: none depends on keys that it does not see)
                 top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-                top = __builtin_fmaxf(top, m);
+                top = top > m + 8.0f ? top : m;
                 const float to = top == -INFINITY ? 0.0f : top;
                 const float fade = __builtin_amdgcn_exp2f(m - to);
                 m = top;

@@ -1,4 +1,5 @@
-"""paged_attention with scores of any finite size and infinities in K."""
+"""paged_attention with scores of any finite size, infinities in K, and the bits
+of rows beside keys that they do not see."""
 import math
 
 import pytest
@@ -61,3 +62,33 @@ def test_scores_of_minus_infinity(n, d):
             c.hole[s] |= hidden
         c.check()
     b.check()
+
+
+@FORMS
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [2, 4, 16, 60, 300])
+def test_bits_do_not_depend_on_unseen_keys(n, d, fp8):
+    """A key that only the last token's rows see, of any score there: the bits of
+    the rows before stay the same; and one that the window hides from all but the
+    first rows.  Scores rise along the keys, some units of base 2 a tile, so that
+    every tile brings every row a new maximum."""
+    for window in (0, 64):
+        b = Batch([(n, n + 537)], 8, 2, d, fp8, window=window, seed=n)
+        slots = slots_of(b, 0)
+        b.q.copy_(b.q.abs())
+        rise = 0.05 * d ** -0.5 * torch.arange(n + 537, device=DEV)[:, None, None]
+        b.cache.put("k", slots, rise + 0.2 * torch.randn((n + 537, 2, d), generator=gen(n), device=DEV))
+        want = b.call().clone()
+        last, old = n + 536, 537 - 63
+        for at, rows, seen_by in ((last, slice(0, n - 1), n - 1), (old, slice(1, n), 0)):
+            if at == old and not window:
+                continue
+            for size in (1.0, 3.0, 30.0, 1000.0):
+                kept = [x.clone() for x in b.cache.tensors()]
+                q = b.q[seen_by].float().view(2, 4, d).mean(dim=1)
+                b.cache.put("k", slots[at:at + 1], size * q[None])
+                out = b.call()
+                assert not torch.equal(out[seen_by], want[seen_by])
+                assert torch.equal(out[rows], want[rows]), (window, at, size)
+                for x, was in zip(b.cache.tensors(), kept):
+                    x.copy_(was)
