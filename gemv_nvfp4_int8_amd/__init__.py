@@ -210,11 +210,21 @@ def _one_device(*tensors):
     return devices.pop()
 
 
-def _on_device(device, *tensors):
-    """Every tensor given is on `device`, and that is the current device."""
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"tensors on devices {device} and {t.get_device()}")
+def _need_on(device, t, name, dtypes, shape=None):
+    """_need of a tensor on `device` (no shape: the caller has taken it from the tensor)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on device {t.get_device()}, not {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+
+
+def _current(device):
     if torch._C._cuda_getDevice() != device:
         raise ValueError(f"tensors on device {device}, which is not the current one")
 
@@ -588,20 +598,33 @@ def rope_inv_freq(rot, base, scaling=QP_ROPE_PLAIN, factor=1.0, low=0.0, high=0.
 class KVCache:
     """A paged cache in the caller's tensors: k and v [pages, kv_heads,
     page_size, d], BF16, or E4M3 with F32 scales [pages, kv_heads, page_size].
-    Checked once, here; the tensors stay the caller's and are kept referenced."""
+    The tensors stay the caller's and are kept referenced; each call takes the
+    memory that they then have, and refuses other shapes than those given here."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         self.pages, self.kv_heads, self.page_size, self.d = k.shape
         self.fmt = QP_KV_BF16 if k.dtype in BF16 else QP_KV_FP8_ROW
-        for name, t, scale in (("k", k, k_scale), ("v", v, v_scale)):
-            _need(t, name, BF16 if self.fmt == QP_KV_BF16 else U8, k.shape)
-            if self.fmt == QP_KV_FP8_ROW:
-                _need(scale, name + "_scale", F32, k.shape[:3])
-            elif scale is not None:
-                raise ValueError(f"{name}_scale: a BF16 cache has none")
+        dtypes = BF16 if self.fmt == QP_KV_BF16 else U8
+        self._parts = [("k", k, dtypes, k.shape), ("v", v, dtypes, k.shape)]
+        if self.fmt == QP_KV_FP8_ROW:
+            self._parts += [("k_scale", k_scale, F32, k.shape[:3]), ("v_scale", v_scale, F32, k.shape[:3])]
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a BF16 cache has no scales")
+        for name, t, kind, shape in self._parts:
+            _need(t, name, kind, shape)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.device = _one_device(k, v, k_scale, v_scale)
-        self._args = (self.fmt, _ptr(k), _ptr(v), _ptr_or_null(k_scale), _ptr_or_null(v_scale))
+        self._known = None
+
+    def _args(self):
+        now = (self.fmt, *[t.data_ptr() for _, t, _, _ in self._parts], None, None)[:5]
+        known = now == self._known
+        for name, t, kind, shape in self._parts:
+            # in other memory all is checked, in the same what may have changed in place
+            if not known or t.shape != shape or not t.is_contiguous():
+                _need_on(self.device, t, name, kind, shape)
+        self._known = now
+        return now
 
 
 def qk_norm_rope_cache(qkv, q_norm, k_norm, eps, positions, inv_freq, rope_scale, layout, slots, cache,
@@ -615,22 +638,23 @@ def qk_norm_rope_cache(qkv, q_norm, k_norm, eps, positions, inv_freq, rope_scale
     kv = cache.kv_heads
     if d != cache.d:
         raise ValueError(f"q_out: head size {d}, the cache's is {cache.d}")
-    _need(qkv, "qkv", BF16, (t, (q_heads + 2 * kv) * d))
-    _need(q_out, "q_out", BF16, (t, q_heads, d))
-    _need(positions, "positions", I32, (t,))
-    _need(slots, "slots", I32, (t,))
+    device = cache.device
+    _need_on(device, qkv, "qkv", BF16, (t, (q_heads + 2 * kv) * d))
+    _need_on(device, q_out, "q_out", BF16)
+    _need_on(device, positions, "positions", I32, (t,))
+    _need_on(device, slots, "slots", I32, (t,))
     half = 0
     if inv_freq is not None:
         half = inv_freq.numel()
-        _need(inv_freq, "inv_freq", F32, (half,))
+        _need_on(device, inv_freq, "inv_freq", F32, (half,))
     if q_norm is not None:
-        _need(q_norm, "q_norm", BF16, (d,))
+        _need_on(device, q_norm, "q_norm", BF16, (d,))
     if k_norm is not None:
-        _need(k_norm, "k_norm", BF16, (d,))
-    _on_device(cache.device, qkv, q_out, positions, slots, inv_freq, q_norm, k_norm)
+        _need_on(device, k_norm, "k_norm", BF16, (d,))
+    _current(device)
     _check("qk_norm_rope_cache", lib().qk_norm_rope_cache(
         _ptr(qkv), _ptr_or_null(q_norm), _ptr_or_null(k_norm), float(eps), _ptr(positions),
-        _ptr_or_null(inv_freq), float(rope_scale), int(layout), 2 * half, _ptr(slots), *cache._args,
+        _ptr_or_null(inv_freq), float(rope_scale), int(layout), 2 * half, _ptr(slots), *cache._args(),
         _ptr(q_out), t, q_heads, kv, d, cache.pages, cache.page_size, _stream(stream)))
 
 
@@ -650,16 +674,18 @@ def paged_attention(q, cache, page_table, q_start, kv_len, max_q, scale, window,
     seqs, width = page_table.shape
     if d != cache.d:
         raise ValueError(f"q: head size {d}, the cache's is {cache.d}")
-    _need(q, "q", BF16, (t, q_heads, d))
-    _need(out, "out", BF16, (t, q_heads, d))
-    _need(page_table, "page_table", I32, (seqs, width))
-    _need(q_start, "q_start", I32, (seqs + 1,))
-    _need(kv_len, "kv_len", I32, (seqs,))
-    _need(workspace, "workspace", (torch.uint8,), (workspace.numel(),))
-    _on_device(cache.device, q, out, page_table, q_start, kv_len, workspace)
+    device = cache.device
+    _need_on(device, q, "q", BF16)
+    _need_on(device, out, "out", BF16, (t, q_heads, d))
+    _need_on(device, page_table, "page_table", I32)
+    _need_on(device, q_start, "q_start", I32, (seqs + 1,))
+    _need_on(device, kv_len, "kv_len", I32, (seqs,))
+    room = workspace.numel()
+    _need_on(device, workspace, "workspace", (torch.uint8,), (room,))
+    _current(device)
     _check("paged_attention", lib().paged_attention(
-        _ptr(q), *cache._args, _ptr(page_table), _ptr(q_start), _ptr(kv_len), float(scale), int(window),
-        _ptr(workspace), workspace.numel(), _ptr(out), t, seqs, int(max_q), q_heads, cache.kv_heads, d,
+        _ptr(q), *cache._args(), _ptr(page_table), _ptr(q_start), _ptr(kv_len), float(scale), int(window),
+        _ptr(workspace), room, _ptr(out), t, seqs, int(max_q), q_heads, cache.kv_heads, d,
         cache.pages, cache.page_size, width, _stream(stream)))
 
 
@@ -676,19 +702,20 @@ def token_logprobs(logits, targets, logprob, entropy, top_ids, top_logprobs, wor
     rows, vocab = logits.shape
     f32 = isinstance(logits, torch.Tensor) and logits.dtype == torch.float32
     _need(logits, "logits", F32 if f32 else BF16, (rows, vocab))
+    device = logits.get_device()
     top = 0
     if targets is not None:
-        _need(targets, "targets", I32, (rows,))
+        _need_on(device, targets, "targets", I32, (rows,))
     if logprob is not None:
-        _need(logprob, "logprob", F32, (rows,))
+        _need_on(device, logprob, "logprob", F32, (rows,))
     if entropy is not None:
-        _need(entropy, "entropy", F32, (rows,))
+        _need_on(device, entropy, "entropy", F32, (rows,))
     if top_ids is not None or top_logprobs is not None:
-        _need(top_ids, "top_ids", I32, (rows, top_ids.shape[-1] if isinstance(top_ids, torch.Tensor) else 0))
+        _need_on(device, top_ids, "top_ids", I32, (rows, top_ids.shape[-1] if isinstance(top_ids, torch.Tensor) else 0))
         top = top_ids.shape[1]
-        _need(top_logprobs, "top_logprobs", F32, (rows, top))
-    _need(workspace, "workspace", (torch.uint8,), (workspace.numel(),))
-    _on_device(_one_device(logits), targets, logprob, entropy, top_ids, top_logprobs, workspace)
+        _need_on(device, top_logprobs, "top_logprobs", F32, (rows, top))
+    _need_on(device, workspace, "workspace", (torch.uint8,), (workspace.numel(),))
+    _current(device)
     _check("token_logprobs", lib().token_logprobs(
         _ptr(logits), QP_LOGITS_F32 if f32 else QP_LOGITS_BF16, _ptr_or_null(targets),
         _ptr_or_null(logprob), _ptr_or_null(entropy), _ptr_or_null(top_ids) if top else None,
