@@ -224,6 +224,12 @@ def _need_on(device, t, name, dtypes, shape=None):
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
 
 
+def _outside_u32(name):
+    """Raised where whole numbers, or-ed, pass 32 bits: the library would take them
+    modulo 2^32."""
+    return ValueError(f"{name}: a whole number outside 0..2^32-1")
+
+
 def _current(device):
     if torch._C._cuda_getDevice() != device:
         raise ValueError(f"tensors on device {device}, which is not the current one")
@@ -588,7 +594,9 @@ def moe_fp8_blockscale(x, router_logits, w13, s13, w2, s2, topk, renormalize, wo
 def rope_inv_freq(rot, base, scaling=QP_ROPE_PLAIN, factor=1.0, low=0.0, high=0.0, original=0):
     """The rotary frequencies [rot/2] (F32, a host tensor) of base^(-2i/rot),
     scaled (QP_ROPE_*) for contexts `factor` times the model's `original` one."""
-    out = torch.empty(max(int(rot) // 2, 0), dtype=torch.float32)
+    if (int(rot) | int(scaling) | int(original)) >> 32:
+        raise _outside_u32("rope_inv_freq")
+    out = torch.empty(int(rot) // 2, dtype=torch.float32)
     _check("rope_inv_freq", lib().rope_inv_freq(
         _ptr(out), int(rot), float(base), int(scaling), float(factor), float(low), float(high),
         int(original)))
@@ -603,6 +611,8 @@ class KVCache:
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         self.pages, self.kv_heads, self.page_size, self.d = k.shape
+        if (self.pages | self.kv_heads | self.page_size | self.d) >> 32:
+            raise _outside_u32("KVCache")
         self.fmt = QP_KV_BF16 if k.dtype in BF16 else QP_KV_FP8_ROW
         dtypes = BF16 if self.fmt == QP_KV_BF16 else U8
         self._parts = [("k", k, dtypes, k.shape), ("v", v, dtypes, k.shape)]
@@ -638,14 +648,15 @@ def qk_norm_rope_cache(qkv, q_norm, k_norm, eps, positions, inv_freq, rope_scale
     kv = cache.kv_heads
     if d != cache.d:
         raise ValueError(f"q_out: head size {d}, the cache's is {cache.d}")
+    half = 0 if inv_freq is None else inv_freq.numel()
+    if (t | q_heads | 2 * half | int(layout)) >> 32:
+        raise _outside_u32("qk_norm_rope_cache")
     device = cache.device
     _need_on(device, qkv, "qkv", BF16, (t, (q_heads + 2 * kv) * d))
     _need_on(device, q_out, "q_out", BF16)
     _need_on(device, positions, "positions", I32, (t,))
     _need_on(device, slots, "slots", I32, (t,))
-    half = 0
     if inv_freq is not None:
-        half = inv_freq.numel()
         _need_on(device, inv_freq, "inv_freq", F32, (half,))
     if q_norm is not None:
         _need_on(device, q_norm, "q_norm", BF16, (d,))
@@ -660,7 +671,9 @@ def qk_norm_rope_cache(qkv, q_norm, k_norm, eps, positions, inv_freq, rope_scale
 
 def paged_attention_workspace(t, seqs, max_q, q_heads, kv_heads, d) -> int:
     """Bytes of scratch paged_attention needs for t rows of seqs sequences with
-    at most max_q rows each."""
+    at most max_q rows each; 0 for a shape that it refuses."""
+    if (t | seqs | max_q | q_heads | kv_heads | d) >> 32:
+        return 0
     return int(lib().paged_attention_workspace(t, seqs, max_q, q_heads, kv_heads, d))
 
 
@@ -674,6 +687,8 @@ def paged_attention(q, cache, page_table, q_start, kv_len, max_q, scale, window,
     seqs, width = page_table.shape
     if d != cache.d:
         raise ValueError(f"q: head size {d}, the cache's is {cache.d}")
+    if (t | q_heads | seqs | width | int(max_q) | int(window)) >> 32:
+        raise _outside_u32("paged_attention")
     device = cache.device
     _need_on(device, q, "q", BF16)
     _need_on(device, out, "out", BF16, (t, q_heads, d))
@@ -690,7 +705,9 @@ def paged_attention(q, cache, page_table, q_start, kv_len, max_q, scale, window,
 
 
 def token_logprobs_workspace(rows, vocab, top) -> int:
-    """Bytes of scratch token_logprobs needs."""
+    """Bytes of scratch token_logprobs needs; 0 for a shape that it refuses."""
+    if (rows | vocab | top) >> 32:
+        return 0
     return int(lib().token_logprobs_workspace(rows, vocab, top))
 
 
@@ -700,19 +717,21 @@ def token_logprobs(logits, targets, logprob, entropy, top_ids, top_logprobs, wor
     tokens and their log probabilities into top_ids and top_logprobs
     [rows, top].  Targets with logprob, entropy, and the last two may be None."""
     rows, vocab = logits.shape
+    asked = top_ids is not None or top_logprobs is not None
+    top = top_ids.shape[-1] if asked and isinstance(top_ids, torch.Tensor) else 0
+    if (rows | vocab | top) >> 32:
+        raise _outside_u32("token_logprobs")
     f32 = isinstance(logits, torch.Tensor) and logits.dtype == torch.float32
     _need(logits, "logits", F32 if f32 else BF16, (rows, vocab))
     device = logits.get_device()
-    top = 0
     if targets is not None:
         _need_on(device, targets, "targets", I32, (rows,))
     if logprob is not None:
         _need_on(device, logprob, "logprob", F32, (rows,))
     if entropy is not None:
         _need_on(device, entropy, "entropy", F32, (rows,))
-    if top_ids is not None or top_logprobs is not None:
-        _need_on(device, top_ids, "top_ids", I32, (rows, top_ids.shape[-1] if isinstance(top_ids, torch.Tensor) else 0))
-        top = top_ids.shape[1]
+    if asked:
+        _need_on(device, top_ids, "top_ids", I32, (rows, top))
         _need_on(device, top_logprobs, "top_logprobs", F32, (rows, top))
     _need_on(device, workspace, "workspace", (torch.uint8,), (workspace.numel(),))
     _current(device)
