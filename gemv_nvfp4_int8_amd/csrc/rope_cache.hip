@@ -113,7 +113,7 @@ __global__ __launch_bounds__(WG) void k_qk_norm_rope(RopeArgs a, uint32_t tokens
     load(h0);
     for (uint32_t i = threadIdx.x; i < nt * (MAX_HALF + 8); i += WG) {
         const uint32_t n = i / (MAX_HALF + 8), j = i % (MAX_HALF + 8);
-        f32x2 cs = {1.0f, 0.0f};
+        f32x2 cs = {1.0f, -0.0f};          // x * 1 + 0 * -0 is x, -0 too
         if (j < half) {
             // the angle in turns, in 64 bits: the whole turns of far positions drop
             // out before anything is rounded to 32
@@ -181,9 +181,11 @@ __global__ __launch_bounds__(WG) void k_qk_norm_rope(RopeArgs a, uint32_t tokens
                 if constexpr (L == PAIRS) {
 #pragma unroll
                     for (int j = 0; j < 8; j += 2) {
+                        // (a pair that is not turned may hold an infinity, which times 0 is NaN)
                         const float lo = x[j], hi = x[j + 1];
-                        x[j] = __builtin_fmaf(lo, c[j / 2], -(hi * s[j / 2]));
-                        x[j + 1] = __builtin_fmaf(hi, c[j / 2], lo * s[j / 2]);
+                        const bool pair = c0 + j < a.rot;
+                        x[j] = pair ? __builtin_fmaf(lo, c[j / 2], -(hi * s[j / 2])) : lo;
+                        x[j + 1] = pair ? __builtin_fmaf(hi, c[j / 2], lo * s[j / 2]) : hi;
                     }
                 } else if constexpr (L == FULL) {
 #pragma unroll
