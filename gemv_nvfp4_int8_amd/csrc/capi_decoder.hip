@@ -1,6 +1,7 @@
 // capi_decoder.hip -- the extern "C" boundary of the operators declared in
 // include/qproj_decoder.h.  As in capi.hip, every argument is checked on the
 // host before anything is enqueued; nothing allocates or synchronises.
+#include <cfloat>
 #include <cmath>
 
 #include "capi_check.hpp"
@@ -113,8 +114,8 @@ int qk_norm_rope_cache(const uint16_t *qkv, const uint16_t *q_norm, const uint16
     const uint64_t row = ((uint64_t)q_heads + 2 * (uint64_t)kv_heads) * d;
     if (t == 0 || q_heads == 0 || rot % 2 != 0 || rot > d || row > MAX_ELEMS || !fits(t, row))
         return QP_ERR_SHAPE;
-    if ((q_norm && (!(eps > 0.0f) || !std::isfinite(eps))) || !std::isfinite(rope_scale))
-        return QP_ERR_RANGE;
+    if ((q_norm && (!(eps >= FLT_MIN) || !std::isfinite(eps))) || !std::isfinite(rope_scale))
+        return QP_ERR_RANGE;               // (a smaller eps is 0 to the reciprocal root, and a head of zeros NaN)
     return done(qp::launch_qk_norm_rope_cache(
         {qkv, q_norm, k_norm, positions, slots, inv_freq, q_out, eps, rope_scale, t, q_heads, rot,
          layout == QP_ROPE_INTERLEAVED,

@@ -84,8 +84,8 @@ int rope_inv_freq(float *inv_freq, uint32_t rot, double base, int scaling, doubl
  * of the entry hold is unspecified.  A token's outputs depend on it alone.
  * Refusals: zero extents, d, page_size, t * (q_heads + 2 kv_heads) * d >= 2^31,
  * rot odd or larger than d: QP_ERR_SHAPE; unknown format or layout:
- * QP_ERR_FORMAT; eps not positive and finite (with norms) or rope_scale not
- * finite: QP_ERR_RANGE; one of q_norm and k_norm alone: QP_ERR_NULL.
+ * QP_ERR_FORMAT; eps (with norms) not finite or below F32's smallest normal
+ * number, 2^-126, or rope_scale not finite: QP_ERR_RANGE; one of q_norm and k_norm alone: QP_ERR_NULL.
  * q_heads need not be a multiple of kv_heads here.
  * ---------------------------------------------------------------------- */
 int qk_norm_rope_cache(const uint16_t *qkv, const uint16_t *q_norm, const uint16_t *k_norm,

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import gemv_nvfp4_int8_amd as qp
+from tests.test_decoder_abi import rope
 
 
 def ramp(rot, base, factor, low, high, original):
@@ -102,3 +103,12 @@ def test_frequencies_and_workspaces_take_no_number_modulo_2_to_the_32():
     for i in range(3):
         for off in (1 << 32, -(1 << 32)):
             assert qp.token_logprobs_workspace(*[v + off * (j == i) for j, v in enumerate((4, 100, 3))]) == 0
+
+
+def test_eps_below_the_normal_numbers():
+    """The reciprocal root takes a subnormal number for 0, and a head of zeros would be
+    0 times infinity."""
+    for eps in (1.1754942e-38, 1e-39, 1e-45):
+        assert rope(eps=eps) == qp.QP_ERR_RANGE
+    # (no norms: eps is not used, and rot is what is refused)
+    assert rope(eps=0.0, q_norm=0, k_norm=0, rot=63) == qp.QP_ERR_SHAPE
