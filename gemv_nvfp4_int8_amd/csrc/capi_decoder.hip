@@ -145,8 +145,8 @@ int paged_attention(const uint16_t *q, int kv_format, const void *k_cache, const
     if (!attention_shape(t, seqs, q_heads, kv_heads, d) || table_width == 0 || !fits(seqs, table_width) ||
         (uint64_t)table_width * page_size >= 1u << 27 || (uint64_t)seqs * table_width * page_size >= 1ull << 38)
         return QP_ERR_SHAPE;               // (tiles of 32 keys or more are counted in 32 bits, 512 blocks at a time)
-    if (max_q < 1 || max_q > t || !(scale > 0.0f) || !std::isfinite(scale))
-        return QP_ERR_RANGE;
+    if (max_q < 1 || max_q > t || !(scale > 0.0f) || !std::isfinite(scale * 1.4426950408889634f))
+        return QP_ERR_RANGE;               // (scores are kept in base 2)
     if (workspace_bytes < qp::paged_attention_work(t, seqs, max_q, q_heads, kv_heads, d))
         return QP_ERR_SCRATCH;
     return done(qp::launch_paged_attention(

@@ -130,8 +130,8 @@ int qk_norm_rope_cache(const uint16_t *qkv, const uint16_t *q_norm, const uint16
  * Refusals: zero extents, q_heads not a multiple of kv_heads, d, page_size,
  * t * q_heads * d, pages * page_size or seqs * table_width of 2^31 or more,
  * table_width * page_size of 2^27 or more, seqs * table_width * page_size of
- * 2^38 or more: QP_ERR_SHAPE; max_q outside 1..t, scale not
- * positive and finite: QP_ERR_RANGE; unknown format: QP_ERR_FORMAT.
+ * 2^38 or more: QP_ERR_SHAPE; max_q outside 1..t, scale not positive and
+ * finite, also times log2(e): QP_ERR_RANGE; unknown format: QP_ERR_FORMAT.
  * ---------------------------------------------------------------------- */
 uint64_t paged_attention_workspace(uint32_t t, uint32_t seqs, uint32_t max_q, uint32_t q_heads,
                                    uint32_t kv_heads, uint32_t d);

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import gemv_nvfp4_int8_amd as qp
-from tests.test_decoder_abi import rope
+from tests.test_decoder_abi import attn, rope
 
 
 def ramp(rot, base, factor, low, high, original):
@@ -112,3 +112,10 @@ def test_eps_below_the_normal_numbers():
         assert rope(eps=eps) == qp.QP_ERR_RANGE
     # (no norms: eps is not used, and rot is what is refused)
     assert rope(eps=0.0, q_norm=0, k_norm=0, rot=63) == qp.QP_ERR_SHAPE
+
+
+def test_scales_that_base_2_does_not_hold():
+    """Scores are kept in base 2: scale times log2(e) has to be finite."""
+    for scale in (2.36e38, 3e38, 3.4028234e38):
+        assert attn(scale=scale) == qp.QP_ERR_RANGE
+    assert attn(scale=2.35e38, bytes=0) == qp.QP_ERR_SCRATCH
