@@ -115,8 +115,9 @@ int qk_norm_rope_cache(const uint16_t *qkv, const uint16_t *q_norm, const uint16
  * are left as they were.  max_q is the most rows of a sequence (a bound; it and
  * the sizes choose the kernel).
  * Scores, maxima, sums and outputs are F32; the probabilities that the matrix
- * cores multiply with V are rounded to BF16 (their sum is of the unrounded
- * ones).  An E4M3 cache's scales of V count as the nearest number of 0 to
+ * cores multiply with V are rounded to BF16, by up to 2^-8 (where few rows meet
+ * a BF16 cache to two such numbers, by up to 2^-16); their sum is of the
+ * unrounded ones.  An E4M3 cache's scales of V count as the nearest number of 0 to
  * 3.4e38 (NaN as 0).  What the cache holds at a position that a row does not attend to,
  * NaN and infinities included, has no influence on that row.  No atomics: the
  * same call gives the same bits; another batch may change a row's last bits.

@@ -92,3 +92,18 @@ def test_bits_do_not_depend_on_unseen_keys(n, d, fp8):
                 assert torch.equal(out[rows], want[rows]), (window, at, size)
                 for x, was in zip(b.cache.tensors(), kept):
                     x.copy_(was)
+
+
+@pytest.mark.parametrize("d,heads,n,length", [(128, 8, 1, 700), (128, 8, 8, 300), (128, 16, 1, 3000), (64, 8, 16, 500), (64, 12, 3, 900),
+                                              (80, 8, 4, 400), (256, 8, 4, 600), (192, 16, 2, 333)])
+def test_few_rows_over_a_bf16_cache_round_the_output_alone(d, heads, n, length):
+    """Probabilities meet V in two parts, to 2^-16: the 64-bit form's bound less what
+    it has for their rounding to BF16, 2^-8 of sum p |v|."""
+    b = Batch([(n, length), (n, n + 5)], heads, 2, d, seed=d + n)
+    out = b.check()
+    for i, (_, m) in enumerate(b.seqs):
+        rows = slice(b.starts[i], b.starts[i] + n)
+        args = b.q[rows], b.k[i], ref.visible(n, m, 0), b.scale
+        want, tol = ref.attention(args[0], args[1], b.v[i], *args[2:])
+        mag, _ = ref.attention(args[0], args[1], b.v[i].abs(), *args[2:])
+        ref.assert_rounded(out[rows], want, tol - (2.0 ** -8 - 2.0 ** -16) * mag)
