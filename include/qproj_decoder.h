@@ -7,9 +7,10 @@
  * The conventions of qproj.h hold (device pointers to dense row-major memory,
  * 16-byte alignment, caller-owned buffers and scratch, no allocation, no
  * synchronisation, work enqueued on `stream`, host-side checks that enqueue
- * nothing).  What a call writes overlaps nothing else that it is given.  What the host cannot see (slots, page numbers, lengths, tokens)
- * is checked on the GPU: a value that fits no buffer is skipped as stated at
- * the operator and never leads outside one.
+ * nothing).  What a call writes overlaps nothing else that it is given.  What
+ * the host cannot see (slots, page numbers, lengths, tokens) is checked on the
+ * GPU: a value that fits no buffer is skipped as stated at the operator and
+ * never leads outside one.
  */
 #ifndef QPROJ_DECODER_H
 #define QPROJ_DECODER_H
@@ -110,24 +111,30 @@ int qk_norm_rope_cache(const uint16_t *qkv, const uint16_t *q_norm, const uint16
  *   max(0, p-w+1)..p:
  *     out = bf16( sum_j v_j e^(scale q.k_j - m) / sum_j e^(scale q.k_j - m) ).
  * A row with nothing to attend to (p < 0, where kv_len is less than the
- * sequence's rows; or holes only) gives zeros.  A score of -inf has probability 0
- * (a row of nothing else gives zeros as well), one of +inf or NaN makes the row NaN.  Rows that belong to no sequence
+ * sequence's rows; or holes only) gives zeros.  Rows that belong to no sequence
  * are left as they were.  max_q is the most rows of a sequence (a bound; it and
  * the sizes choose the kernel).
  * Scores, maxima, sums and outputs are F32; the probabilities that the matrix
  * cores multiply with V are rounded to BF16, by up to 2^-8 (where few rows meet
  * a BF16 cache to two such numbers, by up to 2^-16); their sum is of the
- * unrounded ones.  An E4M3 cache's scales of V count as the nearest number of 0 to
- * 3.4e38 (NaN as 0).  What the cache holds at a position that a row does not attend to,
- * NaN and infinities included, has no influence on that row.  No atomics: the
- * same call gives the same bits; another batch may change a row's last bits.
+ * unrounded ones.  The sum over the line may be 2^9 times the formula's before
+ * it is divided: V of 2^92 and more may overflow it.  An E4M3 cache's scales of
+ * V count as the nearest number of 0 to 3.4e38 (NaN as 0).
+ * A score of -inf has probability 0 (a row of nothing else gives zeros as well),
+ * one of +inf or NaN makes the row NaN.  NaN or an infinity in V makes that
+ * element of the rows that attend to it NaN or an infinity (which of them is
+ * unspecified).  What the cache holds at a position that a row does not attend
+ * to, NaN and infinities included, has no influence on that row.
+ * No atomics: the same call gives the same bits; another batch may change a
+ * row's last bits.
  * A page number outside 0..pages-1 is a hole: none of its positions is
  * attended to.  A sequence whose numbers do not fit (q_start below 0, falling or
  * past t, more than max_q rows, kv_len below 0 or past table_width *
- * page_size) is left out: its rows are left as they were.
+ * page_size) is left out: its rows are left as they were.  A row that two
+ * sequences have (where q_start falls between them) holds either's result.
  * workspace: caller-owned scratch of paged_attention_workspace(...) bytes (fewer
- * is QP_ERR_SCRATCH; enough for a max_q is enough for a smaller one), contents before and after unspecified, not shared by
- * calls that may overlap.
+ * is QP_ERR_SCRATCH; enough for a max_q is enough for a smaller one), contents
+ * before and after unspecified, not shared by calls that may overlap.
  * Refusals: zero extents, q_heads not a multiple of kv_heads, d, page_size,
  * t * q_heads * d, pages * page_size or seqs * table_width of 2^31 or more,
  * table_width * page_size of 2^27 or more, seqs * table_width * page_size of

@@ -107,3 +107,27 @@ def test_few_rows_over_a_bf16_cache_round_the_output_alone(d, heads, n, length):
         want, tol = ref.attention(args[0], args[1], b.v[i], *args[2:])
         mag, _ = ref.attention(args[0], args[1], b.v[i].abs(), *args[2:])
         ref.assert_rounded(out[rows], want, tol - (2.0 ** -8 - 2.0 ** -16) * mag)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("n,length,d", [(1, 700, 128), (5, 5000, 64), (100, 900, 128), (300, 700, 256), (40, 4000, 80)])
+def test_infinities_in_v(n, length, d, bad):
+    """Early in the cache, where all rows see whole tiles, among the chunk's own
+    positions, and where its window begins: NaN or an infinity for the rows that see
+    the position, in that element; all other numbers keep their bits."""
+    for window in (0, length - n - 70):
+        b = Batch([(n, length)], 8, 2, d, window=window, seed=n)
+        want = b.call().clone()
+        slots = slots_of(b, 0)
+        pos = length - n + torch.arange(n, device=DEV)
+        first = length - n - window + 1 if window else 0
+        for at in (3, 130, first + n // 2, length - n, length - 1):
+            where = slots[at] // b.cache.page, 1, slots[at] % b.cache.page, d // 3
+            kept = b.cache.v[where].clone()
+            b.cache.v[where] = bad
+            out = b.call()
+            hit = torch.zeros_like(out, dtype=torch.bool)
+            hit[(at <= pos) & ((pos - at < window) if window else True), 4:, d // 3] = True
+            assert not torch.isfinite(out[hit].float()).any(), (window, at)
+            assert torch.equal(out[~hit], want[~hit]), (window, at)
+            b.cache.v[where] = kept
