@@ -249,6 +249,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tiles(AttnArgs a, Parts par
             qf[ks] = __builtin_bit_cast(bf16x8, v);
         }
         float m = -INFINITY, base = 0.0f, l = 0.0f;
+        float row_scale = FP8 ? 1.0f : scale;
+        bool some_far = false;             // of the wave's rows
         uint32_t nans[CW / 8];             // bit 4 c + j: the row's d = part_d + 8 c + 4 half + j has met NaN or an infinity
 #pragma unroll
         for (uint32_t i = 0; i < CW / 8; ++i)
@@ -416,15 +418,14 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tiles(AttnArgs a, Parts par
                 const float fade = __builtin_amdgcn_exp2f(m - to);
                 m = top;
                 base = to;
+                row_scale = !FP8 && far(base) ? 1.0f : unit_scale;
+                some_far = __any(far(base));
                 l *= fade;
 #pragma unroll
                 for (int db = 0; db < DB; ++db)
                     acc[db] *= fade;
             }
-            float row_scale = unit_scale;
-            if (!FP8 && __any(far(base))) {
-                if (far(base))
-                    row_scale = 1.0f;
+            if (!FP8 && some_far) {
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
