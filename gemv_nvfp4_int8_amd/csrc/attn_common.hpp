@@ -146,18 +146,20 @@ __device__ __forceinline__ uint32_t share_of(uint64_t x, uint64_t n, uint64_t sh
 hipError_t launch_attn_join(const AttnArgs &a, const Parts &p, uint32_t shares, uint32_t rows, uint32_t live,
                             hipStream_t st);
 
-// Rows of a sequence (times heads of a kv head) up to which attn_decode.hip is the
-// faster one.  Measured, 16 sequences over 9001 positions, 4 kv heads, few rows'
-// kernel and tiles', us:
-//   rows            16           32           64          128
-//   BF16 d =  64    34 and  39   35 and  40   40 and  42   65 and  46
-//   BF16 d = 128    56 and  64   61 and  65   76 and  67  121 and  74
-//   BF16 d = 192    88 and  97  110 and  97  183 and 107
-//   BF16 d = 256   117 and 115  125 and 117  198 and 126
-//   E4M3 d =  64    25 and  41   28 and  41   40 and  46   65 and  50
-//   E4M3 d = 128    37 and  92   40 and  93   55 and  94   90 and  98
-//   E4M3 d = 256    57 and 111   74 and 113  116 and 116
-// (the same order over 1 sequence of 32000 and 64 of 1000).
+// Rows of a sequence (times heads of a kv head) up to which attn_decode.hip serves
+// it.  Measured with 4 kv heads, few rows' kernel / tiles', us, over 16 sequences of
+// 4500 to 9001 positions, one of 32000, 64 of 500 to 1000:
+//   rows                 16                    32                    64                   128
+//   BF16 d =  64   31/33 16/18 21/24     34/33 18/20 24/25     41/37 22/22 30/28     65/45 30/25 45/33
+//   BF16 d = 128   47/49 23/24 29/36     56/50 29/25 39/38     63/52 32/26 46/38    101/60 44/29 72/45
+//   BF16 d = 192   77/85 29/31 40/41     95/87 33/32 54/43    139/94 49/35 85/49
+//   BF16 d = 256  102/105 35/35 47/45   116/109 37/35 61/48  163/118 55/38 95/54
+//   E4M3 d =  64   25/35 15/19 18/25     28/35 18/20 23/26     38/41 23/23 29/30     58/48 29/28 41/36
+//   E4M3 d = 128   33/64 20/28 24/43     39/65 24/29 32/45     50/68 29/30 40/45     80/72 39/33 61/50
+//   E4M3 d = 192   42/91 23/38 34/51     55/92 28/39 45/54     91/97 40/41 68/58
+//   E4M3 d = 256   51/92 26/38 36/52     58/94 29/40 46/55     95/100 41/43 70/62
+// The last rows of a range are near the crossing, which moves with the lengths: 16
+// sequences of 9001 each, BF16, d = 128, 32 rows 61/65.
 constexpr uint32_t decode_rows(uint32_t d, bool fp8) { return fp8 || d <= 64 ? 64 : d <= 128 ? 32 : 16; }
 uint64_t decode_work(uint32_t rows, uint32_t d);
 hipError_t launch_attn_decode(const AttnArgs &a, hipStream_t st);

@@ -18,12 +18,14 @@
 // products are issued, V as soon as its own are).  The four waves of a workgroup
 // take every fourth 32 keys and join through LDS at a unit's end.
 //
-// Bound by HBM with up to 16 rows in BF16: a token each of 48 sequences over 1200 to
-// 12000 positions, 8 kv heads of 128, take 240 us, 5.6 TB/s.  In E4M3 the decoding and
-// turning of the codes costs more than their bytes (the kernel alone 44 us for 16
-// sequences of 5 tokens over up to 9001, 4 kv heads, 120 MB: 2.8 TB/s; with a third
-// tile on its way 62 us).  Over one short sequence (700 positions: 10.4 us with the
-// join) it is a chain of trips to memory: lengths, pages, keys, parts.
+// Bound by HBM in BF16 (a token each of 48 sequences over 1200 to 12000 positions, 8 kv
+// heads of 128, 240 us, 5.6 TB/s; 16 sequences of 9001, 4 kv heads, 32 rows: the kernel
+// alone 57 us, 5.3 TB/s) and in E4M3 with up to 16 rows (the same sequences: 30 us, 5.2
+// TB/s).  With more the decoding and turning of the codes, which every block of 32 rows
+// does again, costs more than their bytes (50 rows: 49 us alone, 3.2 TB/s; with a third
+// tile on its way a quarter slower).  The join is 4 to 6 us more.  Over one short
+// sequence (700 positions: 10.5 us with the join) it is a chain of trips to memory:
+// lengths, pages, keys, parts.
 #include "attn_common.hpp"
 #include "qp_launch.hpp"
 

@@ -20,15 +20,21 @@
 // Where d > 128 a row of O would take twice the registers that leave room for two
 // waves a SIMD: two waves have the same 32 rows, each half of O's d, and both compute
 // S, which is half as many matrix operations again (4096 rows over themselves, 32
-// heads of 256: 600 us, in E4M3 670; one wave a SIMD with all of O: 862 and 1508).
+// heads of 256: 560 us, in E4M3 635; one wave a SIMD with all of O took 40% more, in
+// E4M3 twice as long).
 //
-// What bounds it: at two waves a SIMD, the softmax's vector work beside the matrix
-// operations (an exponential takes 8 cycles of a wave, a product of 32x32x16 32), and
-// the LDS reads, which 32 rows a wave just balance with the matrix operations; with
-// heads of 128 and long keys also the part's power (1.84 GHz under 2000 rows over
-// 32000).  Measured, 32 heads of 128 over 8: 8192 rows over themselves 660 us, 830
-// TFLOP/s; 2000 rows over 32000 0.95 ms, 1.07 PFLOP/s; 64 heads of 64, 7 prompts of up
-// to 2500 in a window of 1024: 276 us, 500 TFLOP/s of what is seen.
+// What bounds it: over long keys, at two waves a SIMD, the softmax's vector work beside
+// the matrix operations (an exponential takes 8 cycles of a wave, a product of 32x32x16
+// 32), the LDS reads, which 32 rows a wave just balance with the matrix operations, and
+// with heads of 128 the part's power (1.84 GHz under 2000 rows over 32000); a tile of
+// 256 rows by 64 keys takes 3600 cycles then.  Where units are short, their beginnings
+// (lengths, then page numbers, then keys, each a trip to memory, and a masked tile at
+// the end) come on top: 8192 rows over themselves are 258 tiles a share, of which the
+// first share of a head begins 23 units and the last two, and take 5000 cycles a tile.
+// Measured, 32 heads of 128 over 8: 8192 rows over themselves 655 us, 840 TFLOP/s (in
+// E4M3 730); 2000 rows over 32000 0.92 to 0.98 ms, 1.04 to 1.10 PFLOP/s; 64
+// heads of 64, 7 prompts of 1250 to 2500 in a window of 1024: 280 to 298 us, 470 to 490
+// TFLOP/s of what is seen.
 #include "attn_common.hpp"
 #include "qp_launch.hpp"
 
@@ -37,10 +43,10 @@ namespace attn {
 namespace {
 
 // Keys of a tile: as many as two buffers of them leave room for eight waves a
-// compute unit.  (d = 64 with tiles of 64 and three waves a SIMD: 329 us where this
-// takes 305, 7 prompts of up to 2500 in a window of 1024.  d = 128 with tiles of 128:
-// 2000 rows over 32000 937 for 955, but 32 prompts of 128 45 for 41, 2048 rows over
-// themselves 88 to 93 either way, and E4M3 spills.)
+// compute unit.  (d = 64 with tiles of 64 and three waves a SIMD: 8% slower, 7 prompts
+// of 1250 to 2500 in a window of 1024.  d = 128 with tiles of 128: 2000 rows over 32000
+// 2% faster, but 32 prompts of 128 9% slower, 2048 rows over themselves the same either
+// way, and E4M3 spills.)
 constexpr uint32_t tile_keys(uint32_t d) { return d <= 64 ? 128 : d <= 128 ? 64 : 32; }
 
 typedef __attribute__((ext_vector_type(4))) short s16x4;
@@ -437,8 +443,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tiles(AttnArgs a, Parts par
             }
             // ---- V: 16 keys' probabilities, then their products with every 32 of d; under
             // these the next 16 keys' probabilities and V's fragments
-            // (this wave before the SIMD's other, whose scores and masks then fill the gaps: 298 -> 289 us
-            // at heads of 64 with a window of 1024, 943 -> 929 at 2000 rows over 32000)
+            // (this wave before the SIMD's other, whose scores and masks then fill the gaps: 3% faster at
+            // heads of 64 with a window of 1024, 1.5% at 2000 rows over 32000)
             __builtin_amdgcn_s_setprio(1);
             float part[4] = {0, 0, 0, 0};
             auto probability = [&](int blk, int i) {
@@ -620,8 +626,8 @@ void launch(const AttnArgs &a, const Parts &p, uint32_t shares, hipStream_t st)
 // Waves of a workgroup.  Eight read K and V half as often as four; at d <= 64 two
 // workgroups of four fit side by side, so that one's start and barriers are the
 // other's time to work, which counts where units are short.  Measured there, four
-// waves and eight, 64 heads on 8, us: 32 prompts of 128 40 and 51; 8 of 512 80 and
-// 73, 1 of 4096 280 and 275, 7 of up to 2500 in a window of 1024 318 and 304.
+// waves and eight, 64 heads on 8, us: 32 prompts of 128 42 and 53; 8 of 512 83 and
+// 76, 1 of 4096 275 and 270, 7 of 250 to 2500 in a window of 1024 276 and 265.
 uint32_t waves_of(uint32_t d, uint32_t max_q) { return d <= 64 && max_q <= 256 ? 4 : 8; }
 
 // Rows of a unit (two waves share them for d > 128).

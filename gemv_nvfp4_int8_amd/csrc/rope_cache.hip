@@ -9,10 +9,11 @@
 // the vector instructions bound it then).  Cosines
 // and sines are the same for all heads of a token: one thread a pair computes them
 // into LDS while the heads' loads are on their way; what is not turned has the
-// angle 0 there, so that all lanes do the same.
+// angle 0 there and a partner of 0, so that all lanes do the same (in neighbouring
+// pairs, whose partners are what they are, it is kept by a choice instead).
 //
 // Bound by HBM when large: 8192 tokens of 32 + 2 * 8 heads of 128 take 33 us, 6.1 TB/s
-// read and written; 2047 of 40 + 2 * 4 with an E4M3 cache 9.7 us (5.0 TB/s).  A single
+// read and written; 2047 of 40 + 2 * 4 with an E4M3 cache 9.9 us (4.9 TB/s).  A single
 // token takes 4 us: a launch, one trip to memory, the sums across lanes.
 #include <type_traits>
 
