@@ -114,12 +114,13 @@ int qk_norm_rope_cache(const uint16_t *qkv, const uint16_t *q_norm, const uint16
  * sequence's rows; or holes only) gives zeros.  Rows that belong to no sequence
  * are left as they were.  max_q is the most rows of a sequence (a bound; it and
  * the sizes choose the kernel).
- * Scores, maxima, sums and outputs are F32; the probabilities that the matrix
- * cores multiply with V are rounded to BF16, by up to 2^-8 (where few rows meet
- * a BF16 cache to two such numbers, by up to 2^-16); their sum is of the
- * unrounded ones.  The sum over the line may be 2^9 times the formula's before
- * it is divided: V of 2^92 and more may overflow it.  An E4M3 cache's scales of
- * V count as the nearest number of 0 to 3.4e38 (NaN as 0).
+ * Scores, maxima, sums and outputs are F32; the probabilities (with an E4M3
+ * cache times V's scale) that the matrix cores multiply with V are rounded to
+ * BF16, by up to 2^-8, or, where few rows meet a BF16 cache, to two such numbers,
+ * by up to 2^-16; their sum is of the unrounded ones.  The sum over the line may
+ * be 2^9 times the formula's before it is divided: V of 2^92 and more may
+ * overflow it.  An E4M3 cache's scales of V count as the nearest number of 0 to
+ * 3.4e38 (NaN as 0).
  * A score of -inf has probability 0 (a row of nothing else gives zeros as well),
  * one of +inf or NaN makes the row NaN.  NaN or an infinity in V makes that
  * element of the rows that attend to it NaN or an infinity (which of them is
